@@ -31,6 +31,21 @@ Entry points (same names as the C ABI):
     round_routed(hidden, W1, b1, W2, b2, tau, logits, row_offsets, total_rows, chain_draft,
                  parent, draft_ids, d2t)   route + verify_routed fused
                  -> (delta_al, choice, accept_len, bonus, best_node, row_argmax)
+
+Around the round (the rows described by chain_rows(draft), tree_rows(parent, draft_ids, d2t) or
+routed_rows(row_offsets, total_rows, choice, chain_draft, parent, draft_ids, d2t)):
+    LogitRules(history, slot=, penalties=, bias=, allow=)   penalties for repeated tokens, biases
+                 and grammar masks
+    verify_constrained(logits, rows, rules)               -> (accept_len, bonus, best_node, row_argmax)
+    process_logits(logits, rows, rules)   the processed logits written out -> out
+    history_prompt(history, tokens, offsets), history_update(history, rows, accept_len, best_node,
+                 bonus)   the token history behind the penalties
+    PageCache(k, v, table, held, context, refs), PageCache.empty(...)   a paged key-value cache
+    cache_append(cache, rows, k_rows, v_rows)   the rows' keys and values into their pages
+    attend(q, rows, cache)   attention of the rows over the cache -> out
+    cache_compact(cache, rows, accept_len, best_node)   keeps the accepted path's rows
+    cache_fork(cache, src, dst), cache_reserve(cache, count, seqs=)  -> status
+    cache_free(cache, seqs)
 """
 
 from ._binding import (  # noqa: F401
@@ -89,4 +104,26 @@ from ._binding import (  # noqa: F401
     whiflash_verify_chain,
     whiflash_verify_tree,
     whiflash_verify_routed,
+)
+
+from ._rounds import (  # noqa: F401
+    LogitRules,
+    PageCache,
+    RoundRows,
+    attend,
+    attend_workspace_bytes,
+    cache_append,
+    cache_compact,
+    cache_fork,
+    cache_free,
+    cache_pages_workspace_bytes,
+    cache_reserve,
+    chain_rows,
+    history_prompt,
+    history_update,
+    process_logits,
+    routed_rows,
+    tree_rows,
+    verify_constrained,
+    verify_constrained_workspace_bytes,
 )

@@ -1,0 +1,541 @@
+"""ctypes binding of the calls around a round: decoding rules on the logits, the token
+history, the paged key-value cache and the attention over it (argument marshalling only).
+
+Three handles describe what the calls work on, each a host struct of device pointers built
+once and usable for as long as its tensors are: RoundRows (the rows of a round, laid out as
+the verify calls lay them out), LogitRules and PageCache.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._binding import (_check, _device_tensor, _dtype_code, _i32, _on, _opt_out,
+                       _out, _rows_view, _workspace, lib)
+
+ROWS_CHAIN, ROWS_TREE, ROWS_ROUTED = 0, 1, 2
+
+_p, _i, _l, _sz, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+
+
+class _RowsStruct(ctypes.Structure):
+    _fields_ = [(n, _i) for n in ("kind", "B", "K", "N", "Vd", "total_rows")] + [
+        (n, _p) for n in ("chain_draft", "parent", "draft_ids", "d2t", "row_offsets", "choice")]
+
+
+class _RulesStruct(ctypes.Structure):
+    _fields_ = [("history", _p), ("history_stride", _l), ("slots", _i), ("bias_count", _i),
+                ("slot", _p), ("penalties", _p), ("bias_offsets", _p), ("bias_ids", _p),
+                ("bias_values", _p), ("allow", _p), ("allow_stride", _l)]
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("layer_stride", _l), ("page_stride", _l)] + [
+        (n, _i) for n in ("dtype", "layers", "pages", "heads", "page_size", "head_dim", "seqs",
+                          "max_pages")] + [(n, _p) for n in ("table", "held", "context", "refs")]
+
+
+_R, _U, _C = (ctypes.POINTER(s) for s in (_RowsStruct, _RulesStruct, _CacheStruct))
+
+_SIGNATURES = {
+    "whiflash_process_logits": (_i, [_p, _i, _i, _l, _R, _U, _p, _i, _l, _p]),
+    "whiflash_verify_constrained_workspace_bytes": (_sz, [_R, _i]),
+    "whiflash_verify_constrained": (_i, [_p, _i, _i, _l, _R, _U, _p, _p, _p, _p, _p, _sz, _p]),
+    "whiflash_history_prompt": (_i, [_p, _i, _i, _l, _i, _p, _p, _p, _i, _p]),
+    "whiflash_history_update": (_i, [_p, _i, _i, _l, _R, _p, _p, _p, _p, _p]),
+    "whiflash_cache_append": (_i, [_C, _i, _R, _p, _p, _l, _p, _l, _p]),
+    "whiflash_attend_workspace_bytes": (_sz, [_C, _R, _i, _i]),
+    "whiflash_attend": (_i, [_p, _l, _i, _C, _i, _R, _p, _i, _f, _p, _p, _sz, _p]),
+    "whiflash_cache_compact": (_i, [_C, _R, _p, _p, _p, _p, _p]),
+    "whiflash_cache_pages_workspace_bytes": (_sz, [_C, _i]),
+    "whiflash_cache_fork": (_i, [_C, _i, _p, _p, _p, _p, _sz, _p]),
+    "whiflash_cache_reserve": (_i, [_C, _i, _p, _p, _p, _p, _sz, _p]),
+    "whiflash_cache_free": (_i, [_C, _i, _p, _p]),
+}
+
+_FN = None
+
+
+def functions():
+    """The library's functions of this module, with their signatures set."""
+    global _FN
+    if _FN is None:
+        handle = lib()
+        fns = {}
+        for name, (res, args) in _SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.restype = res
+            fn.argtypes = args
+            fns[name[len("whiflash_"):]] = fn
+        _FN = type("Functions", (), {k: staticmethod(v) for k, v in fns.items()})
+    return _FN
+
+
+class _Run:
+    """Where a call runs: its tensors' device made current, and its stream, so that what the
+    call allocates belongs to the stream that uses it."""
+
+    __slots__ = ("stream", "_was", "_on", "_index")
+
+    def __init__(self, device, stream):
+        self._index = device.index
+        self._on = None
+        self._was = None
+        if stream is not None:
+            self._on = torch.cuda.stream(stream)
+            self.stream = stream.cuda_stream
+
+    def __enter__(self):
+        if self._on is not None:
+            self._on.__enter__()
+        else:
+            if torch.cuda.current_device() != self._index:
+                self._was = torch.cuda.device(self._index)
+                self._was.__enter__()
+            self.stream = torch.cuda.current_stream(self._index).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._on is not None:
+            self._on.__exit__(*exc)
+        elif self._was is not None:
+            self._was.__exit__(*exc)
+
+
+class RoundRows:
+    """The rows of one round (wf_round_rows).  Built by chain_rows, tree_rows and routed_rows;
+    holds its tensors."""
+
+    __slots__ = ("struct", "ref", "total", "B", "kind", "device", "tensors", "tokens")
+
+    def __init__(self, kind, B, K, N, total, device, tokens, **tensors):
+        for name, t in tensors.items():
+            if t is not None and t.device != device:
+                raise ValueError(f"{name} is on {t.device}, the round on {device}")
+        Vd = tensors["d2t"].numel() if tensors.get("d2t") is not None else 0
+        self.kind, self.B, self.total, self.device, self.tokens = kind, B, total, device, tokens
+        self.tensors = tensors
+        self.struct = _RowsStruct(kind, B, K, N, Vd, total,
+                                  **{n: t.data_ptr() for n, t in tensors.items() if t is not None})
+        self.ref = ctypes.byref(self.struct)
+
+
+def chain_rows(draft) -> RoundRows:
+    """B chains of K drafts: draft [B, K] int32.  K = 0 is one new token per sequence."""
+    _i32(draft, "draft")
+    if draft.dim() != 2:
+        raise ValueError("draft must be [B, K]")
+    B, K = draft.shape
+    return RoundRows(ROWS_CHAIN, B, K, 0, B * (K + 1), draft.device, True, chain_draft=draft)
+
+
+def _tree_tensors(parent, draft_ids, d2t):
+    _i32(parent, "parent")
+    if parent.dim() != 2:
+        raise ValueError("parent must be [B, N]")
+    if (draft_ids is None) != (d2t is None):
+        raise ValueError("draft_ids and d2t come together")
+    if draft_ids is not None:
+        _i32(draft_ids, "draft_ids", parent.numel())
+        _i32(d2t, "d2t")
+    return parent.shape
+
+
+def tree_rows(parent, draft_ids=None, d2t=None) -> RoundRows:
+    """B trees of N nodes: parent, draft_ids [B, N], d2t [Vd] int32.  The cache and the
+    attention need parent alone."""
+    B, N = _tree_tensors(parent, draft_ids, d2t)
+    return RoundRows(ROWS_TREE, B, 0, N, B * N, parent.device, draft_ids is not None, parent=parent,
+                     draft_ids=draft_ids, d2t=d2t)
+
+
+def routed_rows(row_offsets, total_rows: int, choice, chain_draft, parent, draft_ids=None,
+                d2t=None) -> RoundRows:
+    """A routed mix, as verify_routed takes it: chains where choice is 0, trees where it is 1."""
+    _i32(choice, "choice")
+    B = choice.numel()
+    _i32(row_offsets, "row_offsets", B + 1)
+    _i32(chain_draft, "chain_draft")
+    _, N = _tree_tensors(parent, draft_ids, d2t)
+    if chain_draft.dim() != 2 or chain_draft.shape[0] != B or parent.shape[0] != B:
+        raise ValueError("chain_draft must be [B, K] and parent [B, N] with the batch of choice")
+    return RoundRows(ROWS_ROUTED, B, chain_draft.shape[1], N, total_rows, choice.device,
+                     draft_ids is not None, chain_draft=chain_draft, parent=parent,
+                     draft_ids=draft_ids, d2t=d2t, row_offsets=row_offsets, choice=choice)
+
+
+def _history(history, V=None):
+    """(slots, V, row stride) of a token history: an int16 [slots, V] tensor whose rows are a
+    multiple of 16 bytes apart (its words are the uint16 words of the C interface)."""
+    _device_tensor(history, "history")
+    if history.dtype != torch.int16 or history.dim() != 2 or history.stride(1) != 1:
+        raise TypeError("history must be a 2-D int16 tensor with unit stride along the vocabulary")
+    slots, have = history.shape
+    if V is not None and have != V:
+        raise ValueError(f"history has {have} tokens, the logits {V}")
+    return slots, have, history.stride(0) if slots > 1 else (have + 7) // 8 * 8
+
+
+class LogitRules:
+    """The rules of decoding (wf_logit_rules); every rule is optional.
+
+    history [slots, V] int16 (history_prompt, history_update) with slot [B] int32 or None;
+    penalties [B, 3] float32 (repetition, frequency, presence); bias (offsets [B + 1] int32,
+    ids int32, values float32), each sequence's ids ascending; allow [rows, >= ceil(V / 32)]
+    int32 bit masks.  Holds its tensors."""
+
+    __slots__ = ("struct", "ref", "tensors", "V", "B", "rows", "device", "words")
+
+    def __init__(self, history=None, *, slot=None, penalties=None, bias=None, allow=None):
+        s = self.struct = _RulesStruct()
+        self.V = self.B = self.rows = self.words = self.device = None
+        self.tensors = (history, slot, penalties, bias, allow)
+        if history is not None:
+            s.slots, self.V, s.history_stride = _history(history)
+            s.history = history.data_ptr()
+            self._place(history, "history")
+        if slot is not None:
+            if history is None:
+                raise ValueError("slot without a history")
+            _i32(slot, "slot")
+            s.slot = slot.data_ptr()
+            self._batch(slot.numel(), "slot")
+            self._place(slot, "slot")
+        if penalties is not None:
+            _device_tensor(penalties, "penalties")
+            if penalties.dtype != torch.float32 or not penalties.is_contiguous() or \
+                    penalties.dim() != 2 or penalties.shape[1] != 3:
+                raise TypeError("penalties must be a contiguous float32 tensor [B, 3]")
+            s.penalties = penalties.data_ptr()
+            self._batch(penalties.shape[0], "penalties")
+            self._place(penalties, "penalties")
+        if bias is not None:
+            offsets, ids, values = bias
+            _i32(offsets, "bias offsets")
+            _i32(ids, "bias ids")
+            _device_tensor(values, "bias values")
+            if values.dtype != torch.float32 or not values.is_contiguous():
+                raise TypeError("bias values must be a contiguous float32 tensor")
+            if values.numel() != ids.numel():
+                raise ValueError(f"{ids.numel()} bias ids, {values.numel()} values")
+            s.bias_offsets, s.bias_ids, s.bias_values = (t.data_ptr() for t in bias)
+            s.bias_count = ids.numel()
+            self._batch(offsets.numel() - 1, "bias offsets")
+            for t in bias:
+                self._place(t, "bias")
+        if allow is not None:
+            _device_tensor(allow, "allow")
+            if allow.dtype != torch.int32 or allow.dim() != 2 or allow.stride(1) != 1:
+                raise TypeError("allow must be a 2-D int32 tensor with unit stride along the words")
+            self.rows, self.words = allow.shape
+            s.allow = allow.data_ptr()
+            s.allow_stride = allow.stride(0) if self.rows > 1 else max(self.words, 1)
+            self._place(allow, "allow")
+        self.ref = ctypes.byref(s)
+
+    def _place(self, t, name):
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the other rules on {self.device}")
+
+    def _batch(self, B, name):
+        if self.B is None:
+            self.B = B
+        elif self.B != B:
+            raise ValueError(f"{name} is for {B} sequences, the other rules for {self.B}")
+
+    def check(self, rows: RoundRows, V: int) -> None:
+        if self.device is not None and self.device != rows.device:
+            raise ValueError(f"the rules are on {self.device}, the round on {rows.device}")
+        if self.V is not None and self.V != V:
+            raise ValueError(f"the history has {self.V} tokens, the logits {V}")
+        if self.B is not None and self.B != rows.B:
+            raise ValueError(f"the rules are for {self.B} sequences, the round for {rows.B}")
+        if self.rows is not None and (self.rows != rows.total or self.words * 32 < V):
+            raise ValueError(f"allow must hold {rows.total} rows of {(V + 31) // 32} words")
+
+
+class PageCache:
+    """A paged key-value cache (wf_page_cache).  k, v [layers, pages, heads, page_size, head_dim]
+    (or without layers) float32 or bfloat16, each page contiguous; table [seqs, max_pages], held,
+    context [seqs], refs [pages] int32.  Holds its tensors, which the calls update in place."""
+
+    __slots__ = ("struct", "ref", "k", "v", "table", "held", "context", "refs", "device", "dtype",
+                 "heads", "head_dim", "seqs")
+
+    def __init__(self, k, v, table, held, context, refs):
+        _device_tensor(k, "k")
+        _device_tensor(v, "v")
+        if k.dim() not in (4, 5) or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype:
+            raise ValueError("k and v must be [layers,] pages, heads, page_size, head_dim tensors of "
+                             "one shape, type and strides")
+        pages, heads, page, dim = k.shape[-4:]
+        st = k.stride()
+        if st[-1] != 1 or st[-2] != dim or st[-3] != page * dim:
+            raise ValueError("each page of k and v must be contiguous")
+        layers = k.shape[0] if k.dim() == 5 else 1
+        _i32(table, "table")
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs, max_pages]")
+        seqs, most = table.shape
+        _i32(held, "held", seqs)
+        _i32(context, "context", seqs)
+        _i32(refs, "refs", pages)
+        self.device = k.device
+        _on(k.device, v=v, table=table, held=held, context=context, refs=refs)
+        self.k, self.v, self.table, self.held, self.context, self.refs = k, v, table, held, context, refs
+        self.dtype, self.heads, self.head_dim, self.seqs = k.dtype, heads, dim, seqs
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), st[0] if k.dim() == 5 else 0,
+                                   st[-4] if pages > 1 else heads * page * dim, _dtype_code(k), layers,
+                                   pages, heads, page, dim, seqs, most, table.data_ptr(),
+                                   held.data_ptr(), context.data_ptr(), refs.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, heads: int, page_size: int, head_dim: int, seqs: int,
+              max_pages: int, *, dtype=torch.bfloat16, device="cuda"):
+        """A cache of free pages and empty sequences."""
+        shape = (layers, pages, heads, page_size, head_dim)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros(shape, dtype=dtype, device=device),
+                   torch.zeros(shape, dtype=dtype, device=device),
+                   torch.full((seqs, max_pages), -1, **i32), torch.zeros(seqs, **i32),
+                   torch.zeros(seqs, **i32), torch.zeros(pages, **i32))
+
+
+# ----------------------------------------------------------------------------- logits
+
+
+def _ruled(logits, rows: RoundRows, rules: LogitRules):
+    _device_tensor(logits, "logits")
+    if logits.device != rows.device:
+        raise ValueError(f"logits is on {logits.device}, the round on {rows.device}")
+    if not rows.tokens:
+        raise ValueError("the rules need the round's draft tokens (draft_ids and d2t)")
+    V, stride = _rows_view(logits, rows.total)
+    rules.check(rows, V)
+    return V, stride
+
+
+def process_logits(logits, rows: RoundRows, rules: LogitRules, *, out=None, dtype=torch.float32,
+                   stream=None):
+    """The processed logits of a round's rows (see whiflash_process_logits).  logits [rows, V] or
+    [B, R, V]; out: a tensor of the rows' shape (logits itself for in place), or None for a new
+    one of `dtype` whose rows are a multiple of 16 bytes apart.  Returns out."""
+    V, stride = _ruled(logits, rows, rules)
+    with _Run(rows.device, stream) as run:
+        if out is None:
+            out = torch.empty((rows.total, (V + 7) // 8 * 8), dtype=dtype, device=rows.device)[:, :V]
+        else:
+            _device_tensor(out, "out")
+            if out.device != rows.device:
+                raise ValueError(f"out is on {out.device}, the round on {rows.device}")
+        oV, ostride = _rows_view(out, rows.total)
+        if oV != V:
+            raise ValueError(f"out has {oV} entries a row, the logits {V}")
+        _check(functions().process_logits(logits.data_ptr(), _dtype_code(logits), V, stride, rows.ref,
+                                          rules.ref, out.data_ptr(), _dtype_code(out), ostride,
+                                          run.stream))
+    return out
+
+
+def verify_constrained_workspace_bytes(rows: RoundRows, V: int) -> int:
+    return int(functions().verify_constrained_workspace_bytes(rows.ref, V))
+
+
+def verify_constrained(logits, rows: RoundRows, rules: LogitRules, *, row_argmax=True,
+                       accept_len=None, bonus=None, best_node=None, workspace=None, stream=None):
+    """Greedy verification of a round under the rules.  Returns (accept_len, bonus, best_node,
+    row_argmax); tokens are -1 where the rules leave nothing."""
+    V, stride = _ruled(logits, rows, rules)
+    dev = rows.device
+    with _Run(dev, stream) as run:
+        accept_len = _out(accept_len, torch.int32, rows.B, dev, "accept_len")
+        bonus = _out(bonus, torch.int32, rows.B, dev, "bonus")
+        best_node = _out(best_node, torch.int32, rows.B, dev, "best_node")
+        row_argmax = _opt_out(row_argmax, rows.total, dev, "row_argmax")
+        ws = _workspace(workspace, verify_constrained_workspace_bytes(rows, V), dev)
+        _check(functions().verify_constrained(
+            logits.data_ptr(), _dtype_code(logits), V, stride, rows.ref, rules.ref,
+            accept_len.data_ptr(), bonus.data_ptr(), best_node.data_ptr(),
+            None if row_argmax is None else row_argmax.data_ptr(),
+            None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), run.stream))
+    return accept_len, bonus, best_node, row_argmax
+
+
+# ----------------------------------------------------------------------------- history
+
+
+def _slot(slot, B, device):
+    if slot is None:
+        return None
+    _i32(slot, "slot", B)
+    _on(device, slot=slot)
+    return slot.data_ptr()
+
+
+def history_prompt(history, tokens, offsets, *, slot=None, stream=None) -> None:
+    """Marks prompt tokens: tokens[offsets[b]:offsets[b+1]] in row slot[b] (None: b)."""
+    slots, V, stride = _history(history)
+    _i32(tokens, "tokens")
+    _i32(offsets, "offsets")
+    if offsets.numel() < 1:
+        raise ValueError("offsets must hold B + 1 elements")
+    B = offsets.numel() - 1
+    _on(history.device, tokens=tokens, offsets=offsets)
+    with _Run(history.device, stream) as run:
+        _check(functions().history_prompt(history.data_ptr(), slots, V, stride, B,
+                                          _slot(slot, B, history.device), tokens.data_ptr(),
+                                          offsets.data_ptr(), tokens.numel(), run.stream))
+
+
+def history_update(history, rows: RoundRows, accept_len, best_node, bonus, *, slot=None,
+                   stream=None) -> None:
+    """Enters a verified round's accepted draft tokens and bonus tokens into the history.
+    best_node may be None for rounds of chains."""
+    slots, V, stride = _history(history)
+    if not rows.tokens:
+        raise ValueError("the history needs the round's draft tokens (draft_ids and d2t)")
+    _verified(rows, accept_len, best_node)
+    _i32(bonus, "bonus", rows.B)
+    _on(history.device, rows=next(iter(rows.tensors.values())), accept_len=accept_len, bonus=bonus)
+    with _Run(history.device, stream) as run:
+        _check(functions().history_update(
+            history.data_ptr(), slots, V, stride, rows.ref, _slot(slot, rows.B, history.device),
+            accept_len.data_ptr(), None if best_node is None else best_node.data_ptr(),
+            bonus.data_ptr(), run.stream))
+
+
+def _verified(rows, accept_len, best_node):
+    _i32(accept_len, "accept_len", rows.B)
+    _on(rows.device, accept_len=accept_len, best_node=best_node)
+    if best_node is not None:
+        _i32(best_node, "best_node", rows.B)
+    elif rows.kind != ROWS_CHAIN:
+        raise ValueError("rounds with trees need best_node")
+
+
+# ----------------------------------------------------------------------------- cache
+
+
+def _cache_call(cache: PageCache, rows: RoundRows, seqs):
+    if rows.device != cache.device:
+        raise ValueError(f"the round is on {rows.device}, the cache on {cache.device}")
+    if seqs is None:
+        return None
+    _i32(seqs, "seqs", rows.B)
+    _on(cache.device, seqs=seqs)
+    return seqs.data_ptr()
+
+
+def _vectors(t, name, rows, heads, cache):
+    """Row stride of [rows, heads, head_dim] vectors of the cache's type, each row contiguous."""
+    _device_tensor(t, name)
+    if t.device != cache.device or t.dtype != cache.dtype:
+        raise ValueError(f"{name} must be {cache.dtype} on {cache.device}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != cache.head_dim or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {cache.head_dim}]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != cache.head_dim):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return t.stride(0) if rows > 1 else t.shape[1] * t.shape[2]
+
+
+def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: int = 0, seqs=None,
+                 stream=None) -> None:
+    """Puts the rows' keys and values [rows, heads, head_dim] at positions context + i of their
+    sequences in one layer.  seqs [B] int32: the cache sequences (None: 0 .. B-1)."""
+    seq = _cache_call(cache, rows, seqs)
+    ks = _vectors(k_rows, "k_rows", rows.total, cache.heads, cache)
+    vs = _vectors(v_rows, "v_rows", rows.total, cache.heads, cache)
+    with _Run(cache.device, stream) as run:
+        _check(functions().cache_append(cache.ref, layer, rows.ref, seq, k_rows.data_ptr(), ks,
+                                        v_rows.data_ptr(), vs, run.stream))
+
+
+def attend_workspace_bytes(cache: PageCache, rows: RoundRows, q_heads: int, max_context: int) -> int:
+    return int(functions().attend_workspace_bytes(cache.ref, rows.ref, q_heads, max_context))
+
+
+def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, scale=None,
+           max_context=None, out=None, workspace=None, stream=None):
+    """Attention of the rows' queries q [rows, q_heads, head_dim] over the cache.  scale: None for
+    head_dim ** -0.5; max_context: an upper bound of the sequences' committed lengths that the host
+    knows (None: what a table row can hold).  Returns out [rows, q_heads, head_dim]."""
+    seq = _cache_call(cache, rows, seqs)
+    qs = _vectors(q, "q", rows.total, None, cache)
+    heads = q.shape[1]
+    s = cache.struct
+    if max_context is None:
+        max_context = s.max_pages * s.page_size
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    with _Run(cache.device, stream) as run:
+        if out is None:
+            out = torch.empty((rows.total, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
+        else:
+            _out(out, cache.dtype, rows.total * heads * cache.head_dim, cache.device, "out")
+        ws = _workspace(workspace, attend_workspace_bytes(cache, rows, heads, max_context), cache.device)
+        _check(functions().attend(q.data_ptr(), qs, heads, cache.ref, layer, rows.ref, seq, max_context,
+                                  scale, out.data_ptr(), None if ws is None else ws.data_ptr(),
+                                  0 if ws is None else ws.numel() * ws.element_size(), run.stream))
+    return out
+
+
+def cache_compact(cache: PageCache, rows: RoundRows, accept_len, best_node=None, *, seqs=None,
+                  next_context=None, stream=None) -> None:
+    """Moves each accepted tree path's rows to the front of the round's positions, in every layer,
+    and commits accept_len positions: next_context (None: the cache's context, in place) gets
+    context + accept_len.  best_node may be None for rounds of chains."""
+    seq = _cache_call(cache, rows, seqs)
+    _verified(rows, accept_len, best_node)
+    if next_context is not None:
+        _i32(next_context, "next_context", cache.seqs)
+        _on(cache.device, next_context=next_context)
+    with _Run(cache.device, stream) as run:
+        _check(functions().cache_compact(cache.ref, rows.ref, seq, accept_len.data_ptr(),
+                                         None if best_node is None else best_node.data_ptr(),
+                                         None if next_context is None else next_context.data_ptr(),
+                                         run.stream))
+
+
+def cache_pages_workspace_bytes(cache: PageCache, n: int) -> int:
+    return int(functions().cache_pages_workspace_bytes(cache.ref, n))
+
+
+def _pages_call(fn, cache, first, second, names, status, workspace, stream):
+    _i32(first, names[0])
+    n = first.numel()
+    _i32(second, names[1], n)
+    _on(cache.device, **{names[0]: first, names[1]: second})
+    with _Run(cache.device, stream) as run:
+        status = _out(status, torch.int32, n, cache.device, "status")
+        ws = _workspace(workspace, cache_pages_workspace_bytes(cache, n), cache.device)
+        _check(fn(cache.ref, n, first.data_ptr(), second.data_ptr(), status.data_ptr(),
+                  None if ws is None else ws.data_ptr(),
+                  0 if ws is None else ws.numel() * ws.element_size(), run.stream))
+    return status
+
+
+def cache_fork(cache: PageCache, src, dst, *, status=None, workspace=None, stream=None):
+    """Makes sequence dst[i] a fork of src[i]: full pages shared, the last partly filled one copied.
+    Returns status [n] int32, 1 where done, 0 where refused."""
+    return _pages_call(functions().cache_fork, cache, src, dst, ("src", "dst"), status, workspace, stream)
+
+
+def cache_reserve(cache: PageCache, count, *, seqs, status=None, workspace=None, stream=None):
+    """Gives sequence seqs[i] pages for context + count[i] positions.  Returns status [n] int32."""
+    return _pages_call(functions().cache_reserve, cache, seqs, count, ("seqs", "count"), status,
+                       workspace, stream)
+
+
+def cache_free(cache: PageCache, seqs, *, stream=None) -> None:
+    """Frees the sequences' pages and empties the sequences."""
+    _i32(seqs, "seqs")
+    _on(cache.device, seqs=seqs)
+    with _Run(cache.device, stream) as run:
+        _check(functions().cache_free(cache.ref, seqs.numel(), seqs.data_ptr(), run.stream))

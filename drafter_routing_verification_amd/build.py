@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libwhiflash.so")
 SOURCES = ["api.hip", "sweep.hip", "finalize.hip", "router.hip", "entropy.hip", "catchup.hip", "round.hip", "early_exit.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "api_rounds.hip", "rules.hip", "history.hip", "attend.hip", "pages.hip"]
 ARCH = "gfx950"
 
 

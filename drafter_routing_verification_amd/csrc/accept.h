@@ -119,7 +119,8 @@ __device__ inline void chain_accept(int draft0, const int* t_s, int K,
   for (int i0 = 0; i0 < K; i0 += 64) {
     const int i = i0 + lane;
     const int d = i0 == 0 ? draft0 : (i < K ? draft[i] : -1);
-    const bool mismatch = i < K && d != t_s[i];
+    // A row without a token (t = -1, whiflash_verify_constrained) matches no draft.
+    const bool mismatch = i < K && (d != t_s[i] || d < 0);
     const unsigned long long mask = __ballot(mismatch);
     if (mask) {
       n = i0 + __ffsll(mask) - 1;

@@ -518,6 +518,268 @@ int32_t whiflash_round_chain_noalloc(const void* hidden, int32_t hidden_dtype, i
                                      const int32_t* draft, int32_t* accept_len, int32_t* bonus,
                                      int32_t* row_argmax, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the round: the rules of decoding on the logits, the token history, the
+ * paged key-value cache and the attention that reads it.  These calls describe
+ * the round's rows, the rules and the cache by host structs of device pointers;
+ * a struct is read during the call and not kept.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { WF_ROWS_CHAIN = 0, WF_ROWS_TREE = 1, WF_ROWS_ROUTED = 2 } wf_rows_kind;
+
+/*
+ * The rows of one round, as the verify entry points lay them out:
+ *   WF_ROWS_CHAIN   B * (K + 1) rows; row b*(K+1)+i follows the first i drafts of
+ *                   chain_draft [B, K];
+ *   WF_ROWS_TREE    B * N rows; row b*N+u follows node u of the tree parent [B, N],
+ *                   draft_ids [B, N], d2t [Vd] (node 0 is the root);
+ *   WF_ROWS_ROUTED  total_rows packed rows; sequence b owns rows [row_offsets[b],
+ *                   row_offsets[b+1]): a chain's K + 1 (choice[b] = 0) or a tree's N
+ *                   (choice[b] = 1).  A sequence whose offsets are decreasing or
+ *                   outside [0, total_rows], whose row count does not match its
+ *                   choice, or whose choice is neither is malformed.
+ * K + 1 and N are at most WHIFLASH_MAX_SEQ_ROWS; fields of the other kinds are
+ * not read (a routed round has K >= 0 and N >= 1).  total_rows is read for routed
+ * rounds.  Calls that need no draft tokens (the cache's and the attention) do not
+ * read chain_draft, draft_ids or d2t.
+ *
+ * The path of a row is the row itself and the rows of its node's ancestors (a
+ * chain's row i: rows 0..i).  A node whose parent lies outside [0, u) has none:
+ * its path ends with it.  The path's tokens are the draft tokens of its nodes
+ * without the first row's; a draft id outside [0, Vd), a table entry or chain
+ * draft outside [0, V) is no token.
+ */
+typedef struct wf_round_rows {
+  int32_t kind, B, K, N, Vd, total_rows;
+  const int32_t* chain_draft;
+  const int32_t* parent;
+  const int32_t* draft_ids;
+  const int32_t* d2t;
+  const int32_t* row_offsets;
+  const int32_t* choice;
+} wf_round_rows;
+
+/*
+ * The rules of decoding for B sequences over V tokens; every pointer may be NULL
+ * (that rule is off).
+ *   history [slots, V] uint16, rows history_stride elements apart (base and row
+ *     stride multiples of 16 bytes): one word per token, bit 15 set if the token
+ *     is in the prompt, the low 15 bits how often it was put out (it stays at
+ *     32767).  Sequence b uses row slot[b] (slot NULL: b); a slot outside
+ *     [0, slots) means no history.
+ *   penalties [B, 3] float32: repetition, frequency, presence.
+ *   bias_offsets [B + 1], bias_ids, bias_values [bias_count] (float32): sequence b
+ *     adds bias_values[i] to token bias_ids[i] for i in [bias_offsets[b],
+ *     bias_offsets[b+1]).  Each sequence's ids ascend strictly (otherwise which of
+ *     its entries are applied is unspecified); ids outside [0, V) are ignored.
+ *   allow [rows, allow_stride] int32, 32 tokens a word, lowest bit first: row r
+ *     allows token v iff bit v % 32 of word v / 32 of its row is set;
+ *     allow_stride >= ceil(V / 32).  Rows are the round's packed rows.
+ *
+ * The processed logit of token v in row r of sequence b, in float32, each
+ * operation rounded once: with h the history word, e the times v is among the
+ * path's tokens, c = (h & 0x7fff) + e and seen = (h >> 15) or c > 0,
+ *   x = logit;  if seen: x = x > 0 ? x / repetition : x * repetition;
+ *   x = x - frequency * c;  x = x - presence * (c > 0);  x = x + bias;
+ *   x = -inf if v is not allowed.
+ * Without penalties the first three steps are left out.
+ */
+typedef struct wf_logit_rules {
+  const uint16_t* history;
+  int64_t history_stride;
+  int32_t slots;
+  int32_t bias_count;
+  const int32_t* slot;
+  const float* penalties;
+  const int32_t* bias_offsets;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  const int32_t* allow;
+  int64_t allow_stride;
+} wf_logit_rules;
+
+/*
+ * The processed logits of a round's rows, written out (for a sampler).
+ *   logits: the round's rows of V entries, row_stride apart; out: as many rows of
+ *   out_dtype, out_stride apart (base and row stride multiples of 16 bytes).  out
+ *   may be logits itself with the same dtype and stride; otherwise they must not
+ *   overlap.  Rows of malformed sequences, rows that no sequence owns and the
+ *   entries past V are left as they were.  bfloat16 output is rounded to nearest
+ *   even.  Rows that two sequences own hold either one's values.
+ * B == 0 is a no-op.  No workspace.
+ */
+int32_t whiflash_process_logits(const void* logits, int32_t dtype, int32_t V, int64_t row_stride,
+                                const wf_round_rows* rows, const wf_logit_rules* rules, void* out,
+                                int32_t out_dtype, int64_t out_stride, hipStream_t stream);
+
+/* Workspace bytes of whiflash_verify_constrained (host only; 0 on bad sizes). */
+size_t whiflash_verify_constrained_workspace_bytes(const wf_round_rows* rows, int32_t V);
+
+/*
+ * Greedy verification under the rules: whiflash_verify_chain, _tree or _routed on
+ * the processed logits, without writing them.  t[r] is the lowest token holding
+ * the maximum of row r's processed logits, or -1 when all of them are -inf (a mask
+ * that leaves nothing): no draft matches it, and it is the bonus token if the row
+ * is the last accepted one.  A malformed sequence gets accept_len 0, bonus -1 and
+ * best_node -1.  row_argmax (when not NULL) is written for the rows of well-formed
+ * sequences.  best_node may be NULL (a chain's is accept_len - 1).  Without any
+ * rule the results are those of the plain calls, rows of only -inf aside.
+ * The logits must not be NaN (t is then unspecified, in [-1, V)).
+ * Workspace: whiflash_verify_constrained_workspace_bytes(rows, V), 256-byte
+ * aligned, contents ignored on entry; calls sharing one must not overlap in time.
+ */
+int32_t whiflash_verify_constrained(const void* logits, int32_t dtype, int32_t V,
+                                    int64_t row_stride, const wf_round_rows* rows,
+                                    const wf_logit_rules* rules, int32_t* accept_len,
+                                    int32_t* bonus, int32_t* best_node, int32_t* row_argmax,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Marks prompt tokens in the history: for i in [offsets[b], offsets[b+1]), bit 15
+ * of history[slot[b]][tokens[i]].  tokens holds `count` int32; offsets [B + 1] are
+ * cut to [0, count].  Tokens outside [0, V) and slots outside [0, slots) are
+ * skipped.
+ */
+int32_t whiflash_history_prompt(uint16_t* history, int32_t slots, int32_t V, int64_t history_stride,
+                                int32_t B, const int32_t* slot, const int32_t* tokens,
+                                const int32_t* offsets, int32_t count, hipStream_t stream);
+
+/*
+ * Enters a verified round's tokens into the history: the draft tokens of the
+ * accepted path (the path of row accept_len[b] - 1 of a chain, of best_node[b] of a
+ * tree, without the first row) and the bonus token each count once more.  Tokens
+ * outside [0, V) are skipped; a malformed sequence, a chain's accept_len outside
+ * [1, K + 1] and a tree's best_node outside [0, N) or whose path does not reach the
+ * root enter nothing.  best_node may be NULL for rounds of chains.
+ */
+int32_t whiflash_history_update(uint16_t* history, int32_t slots, int32_t V, int64_t history_stride,
+                                const wf_round_rows* rows, const int32_t* slot,
+                                const int32_t* accept_len, const int32_t* best_node,
+                                const int32_t* bonus, hipStream_t stream);
+
+/*
+ * A paged key-value cache.  Page p of layer l holds page_size positions of every
+ * head: element d of position o of head h of the keys is
+ *   k[l * layer_stride + p * page_stride + (h * page_size + o) * head_dim + d]
+ * (strides in elements, the page's stride and the base multiples of 16 bytes; v
+ * alike).  dtype WF_F32 or WF_BF16; head_dim 64 or 128; page_size a power of two
+ * from 16 to 1024.
+ *   table [seqs, max_pages]: the pages of each sequence's positions (position j in
+ *     page table[s][j / page_size]); -1 where it holds none;
+ *   held [seqs]: how many entries of its table row hold pages;
+ *   context [seqs]: its committed positions;
+ *   refs [pages]: how many table entries hold each page (0: the page is free).
+ * An empty cache has table -1 and held, context and refs 0.  A position at or past
+ * a sequence's context is in a page that no other sequence holds: whiflash_cache_fork
+ * keeps it so.  A call's sequence b is the cache's sequence seq[b] (seq NULL: b).
+ */
+typedef struct wf_page_cache {
+  void* k;
+  void* v;
+  int64_t layer_stride, page_stride;
+  int32_t dtype, layers, pages, heads, page_size, head_dim, seqs, max_pages;
+  int32_t* table;
+  int32_t* held;
+  int32_t* context;
+  int32_t* refs;
+} wf_page_cache;
+
+/*
+ * Puts the keys and values of a round's rows into one layer of the cache: row i of
+ * sequence s at position context[s] + i.  k_rows, v_rows: rows of heads * head_dim
+ * elements of the cache's dtype, k_row_stride and v_row_stride elements apart (bases
+ * and row strides multiples of 16 bytes), which must not overlap the cache.  Rows of
+ * malformed sequences, of sequences outside [0, seqs) and at positions without a
+ * page are skipped.
+ */
+int32_t whiflash_cache_append(const wf_page_cache* cache, int32_t layer, const wf_round_rows* rows,
+                              const int32_t* seq, const void* k_rows, int64_t k_row_stride,
+                              const void* v_rows, int64_t v_row_stride, hipStream_t stream);
+
+/* Workspace bytes of whiflash_attend (host only; 0 on bad sizes). */
+size_t whiflash_attend_workspace_bytes(const wf_page_cache* cache, const wf_round_rows* rows,
+                                       int32_t q_heads, int32_t max_context);
+
+/*
+ * Attention of a round's rows over the cache (their own keys and values are in it,
+ * whiflash_cache_append).  Row i of sequence s sees the committed positions
+ * [0, context[s]) and, of the round's own positions context[s] + u, those whose row u
+ * is on its path: a chain's are causal, a tree's follow its ancestors.  With K = 0
+ * this is the attention of one new token.  For head h, with key-value head
+ * h / (q_heads / heads),
+ *   out[r, h] = sum_j p_j v_j,  p = softmax over the seen j of scale * q[r, h] . k_j
+ * q: rows of q_heads * head_dim elements of the cache's dtype, q_row_stride elements
+ * apart; out [rows, q_heads, head_dim] of the same dtype.  q_heads is a multiple of
+ * heads.  max_context: no context is larger (it sizes the launch).
+ *   Scores, maxima and sums are float32; for bfloat16 the weights p (relative to the
+ * largest) are rounded to bfloat16 before they multiply v, as the matrix units take
+ * them.  The order of all sums is fixed: results are reproducible bit by bit.
+ *   Positions without a page (a table entry outside [0, pages)) are not seen.  A row
+ * that sees nothing gets zeros, and so do the rows of a sequence outside [0, seqs), or
+ * whose context is negative, above max_context or leaves its rows no room in max_pages
+ * pages.  Rows of malformed sequences and rows that no sequence owns are left as they
+ * were.
+ * Workspace: whiflash_attend_workspace_bytes(cache, rows, q_heads, max_context) bytes,
+ * 256-byte aligned, contents ignored on entry; calls sharing one must not overlap.
+ */
+int32_t whiflash_attend(const void* q, int64_t q_row_stride, int32_t q_heads,
+                        const wf_page_cache* cache, int32_t layer, const wf_round_rows* rows,
+                        const int32_t* seq, int32_t max_context, float scale, void* out,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Keeps the accepted rows of a verified round: in every layer, the keys and values of
+ * the accepted path's rows u_0 < u_1 < ... move from position context + u_j to
+ * context + j, and next_context[s] = context[s] + accept_len[b].  A chain's rows are
+ * in place already.  next_context [seqs] may be the cache's context itself (NULL
+ * means that).  Nothing moves and next_context[s] = context[s] for a malformed
+ * sequence, a chain whose accept_len is outside [0, K + 1], and a tree whose best_node
+ * is outside [0, N) or has no path of accept_len rows to the root.  Positions without
+ * a page are skipped.  best_node may be NULL for rounds of chains.  A cache sequence
+ * may occur once in seq.
+ */
+int32_t whiflash_cache_compact(const wf_page_cache* cache, const wf_round_rows* rows,
+                               const int32_t* seq, const int32_t* accept_len,
+                               const int32_t* best_node, int32_t* next_context,
+                               hipStream_t stream);
+
+/* Workspace bytes of whiflash_cache_fork and whiflash_cache_reserve for n entries
+ * (host only; 0 on bad sizes). */
+size_t whiflash_cache_pages_workspace_bytes(const wf_page_cache* cache, int32_t n);
+
+/*
+ * Forks sequences: dst[i] becomes a copy of src[i], with the full pages of its context
+ * shared (refs + 1) and a partly filled last page copied, in every layer, into a free
+ * page.  status[i] is 1 if done, 0 if refused (nothing changed then): an index outside
+ * [0, seqs); a src whose context is negative or past its held pages, or that is a dst
+ * of the same call; a dst that holds pages or appeared before in dst; no free page left.
+ * Free pages are handed out lowest first, in the order of the entries; from the first
+ * entry on that finds too few, entries that need pages are refused.
+ * Workspace: whiflash_cache_pages_workspace_bytes(cache, n) bytes, 256-byte aligned.
+ */
+int32_t whiflash_cache_fork(const wf_page_cache* cache, int32_t n, const int32_t* src,
+                            const int32_t* dst, int32_t* status, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gives sequences room: seq[i] gets free pages until its pages hold context + count[i]
+ * positions.  status[i] is 1 if it has the room now, 0 if refused (nothing changed): an
+ * index outside [0, seqs) or that appeared before, a negative context or count, more
+ * than max_pages pages, or too few free pages.  Order and workspace as in
+ * whiflash_cache_fork.
+ */
+int32_t whiflash_cache_reserve(const wf_page_cache* cache, int32_t n, const int32_t* seq,
+                               const int32_t* count, int32_t* status, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Frees sequences: every page that seq[i] holds loses one reference, its table entries
+ * become -1, its held and context 0.  Indices outside [0, seqs) and sequences that hold
+ * nothing (one named twice, the second time) are skipped.
+ */
+int32_t whiflash_cache_free(const wf_page_cache* cache, int32_t n, const int32_t* seq,
+                            hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
