@@ -9,6 +9,8 @@ namespace {
 constexpr size_t kWorkspaceAlign = 256;
 constexpr int64_t kMaxBlocks = int64_t{1} << 22;  // x 1024 threads: below 2^32 work items
 
+constexpr int32_t kMaxVocab = 1 << 30;
+
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 inline bool valid_dtype(int32_t d) { return d == WF_F32 || d == WF_BF16; }
@@ -70,14 +72,15 @@ int32_t check_pointers(const wf_round_rows* r, bool tokens) {
 
 int32_t check_matrix(const void* p, int32_t dtype, int64_t rows, int32_t V, int64_t stride) {
   if (!valid_dtype(dtype)) return WF_ERR_DTYPE;
-  if (V <= 0 || stride < V || stride > INT64_MAX / 16 / (rows > 0 ? rows : 1)) return WF_ERR_SHAPE;
+  if (V <= 0 || V > kMaxVocab || stride < V || stride > INT64_MAX / 16 / (rows > 0 ? rows : 1))
+    return WF_ERR_SHAPE;
   if (rows > 0 && !p) return WF_ERR_NULL;
   if (!aligned16(p) || (stride * elem_bytes(dtype)) % 16 != 0) return WF_ERR_ALIGN;
   return WF_OK;
 }
 
 int32_t check_history(const uint16_t* h, int32_t slots, int32_t V, int64_t stride) {
-  if (slots < 0 || V <= 0 || stride < V || stride > INT64_MAX / 4 / (slots > 0 ? slots : 1))
+  if (slots < 0 || V <= 0 || V > kMaxVocab || stride < V || stride > INT64_MAX / 4 / (slots > 0 ? slots : 1))
     return WF_ERR_SHAPE;
   if (slots > 0 && !h) return WF_ERR_NULL;
   if (!aligned16(h) || stride % 8 != 0) return WF_ERR_ALIGN;
@@ -184,7 +187,7 @@ int32_t whiflash_process_logits(const void* logits, int32_t dtype, int32_t V, in
 
 size_t whiflash_verify_constrained_workspace_bytes(const wf_round_rows* rows, int32_t V) {
   int64_t total = 0;
-  if (V <= 0 || check_sizes(rows, &total) != WF_OK || rows->B == 0) return 0;
+  if (V <= 0 || V > kMaxVocab || check_sizes(rows, &total) != WF_OK || rows->B == 0) return 0;
   const wf::RowsArgs a = rows_args(rows, total);
   // The chunk count depends on the element type: the larger of the two.
   size_t most = 0;

@@ -11,95 +11,393 @@
 namespace wf {
 namespace {
 
-constexpr int kChunk = 8192;  // entries of a row per workgroup
+constexpr int kVecsPer = 4;                       // 16-byte vectors of a row per thread
+constexpr int kChunkVecs = kVecsPer * kThreads;   // vectors of a row per workgroup
+constexpr int kBiasLds = 256;                     // biases of a chunk that are kept in LDS
+constexpr int kMaxGroup = 64;                     // rows per workgroup
+constexpr int kArgmax = -1;
+constexpr int64_t kRulesBlocks = 8192;            // workgroups of a large launch
 
 struct RulesArgs {
   RowsArgs rows;
   wf_logit_rules rules;
   const unsigned char* logits;
   int64_t row_bytes;
-  int V, chunks;
+  int V, nvec, chunks, groups, group;
   Partial* part;       // argmax: [B * rmax][chunks]
   unsigned char* out;  // written form
   int64_t out_bytes;
 };
 
-// One workgroup per (sequence, row, chunk); OUT < 0: argmax.
+// A round's drafted tokens that lie in one chunk, and the paths of its rows.
+struct PathLds {
+  int tok[kMaxSeqRows];                // target token of node u, -1 for none
+  int par[kMaxSeqRows];                // parent of node u, -1 where its path ends
+  unsigned long long anc[64];          // ancestors-or-self of node u, trees of up to 64
+  int node[kMaxSeqRows];               // nodes whose token lies in the chunk, any order
+  int count;
+  unsigned node_bits[kChunkVecs / 4];  // one byte a vector: elements that some node drafted
+  unsigned bias_bits[kChunkVecs / 4];  // ... and that have a bias
+  int bias_id[kBiasLds];
+  float bias_value[kBiasLds];
+};
+
+// Element k of a vector of history words (8 or 4 of them).
+template <int DT>
+__device__ inline unsigned word_at(const u32x4& h, int k) {
+  const unsigned w = k < 2 ? h.x : k < 4 ? h.y : k < 6 ? h.z : h.w;
+  return (w >> ((k & 1) * 16)) & 0xffffu;
+}
+
+// How often token t is among the path tokens of row i.
+__device__ inline int times_on_path(const PathLds& L, bool tree, int n, int i, int t) {
+  int c = 0;
+  if (tree && n > 64) {
+    for (int u = i; u > 0; u = L.par[u]) c += L.tok[u] == t;
+    return c;
+  }
+  const unsigned long long path =
+      !tree ? 0ull : L.anc[i];
+  for (int j = 0; j < L.count; ++j) {
+    const int u = L.node[j];
+    const bool on = tree ? (path >> u) & 1ull : u <= i;
+    c += on && L.tok[u] == t;
+  }
+  return c;
+}
+
+// Maximum over the 64 lanes of a wave, in every lane.
+__device__ inline float wave_max_f32(float x) {
+  x = fmaxf(x, dpp_mov<kDppQuadXor1>(x));
+  x = fmaxf(x, dpp_mov<kDppQuadXor2>(x));
+  x = fmaxf(x, dpp_mov<kDppHalfMirror>(x));
+  x = fmaxf(x, dpp_mov<kDppMirror>(x));
+  x = fmaxf(x, dpp_mov<kDppBcast15, 0xa>(x));
+  x = fmaxf(x, dpp_mov<kDppBcast31, 0xc>(x));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// The first n of a vector's PER values, at vector v of an output row.
+template <int OUT, int PER>
+__device__ inline void store_vec(unsigned char* row, int v, const float* x, int n) {
+  if constexpr (OUT == WF_F32) {
+    float* p = reinterpret_cast<float*>(row) + static_cast<int64_t>(v) * PER;
+    if (n == PER) {
+#pragma unroll
+      for (int k = 0; k < PER; k += 4)
+        *reinterpret_cast<float4*>(p + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (k < n) p[k] = x[k];
+    }
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + static_cast<int64_t>(v) * PER;
+    if (n == PER) {
+      unsigned w[PER / 2];
+#pragma unroll
+      for (int k = 0; k < PER / 2; ++k) w[k] = bf16_bits(x[2 * k]) | bf16_bits(x[2 * k + 1]) << 16;
+      if constexpr (PER == 8) {
+        *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (k < n) p[k] = static_cast<uint16_t>(bf16_bits(x[k]));
+    }
+  }
+}
+
+// One workgroup per (sequence, group of rows, chunk of the vocabulary), the group's rows
+// one after the other: a chunk's history words stay in registers for all of them.
+//
+// HBM-bound streaming of the logits.  Nearly all tokens have neither history nor bias
+// and were not drafted in this round, so every element has one "special" bit, worked
+// out once a workgroup: elements without it take the plain path (a masked maximum, or a
+// copy), and each lane handles the special ones of its vectors in a loop of its own.
+// The path's tokens differ from row to row; only elements that some node drafted look
+// them up.  A row's maximum is reduced over the wave first, and only the lanes that hold
+// it look for its index.
 template <int DT, int OUT>
 __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
-  __shared__ int path_s[kMaxSeqRows];
-  __shared__ int np_s;
-  __shared__ float sv[kWaves];
-  __shared__ int si[kWaves];
+  using E = Elem<DT>;
+  constexpr int kPer = E::kPerVec;
+  constexpr unsigned kAll = (1u << kPer) - 1u;
+  __shared__ PathLds L;
+  __shared__ Partial best_s[OUT == kArgmax ? kMaxGroup : 1][kWaves];
   const int tid = threadIdx.x;
   const int c = blockIdx.x % a.chunks;
-  const int bi = blockIdx.x / a.chunks;
-  const int b = bi / a.rows.rmax, i = bi - b * a.rows.rmax;
+  const int bg = blockIdx.x / a.chunks;
+  const int b = bg / a.groups, g = bg - b * a.groups;
   const SeqRows q = seq_rows(a.rows, b);
-  if (i >= q.n) return;
-  const int64_t r = static_cast<int64_t>(q.row0) + i;
-  // The row's path tokens.
-  if (tid == 0) {
-    int n = 0;
-    for (int u = i; u > 0; u = node_parent(a.rows, b, q.tree, u)) {
-      const int v = node_token(a.rows, b, q.tree, u, a.V);
-      if (v >= 0 && v / kChunk == c) path_s[n++] = v;
-    }
-    np_s = n;
-  }
-  __syncthreads();
-  const int np = np_s;
+  const int i0 = g * a.group, i1 = min(i0 + a.group, q.n);
+  if (i0 >= i1) return;
   const wf_logit_rules& R = a.rules;
+  const int v0 = c * kChunkVecs + tid;  // the thread's vectors: v0 + u * kThreads
+  const int tail = a.V - a.nvec * kPer;
+
+  const unsigned char* rowp = a.logits + (static_cast<int64_t>(q.row0) + i0) * a.row_bytes;
+  auto load_row = [&](const unsigned char* p, u32x4* d) {
+#pragma unroll
+    for (int u = 0; u < kVecsPer; ++u) {
+      const int v = v0 + u * kThreads;
+      if (v < a.nvec) {
+        d[u] = load16(reinterpret_cast<const u32x4*>(p) + v);
+      } else if (v == a.nvec && tail) {
+        // The entries past the last whole vector, one by one.
+        unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (k < tail) {
+            if constexpr (DT == WF_BF16) {
+              const unsigned x = reinterpret_cast<const uint16_t*>(p)[v * kPer + k];
+              w[k >> 1] |= x << ((k & 1) * 16);
+            } else {
+              w[k] = reinterpret_cast<const unsigned*>(p)[v * kPer + k];
+            }
+          }
+        }
+        d[u] = u32x4{w[0], w[1], w[2], w[3]};
+      }
+    }
+  };
+  u32x4 d[kVecsPer] = {};
+  load_row(rowp, d);
+
+  // What the chunk's elements need beyond a mask.
   Penalties pen{1.f, 0.f, 0.f};
   const bool penal = R.penalties != nullptr;
   if (penal) pen = Penalties{R.penalties[3 * b], R.penalties[3 * b + 1], R.penalties[3 * b + 2]};
-  const int slot = R.history ? slot_of(R.slot, b, R.slots) : -1;
+  const int slot = penal && R.history ? slot_of(R.slot, b, R.slots) : -1;
+  u32x4 hw[kVecsPer] = {};
+  unsigned valid = 0, special = 0;
   const uint16_t* hist = slot >= 0 ? R.history + slot * R.history_stride : nullptr;
+#pragma unroll
+  for (int u = 0; u < kVecsPer; ++u) {
+    const int v = v0 + u * kThreads;
+    const unsigned have = v < a.nvec ? kAll : v == a.nvec ? (1u << tail) - 1u : 0u;
+    valid |= have << (8 * u);
+    if (hist && have) {
+      if (have == kAll) {
+        if constexpr (DT == WF_BF16) {
+          hw[u] = reinterpret_cast<const u32x4*>(hist)[v];
+        } else {
+          const uint2 h = reinterpret_cast<const uint2*>(hist)[v];
+          hw[u].x = h.x;
+          hw[u].y = h.y;
+        }
+      } else {
+        unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (k < tail) w[k >> 1] |= static_cast<unsigned>(hist[v * kPer + k]) << ((k & 1) * 16);
+        hw[u] = u32x4{w[0], w[1], w[2], w[3]};
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kVecsPer; ++u) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      special |= word_at<DT>(hw[u], k) ? 1u << (8 * u + k) : 0u;
+  }
   int blo = 0, bhi = 0;
   if (R.bias_offsets) {
     blo = min(max(R.bias_offsets[b], 0), R.bias_count);
     bhi = min(max(R.bias_offsets[b + 1], blo), R.bias_count);
+    const int t0 = c * kChunkVecs * kPer;
+    blo = lower_bound(R.bias_ids, blo, bhi, t0);
+    bhi = lower_bound(R.bias_ids, blo, bhi, min(t0 + kChunkVecs * kPer, a.V));
   }
-  const unsigned char* rowp = a.logits + r * a.row_bytes;
-  const int32_t* allow = R.allow ? R.allow + r * R.allow_stride : nullptr;
-  float best = -INFINITY;
-  int idx = -1;
-  const int end = min((c + 1) * kChunk, a.V);
-  for (int v = c * kChunk + tid; v < end; v += kThreads) {
-    float x = Elem<DT>::scalar(rowp, v);
-    if (penal) {
-      int extra = 0;
-      for (int k = 0; k < np; ++k) extra += path_s[k] == v;
-      x = apply_penalties(x, hist ? hist[v] : 0u, extra, pen);
-    }
-    if (blo < bhi) {
-      const int k = lower_bound(R.bias_ids, blo, bhi, v);
-      if (k < bhi && R.bias_ids[k] == v) x += R.bias_values[k];
-    }
-    if (allow && !((static_cast<unsigned>(allow[v >> 5]) >> (v & 31)) & 1u)) x = -INFINITY;
-    if constexpr (OUT < 0) {
-      if (x > best) {
-        best = x;
-        idx = v;
+  const bool paths = penal && q.n > 1;
+  unsigned node_bits = 0, bias_bits = 0;
+  if (paths || blo < bhi) {
+    if (tid == 0) L.count = 0;
+    L.node_bits[tid] = 0;
+    L.bias_bits[tid] = 0;
+    __syncthreads();
+    if (paths) {
+      for (int u = 1 + tid; u < q.n; u += kThreads) {
+        const int t = node_token(a.rows, b, q.tree, u, a.V);
+        L.tok[u] = t;
+        if (q.tree) L.par[u] = node_parent(a.rows, b, true, u);
+        const int v = t / kPer - c * kChunkVecs;
+        if (t >= 0 && v >= 0 && v < kChunkVecs) {
+          L.node[atomicAdd(&L.count, 1)] = u;
+          atomicOr(&L.node_bits[v >> 2], 1u << ((v & 3) * 8 + t % kPer));
+        }
       }
-    } else if constexpr (OUT == WF_F32) {
-      reinterpret_cast<float*>(a.out + r * a.out_bytes)[v] = x;
-    } else {
-      reinterpret_cast<uint16_t*>(a.out + r * a.out_bytes)[v] = static_cast<uint16_t>(bf16_bits(x));
     }
-  }
-  if constexpr (OUT < 0) {
-    wave_argmax_to_lane63(best, idx);
-    if ((tid & 63) == 63) {
-      sv[tid >> 6] = best;
-      si[tid >> 6] = idx;
+    for (int k = blo + tid; k < bhi; k += kThreads) {
+      const int t = R.bias_ids[k];
+      const int v = t / kPer - c * kChunkVecs;
+      // (ids out of order may lie outside the chunk)
+      if (t >= 0 && v >= 0 && v < kChunkVecs)
+        atomicOr(&L.bias_bits[v >> 2], 1u << ((v & 3) * 8 + t % kPer));
+      if (k - blo < kBiasLds) {
+        L.bias_id[k - blo] = t;
+        L.bias_value[k - blo] = R.bias_values[k];
+      }
     }
     __syncthreads();
-    if (tid == 0) {
-      best = sv[0];
-      idx = si[0];
-      for (int w = 1; w < kWaves; ++w) better_partial(best, idx, sv[w], si[w]);
-      a.part[static_cast<int64_t>(bi) * a.chunks + c] = Partial{best, idx};
+    if (paths && q.tree && q.n <= 64 && L.count > 0 && tid < q.n) {
+      unsigned long long m = 0;
+      for (int u = tid; u >= 0; u = u > 0 ? L.par[u] : -1) m |= 1ull << u;
+      L.anc[tid] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kVecsPer; ++u) {
+      const int v = u * kThreads + tid;
+      node_bits |= ((L.node_bits[v >> 2] >> ((v & 3) * 8)) & 0xffu) << (8 * u);
+      bias_bits |= ((L.bias_bits[v >> 2] >> ((v & 3) * 8)) & 0xffu) << (8 * u);
+    }
+    special |= node_bits | bias_bits;
+  }
+  const int nb = bhi - blo;
+  // The processed value of special element k of vector u, in row i.
+  auto value = [&](const u32x4& dv, const u32x4& h, int u, int k, int i) {
+    float x = E::at(dv, k);
+    const int t = (v0 + u * kThreads) * kPer + k;
+    const unsigned bit = 1u << (8 * u + k);
+    if (penal) {
+      const int extra = (node_bits & bit) ? times_on_path(L, q.tree, q.n, i, t) : 0;
+      x = apply_penalties(x, word_at<DT>(h, k), extra, pen);
+    }
+    if (bias_bits & bit) {
+      if (nb <= kBiasLds) {
+        int lo = 0, hi = nb;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (L.bias_id[mid] < t) {
+            lo = mid + 1;
+          } else {
+            hi = mid;
+          }
+        }
+        if (lo < nb && L.bias_id[lo] == t) x += L.bias_value[lo];
+      } else {
+        const int j = lower_bound(R.bias_ids, blo, bhi, t);
+        if (j < bhi && R.bias_ids[j] == t) x += R.bias_values[j];
+      }
+    }
+    return x;
+  };
+
+  for (int i = i0; i < i1; ++i) {
+    const int64_t r = static_cast<int64_t>(q.row0) + i;
+    u32x4 next[kVecsPer] = {};
+    if (i + 1 < i1) load_row(rowp + a.row_bytes, next);
+    unsigned allowed = valid;
+    if (R.allow) {
+      const unsigned char* m = reinterpret_cast<const unsigned char*>(R.allow + r * R.allow_stride);
+      unsigned bits = 0;
+#pragma unroll
+      for (int u = 0; u < kVecsPer; ++u) {
+        const int v = v0 + u * kThreads;
+        if (v * kPer < a.V) {
+          const unsigned f = kPer == 8 ? m[v] : (m[v >> 1] >> ((v & 1) * 4)) & 0xfu;
+          bits |= f << (8 * u);
+        }
+      }
+      allowed &= bits;
+    }
+    const unsigned plain = allowed & ~special;
+    const unsigned hits = allowed & special;
+    if constexpr (OUT == kArgmax) {
+      float top[kVecsPer];
+      float best = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kVecsPer; ++u) {
+        const unsigned f = (plain >> (8 * u)) & 0xffu;
+        if (__all(f == kAll)) {
+          top[u] = E::vmax(d[u]);
+        } else {
+          top[u] = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            top[u] = fmaxf(top[u], (f >> k) & 1u ? E::at(d[u], k) : -INFINITY);
+        }
+        best = fmaxf(best, top[u]);
+      }
+      // The lane's special elements: (value, lowest index).
+      float hv = -INFINITY;
+      int hi = INT_MAX;
+      if (hits) {
+#pragma unroll
+        for (int u = 0; u < kVecsPer; ++u) {
+          unsigned h = (hits >> (8 * u)) & 0xffu;
+          while (h) {
+            const int k = __ffs(h) - 1;
+            h &= h - 1;
+            const float x = value(d[u], hw[u], u, k, i);
+            if (x > hv) {
+              hv = x;
+              hi = (v0 + u * kThreads) * kPer + k;
+            }
+          }
+        }
+      }
+      const float mine = fmaxf(best, hv);
+      const float wave_top = wave_max_f32(mine);
+      int idx = INT_MAX;
+      if (mine == wave_top && wave_top > -INFINITY) {
+        if (best == wave_top) {
+          // The first vector that holds it, then the first of its elements.
+          u32x4 dv = d[0];
+          unsigned f = plain;
+          int at = v0;
+#pragma unroll
+          for (int u = kVecsPer - 1; u >= 0; --u) {
+            if (top[u] == wave_top) {
+              dv = d[u];
+              f = plain >> (8 * u);
+              at = v0 + u * kThreads;
+            }
+          }
+#pragma unroll
+          for (int k = kPer - 1; k >= 0; --k)
+            if (((f >> k) & 1u) && E::at(dv, k) == wave_top) idx = at * kPer + k;
+        }
+        if (hv == wave_top) idx = min(idx, hi);
+      }
+      idx = ~wave_max_to_lane63(~idx);
+      if ((tid & 63) == 63)
+        best_s[i - i0][tid >> 6] = Partial{wave_top, idx == INT_MAX ? -1 : idx};
+    } else {
+      unsigned char* o = a.out + r * a.out_bytes;
+#pragma unroll
+      for (int u = 0; u < kVecsPer; ++u) {
+        const int v = v0 + u * kThreads;
+        float x[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          x[k] = (allowed >> (8 * u + k)) & 1u ? E::at(d[u], k) : -INFINITY;
+        unsigned h = (hits >> (8 * u)) & 0xffu;
+        while (h) {
+          const int k = __ffs(h) - 1;
+          h &= h - 1;
+          const float y = value(d[u], hw[u], u, k, i);
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) x[j] = j == k ? y : x[j];
+        }
+        store_vec<OUT, kPer>(o, v, x, v < a.nvec ? kPer : v == a.nvec ? tail : 0);
+      }
+    }
+    rowp += a.row_bytes;
+#pragma unroll
+    for (int u = 0; u < kVecsPer; ++u) d[u] = next[u];
+  }
+  if constexpr (OUT == kArgmax) {
+    __syncthreads();
+    for (int k = tid; k < i1 - i0; k += kThreads) {
+      float bv = best_s[k][0].val;
+      int bi = best_s[k][0].idx;
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) better_partial(bv, bi, best_s[k][w].val, best_s[k][w].idx);
+      a.part[(static_cast<int64_t>(b) * a.rows.rmax + i0 + k) * a.chunks + c] = Partial{bv, bi};
     }
   }
 }
@@ -158,7 +456,11 @@ RulesArgs rules_args(const RowsArgs& rows, const wf_logit_rules& rules, const vo
   a.logits = static_cast<const unsigned char*>(logits);
   a.row_bytes = row_stride * (dtype == WF_BF16 ? 2 : 4);
   a.V = V;
-  a.chunks = rules_plan(dtype, rows.B, rows.rmax, V).chunks;
+  a.nvec = V / (dtype == WF_BF16 ? 8 : 4);
+  const RulesPlan p = rules_plan(dtype, rows.B, rows.rmax, V);
+  a.chunks = p.chunks;
+  a.groups = p.groups;
+  a.group = p.group;
   return a;
 }
 
@@ -173,8 +475,16 @@ void launch_written(const RulesArgs& a, int out_dtype, dim3 grid, hipStream_t st
 
 }  // namespace
 
-RulesPlan rules_plan(int, int32_t, int32_t rmax, int32_t V) {
-  return RulesPlan{(V + kChunk - 1) / kChunk, rmax, 1};
+RulesPlan rules_plan(int dtype, int32_t B, int32_t rmax, int32_t V) {
+  const int32_t per = kChunkVecs * (dtype == WF_BF16 ? 8 : 4);
+  const int32_t chunks = V / per + (V % per != 0);
+  // As many workgroups as fill the card a few times over; beyond that, longer groups.
+  const int64_t one = static_cast<int64_t>(B) * chunks;
+  int64_t groups = one > 0 ? (kRulesBlocks + one - 1) / one : 1;
+  const int32_t least = (rmax + kMaxGroup - 1) / kMaxGroup;
+  groups = groups < least ? least : groups > rmax ? rmax : groups;
+  const int32_t group = static_cast<int32_t>((rmax + groups - 1) / groups);
+  return RulesPlan{chunks, (rmax + group - 1) / group, group};
 }
 
 hipError_t launch_process(const RowsArgs& rows, const wf_logit_rules& rules, const void* logits,
@@ -183,7 +493,7 @@ hipError_t launch_process(const RowsArgs& rows, const wf_logit_rules& rules, con
   RulesArgs a = rules_args(rows, rules, logits, dtype, V, row_stride);
   a.out = static_cast<unsigned char*>(out);
   a.out_bytes = out_stride * (out_dtype == WF_BF16 ? 2 : 4);
-  const dim3 grid(static_cast<unsigned>(rows.B) * rows.rmax * a.chunks);
+  const dim3 grid(static_cast<unsigned>(rows.B) * a.groups * a.chunks);
   if (dtype == WF_BF16) {
     launch_written<WF_BF16>(a, out_dtype, grid, stream);
   } else {
@@ -198,11 +508,11 @@ hipError_t launch_constrained(const RowsArgs& rows, const wf_logit_rules& rules,
                               int32_t* best_node, int32_t* row_argmax, hipStream_t stream) {
   RulesArgs a = rules_args(rows, rules, logits, dtype, V, row_stride);
   a.part = part;
-  const dim3 grid(static_cast<unsigned>(rows.B) * rows.rmax * a.chunks);
+  const dim3 grid(static_cast<unsigned>(rows.B) * a.groups * a.chunks);
   if (dtype == WF_BF16) {
-    hipLaunchKernelGGL((rules_kernel<WF_BF16, -1>), grid, dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((rules_kernel<WF_BF16, kArgmax>), grid, dim3(kThreads), 0, stream, a);
   } else {
-    hipLaunchKernelGGL((rules_kernel<WF_F32, -1>), grid, dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((rules_kernel<WF_F32, kArgmax>), grid, dim3(kThreads), 0, stream, a);
   }
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   const ConstrainedAccept f{rows,       part,  a.chunks,  V,

@@ -16,7 +16,8 @@ __device__ inline float apply_penalties(float x, unsigned word, int extra, const
 #pragma clang fp contract(off)
   const int count = static_cast<int>(word & 0x7fffu) + extra;
   const bool put_out = count > 0;
-  if (put_out || (word & 0x8000u)) x = x > 0.f ? x / p.repetition : x * p.repetition;
+  if (!put_out && !(word & 0x8000u)) return x;
+  x = x > 0.f ? x / p.repetition : x * p.repetition;
   const float f = p.frequency * static_cast<float>(count);
   x = x - f;
   x = x - (put_out ? p.presence : 0.f);

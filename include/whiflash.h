@@ -579,10 +579,11 @@ typedef struct wf_round_rows {
  * The processed logit of token v in row r of sequence b, in float32, each
  * operation rounded once: with h the history word, e the times v is among the
  * path's tokens, c = (h & 0x7fff) + e and seen = (h >> 15) or c > 0,
- *   x = logit;  if seen: x = x > 0 ? x / repetition : x * repetition;
- *   x = x - frequency * c;  x = x - presence * (c > 0);  x = x + bias;
- *   x = -inf if v is not allowed.
- * Without penalties the first three steps are left out.
+ *   x = logit;
+ *   if seen: x = x > 0 ? x / repetition : x * repetition;
+ *            x = x - frequency * c;  x = x - presence * (c > 0);
+ *   x = x + bias;  x = -inf if v is not allowed.
+ * Without penalties the steps for seen tokens are left out.
  */
 typedef struct wf_logit_rules {
   const uint16_t* history;
@@ -605,8 +606,8 @@ typedef struct wf_logit_rules {
  *   may be logits itself with the same dtype and stride; otherwise they must not
  *   overlap.  Rows of malformed sequences, rows that no sequence owns and the
  *   entries past V are left as they were.  bfloat16 output is rounded to nearest
- *   even.  Rows that two sequences own hold either one's values.
- * B == 0 is a no-op.  No workspace.
+ *   even.  Rows that two sequences own hold either one's values (in place: unspecified
+ * ones).  V is at most 2^30.  B == 0 is a no-op.  No workspace.
  */
 int32_t whiflash_process_logits(const void* logits, int32_t dtype, int32_t V, int64_t row_stride,
                                 const wf_round_rows* rows, const wf_logit_rules* rules, void* out,

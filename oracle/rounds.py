@@ -101,9 +101,10 @@ def process_rows(x, b, seq: Seq, rules: Rules) -> np.ndarray:
                     count[seq.token[a]] += 1
             seen = (count > 0) | (word >= 0x8000)
             with np.errstate(all="ignore"):
-                x[u] = np.where(seen, np.where(x[u] > 0, x[u] / rep, x[u] * rep), x[u])
-                x[u] = x[u] - freq * count.astype(np.float32)
-                x[u] = x[u] - np.where(count > 0, pres, np.float32(0))
+                y = np.where(x[u] > 0, x[u] / rep, x[u] * rep)
+                y = y - freq * count.astype(np.float32)
+                y = y - np.where(count > 0, pres, np.float32(0))
+                x[u] = np.where(seen, y, x[u])
     if rules.bias is not None:
         offsets, ids, values = rules.bias
         lo = min(max(int(offsets[b]), 0), len(ids))
