@@ -15,6 +15,7 @@ constexpr int kVecsPer = 4;                       // 16-byte vectors of a row pe
 constexpr int kChunkVecs = kVecsPer * kThreads;   // vectors of a row per workgroup
 constexpr int kBiasLds = 256;                     // biases of a chunk that are kept in LDS
 constexpr int kMaxGroup = 64;                     // rows per workgroup
+constexpr int kListMax = 256;                     // special elements of a wave that are listed
 constexpr int kArgmax = -1;
 constexpr int64_t kRulesBlocks = 8192;            // workgroups of a large launch
 
@@ -32,9 +33,9 @@ struct RulesArgs {
 // A round's drafted tokens that lie in one chunk, and the paths of its rows.
 struct PathLds {
   int tok[kMaxSeqRows];                // target token of node u, -1 for none
-  int par[kMaxSeqRows];                // parent of node u, -1 where its path ends
+  int16_t par[kMaxSeqRows];            // parent of node u, -1 where its path ends
   unsigned long long anc[64];          // ancestors-or-self of node u, trees of up to 64
-  int node[kMaxSeqRows];               // nodes whose token lies in the chunk, any order
+  int16_t node[kMaxSeqRows];           // nodes whose token lies in the chunk, any order
   int count;
   unsigned node_bits[kChunkVecs / 4];  // one byte a vector: elements that some node drafted
   unsigned bias_bits[kChunkVecs / 4];  // ... and that have a bias
@@ -47,6 +48,27 @@ template <int DT>
 __device__ inline unsigned word_at(const u32x4& h, int k) {
   const unsigned w = k < 2 ? h.x : k < 4 ? h.y : k < 6 ? h.z : h.w;
   return (w >> ((k & 1) * 16)) & 0xffffu;
+}
+
+// Orders a wave's LDS accesses: what a lane wrote before, every lane reads after.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <typename T>
+__device__ inline T read_lane(T x, int lane) {
+  return static_cast<T>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
+}
+
+// Equal for equal float32 values (-0 and +0 too).
+__device__ inline unsigned float_key(unsigned bits) { return bits == 0x80000000u ? 0u : bits; }
+
+// x if bit k of f is set, else -inf.
+__device__ inline float masked(float x, unsigned f, int k) {
+  const unsigned m = static_cast<unsigned>(static_cast<int>(f << (31 - k)) >> 31);
+  return __uint_as_float((__float_as_uint(x) & m) | (~m & 0xff800000u));
 }
 
 // How often token t is among the path tokens of row i.
@@ -127,35 +149,46 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
   constexpr unsigned kAll = (1u << kPer) - 1u;
   __shared__ PathLds L;
   __shared__ Partial best_s[OUT == kArgmax ? kMaxGroup : 1][kWaves];
+  __shared__ u32x4 stage_s[kWaves][OUT == kArgmax ? kVecsPer * 64 : 1];
+  __shared__ unsigned list_s[kWaves][OUT == kArgmax ? kListMax : 1];
   const int tid = threadIdx.x;
   const int c = blockIdx.x % a.chunks;
   const int bg = blockIdx.x / a.chunks;
   const int b = bg / a.groups, g = bg - b * a.groups;
   const SeqRows q = seq_rows(a.rows, b);
-  const int i0 = g * a.group, i1 = min(i0 + a.group, q.n);
-  if (i0 >= i1) return;
+  // Of a sequence shorter than the longest, as few groups as hold it, evenly.
+  const int used = (q.n + a.group - 1) / a.group;
+  if (g >= used) return;
+  const int i0 = g * q.n / used, i1 = (g + 1) * q.n / used;
   const wf_logit_rules& R = a.rules;
   const int v0 = c * kChunkVecs + tid;  // the thread's vectors: v0 + u * kThreads
   const int tail = a.V - a.nvec * kPer;
 
   const unsigned char* rowp = a.logits + (static_cast<int64_t>(q.row0) + i0) * a.row_bytes;
-  auto load_row = [&](const unsigned char* p, u32x4* d) {
+  // Lanes past the row's whole vectors read its last one and mask it.
+  const bool has_tail = tail && a.nvec / kChunkVecs == c;
+  unsigned off[kVecsPer];
 #pragma unroll
-    for (int u = 0; u < kVecsPer; ++u) {
-      const int v = v0 + u * kThreads;
-      if (v < a.nvec) {
-        d[u] = load16(reinterpret_cast<const u32x4*>(p) + v);
-      } else if (v == a.nvec && tail) {
+  for (int u = 0; u < kVecsPer; ++u) off[u] = 16u * max(min(v0 + u * kThreads, a.nvec - 1), 0);
+  auto load_row = [&](const unsigned char* p, u32x4* d) {
+    if (a.nvec > 0) {
+#pragma unroll
+      for (int u = 0; u < kVecsPer; ++u) d[u] = load16(reinterpret_cast<const u32x4*>(p + off[u]));
+    }
+    if (has_tail) {
+#pragma unroll
+      for (int u = 0; u < kVecsPer; ++u) {
+        if (v0 + u * kThreads != a.nvec) continue;
         // The entries past the last whole vector, one by one.
         unsigned w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
           if (k < tail) {
             if constexpr (DT == WF_BF16) {
-              const unsigned x = reinterpret_cast<const uint16_t*>(p)[v * kPer + k];
+              const unsigned x = reinterpret_cast<const uint16_t*>(p)[a.nvec * kPer + k];
               w[k >> 1] |= x << ((k & 1) * 16);
             } else {
-              w[k] = reinterpret_cast<const unsigned*>(p)[v * kPer + k];
+              w[k] = reinterpret_cast<const unsigned*>(p)[a.nvec * kPer + k];
             }
           }
         }
@@ -163,7 +196,19 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
       }
     }
   };
+  // The byte of a row's mask that holds each vector's bits (a row has ceil(V / 8) at least).
+  auto load_mask = [&](int64_t r, unsigned* m) {
+    if (!R.allow) return;
+    const unsigned char* p = reinterpret_cast<const unsigned char*>(R.allow + r * R.allow_stride);
+#pragma unroll
+    for (int u = 0; u < kVecsPer; ++u) {
+      const int v = min(v0 + u * kThreads, (a.V - 1) / kPer);
+      m[u] = p[kPer == 8 ? v : v >> 1];
+    }
+  };
   u32x4 d[kVecsPer] = {};
+  unsigned mask[kVecsPer] = {};
+  load_mask(static_cast<int64_t>(q.row0) + i0, mask);
   load_row(rowp, d);
 
   // What the chunk's elements need beyond a mask.
@@ -222,10 +267,10 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
       for (int u = 1 + tid; u < q.n; u += kThreads) {
         const int t = node_token(a.rows, b, q.tree, u, a.V);
         L.tok[u] = t;
-        if (q.tree) L.par[u] = node_parent(a.rows, b, true, u);
+        if (q.tree) L.par[u] = static_cast<int16_t>(node_parent(a.rows, b, true, u));
         const int v = t / kPer - c * kChunkVecs;
         if (t >= 0 && v >= 0 && v < kChunkVecs) {
-          L.node[atomicAdd(&L.count, 1)] = u;
+          L.node[atomicAdd(&L.count, 1)] = static_cast<int16_t>(u);
           atomicOr(&L.node_bits[v >> 2], 1u << ((v & 3) * 8 + t % kPer));
         }
       }
@@ -257,16 +302,14 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
     special |= node_bits | bias_bits;
   }
   const int nb = bhi - blo;
-  // The processed value of special element k of vector u, in row i.
-  auto value = [&](const u32x4& dv, const u32x4& h, int u, int k, int i) {
-    float x = E::at(dv, k);
-    const int t = (v0 + u * kThreads) * kPer + k;
-    const unsigned bit = 1u << (8 * u + k);
+  // The processed value of a special element: logit x of token t with history word
+  // `word`, in row i.
+  auto value = [&](float x, unsigned word, bool node, bool biased, int t, int i) {
     if (penal) {
-      const int extra = (node_bits & bit) ? times_on_path(L, q.tree, q.n, i, t) : 0;
-      x = apply_penalties(x, word_at<DT>(h, k), extra, pen);
+      const int extra = node ? times_on_path(L, q.tree, q.n, i, t) : 0;
+      x = apply_penalties(x, word, extra, pen);
     }
-    if (bias_bits & bit) {
+    if (biased) {
       if (nb <= kBiasLds) {
         int lo = 0, hi = nb;
         while (lo < hi) {
@@ -285,22 +328,55 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
     }
     return x;
   };
+  // The same for element k of the lane's own vector u.
+  auto own_value = [&](const u32x4& dv, const u32x4& h, int u, int k, int i) {
+    const unsigned bit = 1u << (8 * u + k);
+    return value(E::at(dv, k), word_at<DT>(h, k), node_bits & bit, bias_bits & bit,
+                 (v0 + u * kThreads) * kPer + k, i);
+  };
+  // Up to kListMax special elements of a wave are listed, so that its lanes share them
+  // evenly: bits 0-15 the history word, 16-26 the place in the wave's vectors, 27 and 28
+  // whether some node drafted it and whether it has a bias.
+  const int lane = tid & 63, wave = tid >> 6;
+  int listed = 0;
+  if constexpr (OUT == kArgmax) {
+    int before = __popc(special);
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(before, off);
+      before += lane >= off ? o : 0;
+    }
+    listed = __shfl(before, 63);
+    if (listed <= kListMax) {
+      unsigned* p = list_s[wave] + before - __popc(special);
+#pragma unroll
+      for (int u = 0; u < kVecsPer; ++u) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const unsigned bit = 1u << (8 * u + k);
+          if (special & bit)
+            *p++ = word_at<DT>(hw[u], k) | ((u * 64 + lane) * kPer + k) << 16 |
+                   ((node_bits & bit) ? 1u << 27 : 0u) | ((bias_bits & bit) ? 1u << 28 : 0u);
+        }
+      }
+    }
+  }
 
   for (int i = i0; i < i1; ++i) {
     const int64_t r = static_cast<int64_t>(q.row0) + i;
-    u32x4 next[kVecsPer] = {};
-    if (i + 1 < i1) load_row(rowp + a.row_bytes, next);
+    // The next row's mask and vectors are on their way while this one is worked on.
+    u32x4 next[kVecsPer];
+    unsigned next_mask[kVecsPer];
+    if (i + 1 < i1) {
+      load_mask(r + 1, next_mask);
+      load_row(rowp + a.row_bytes, next);
+    }
     unsigned allowed = valid;
     if (R.allow) {
-      const unsigned char* m = reinterpret_cast<const unsigned char*>(R.allow + r * R.allow_stride);
       unsigned bits = 0;
 #pragma unroll
       for (int u = 0; u < kVecsPer; ++u) {
-        const int v = v0 + u * kThreads;
-        if (v * kPer < a.V) {
-          const unsigned f = kPer == 8 ? m[v] : (m[v >> 1] >> ((v & 1) * 4)) & 0xfu;
-          bits |= f << (8 * u);
-        }
+        const unsigned f = kPer == 8 ? mask[u] : mask[u] >> ((tid & 1) * 4) & 0xfu;
+        bits |= f << (8 * u);
       }
       allowed &= bits;
     }
@@ -318,54 +394,91 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
           top[u] = -INFINITY;
 #pragma unroll
           for (int k = 0; k < kPer; ++k)
-            top[u] = fmaxf(top[u], (f >> k) & 1u ? E::at(d[u], k) : -INFINITY);
+            top[u] = fmaxf(top[u], masked(E::at(d[u], k), f, k));
         }
         best = fmaxf(best, top[u]);
       }
       // The lane's special elements: (value, lowest index).
       float hv = -INFINITY;
       int hi = INT_MAX;
-      if (hits) {
+      if (listed > 0) {
+        // The wave's vectors through LDS, read back by whichever lane has the element.
+#pragma unroll
+        for (int u = 0; u < kVecsPer; ++u) stage_s[wave][u * 64 + lane] = d[u];
+        wave_sync();
+        const unsigned char* stage = reinterpret_cast<const unsigned char*>(stage_s[wave]);
+        // Listed: lane j takes entries j, j + 64, ...; else each lane its own elements.
+        const bool list = listed <= kListMax;
+        unsigned h = hits;
+        for (int j0 = 0; list ? j0 < listed : __any(h != 0); j0 += 64) {
+          int owner = lane, u = 0, k = 0;
+          unsigned word = 0;
+          bool node = false, biased = false, on;
+          if (list) {
+            on = j0 + lane < listed;
+            const unsigned e = list_s[wave][on ? j0 + lane : 0];
+            const int at = (e >> 16) & 0x7ffu;
+            owner = (at / kPer) & 63;
+            u = at / (64 * kPer);
+            k = at % kPer;
+            const unsigned theirs = __shfl(allowed, owner);
+            on = on && ((theirs >> (8 * u + k)) & 1u);
+            word = e & 0xffffu;
+            node = e >> 27 & 1u;
+            biased = e >> 28 & 1u;
+          } else {
+            on = h != 0;
+            const int bit = on ? __ffs(h) - 1 : 0;
+            h &= h - 1;
+            u = bit >> 3;
+            k = bit & 7;
+            node = node_bits >> bit & 1u;
+            biased = bias_bits >> bit & 1u;
+          }
+          if (on) {
+            const int t = (c * kChunkVecs + u * kThreads + wave * 64 + owner) * kPer + k;
+            if (!list && hist) word = hist[t];
+            const float x = value(E::scalar(stage, (u * 64 + owner) * kPer + k), word, node, biased,
+                                  t, i);
+            if (x > hv || (x == hv && t < hi)) {
+              hv = x;
+              hi = t;
+            }
+          }
+        }
+        wave_sync();
+      }
+      const float wave_top = wave_max_f32(fmaxf(best, hv));
+      // The first plain element that holds it: its vector and lane by ballots, then the
+      // element in scalar registers.  (Places ascend with u, then the lane, then k.)
+      int idx = INT_MAX;
+      if (wave_top > -INFINITY) {
 #pragma unroll
         for (int u = 0; u < kVecsPer; ++u) {
-          unsigned h = (hits >> (8 * u)) & 0xffu;
-          while (h) {
-            const int k = __ffs(h) - 1;
-            h &= h - 1;
-            const float x = value(d[u], hw[u], u, k, i);
-            if (x > hv) {
-              hv = x;
-              hi = (v0 + u * kThreads) * kPer + k;
+          if (idx == INT_MAX) {
+            const unsigned long long who = __ballot(top[u] == wave_top);
+            if (who) {
+              const int from = __builtin_ctzll(who);
+              const unsigned f = read_lane(plain, from) >> (8 * u);
+              const unsigned w[4] = {read_lane(d[u].x, from), read_lane(d[u].y, from),
+                                     read_lane(d[u].z, from), read_lane(d[u].w, from)};
+              const unsigned want = float_key(__float_as_uint(wave_top));
+              int k = 0;
+#pragma unroll
+              for (int j = kPer - 1; j >= 0; --j) {
+                const unsigned x = kPer == 4 ? w[j] : j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16;
+                if ((f >> j & 1u) && float_key(x) == want) k = j;
+              }
+              idx = (c * kChunkVecs + u * kThreads + wave * 64 + from) * kPer + k;
             }
           }
         }
-      }
-      const float mine = fmaxf(best, hv);
-      const float wave_top = wave_max_f32(mine);
-      int idx = INT_MAX;
-      if (mine == wave_top && wave_top > -INFINITY) {
-        if (best == wave_top) {
-          // The first vector that holds it, then the first of its elements.
-          u32x4 dv = d[0];
-          unsigned f = plain;
-          int at = v0;
-#pragma unroll
-          for (int u = kVecsPer - 1; u >= 0; --u) {
-            if (top[u] == wave_top) {
-              dv = d[u];
-              f = plain >> (8 * u);
-              at = v0 + u * kThreads;
-            }
-          }
-#pragma unroll
-          for (int k = kPer - 1; k >= 0; --k)
-            if (((f >> k) & 1u) && E::at(dv, k) == wave_top) idx = at * kPer + k;
+        if (__any(hv == wave_top)) {
+          const int mine = hv == wave_top ? hi : INT_MAX;
+          idx = min(idx, read_lane(~wave_max_to_lane63(~mine), 63));
         }
-        if (hv == wave_top) idx = min(idx, hi);
       }
-      idx = ~wave_max_to_lane63(~idx);
-      if ((tid & 63) == 63)
-        best_s[i - i0][tid >> 6] = Partial{wave_top, idx == INT_MAX ? -1 : idx};
+      if (lane == 0) best_s[i - i0][wave] = Partial{wave_top, idx == INT_MAX ? -1 : idx};
     } else {
       unsigned char* o = a.out + r * a.out_bytes;
 #pragma unroll
@@ -379,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
         while (h) {
           const int k = __ffs(h) - 1;
           h &= h - 1;
-          const float y = value(d[u], hw[u], u, k, i);
+          const float y = own_value(d[u], hw[u], u, k, i);
 #pragma unroll
           for (int j = 0; j < kPer; ++j) x[j] = j == k ? y : x[j];
         }
@@ -388,7 +501,10 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
     }
     rowp += a.row_bytes;
 #pragma unroll
-    for (int u = 0; u < kVecsPer; ++u) d[u] = next[u];
+    for (int u = 0; u < kVecsPer; ++u) {
+      d[u] = next[u];
+      mask[u] = next_mask[u];
+    }
   }
   if constexpr (OUT == kArgmax) {
     __syncthreads();
@@ -482,7 +598,8 @@ RulesPlan rules_plan(int dtype, int32_t B, int32_t rmax, int32_t V) {
   const int64_t one = static_cast<int64_t>(B) * chunks;
   int64_t groups = one > 0 ? (kRulesBlocks + one - 1) / one : 1;
   const int32_t least = (rmax + kMaxGroup - 1) / kMaxGroup;
-  groups = groups < least ? least : groups > rmax ? rmax : groups;
+  groups = groups > rmax ? rmax : groups;
+  groups = groups < least ? least : groups;
   const int32_t group = static_cast<int32_t>((rmax + groups - 1) / groups);
   return RulesPlan{chunks, (rmax + group - 1) / group, group};
 }
