@@ -34,7 +34,7 @@ struct RulesArgs {
 struct PathLds {
   int tok[kMaxSeqRows];                // target token of node u, -1 for none
   int16_t par[kMaxSeqRows];            // parent of node u, -1 where its path ends
-  unsigned long long anc[64];          // ancestors-or-self of node u, trees of up to 64
+  unsigned long long rows[64];         // rows that have node u on their path (up to 64 rows)
   int16_t node[kMaxSeqRows];           // nodes whose token lies in the chunk, any order
   int count;
   unsigned node_bits[kChunkVecs / 4];  // one byte a vector: elements that some node drafted
@@ -78,11 +78,9 @@ __device__ inline int times_on_path(const PathLds& L, bool tree, int n, int i, i
     for (int u = i; u > 0; u = L.par[u]) c += L.tok[u] == t;
     return c;
   }
-  const unsigned long long path =
-      !tree ? 0ull : L.anc[i];
   for (int j = 0; j < L.count; ++j) {
     const int u = L.node[j];
-    const bool on = tree ? (path >> u) & 1ull : u <= i;
+    const bool on = n <= 64 ? (L.rows[u] >> i) & 1ull : u <= i;
     c += on && L.tok[u] == t;
   }
   return c;
@@ -287,10 +285,11 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
       }
     }
     __syncthreads();
-    if (paths && q.tree && q.n <= 64 && L.count > 0 && tid < q.n) {
-      unsigned long long m = 0;
-      for (int u = tid; u >= 0; u = u > 0 ? L.par[u] : -1) m |= 1ull << u;
-      L.anc[tid] = m;
+    if (paths && q.n <= 64 && L.count > 0) {
+      if (tid < q.n) L.rows[tid] = q.tree ? 0ull : ~0ull << tid;
+      __syncthreads();
+      if (q.tree && tid < q.n)
+        for (int u = tid; u > 0; u = L.par[u]) atomicOr(&L.rows[u], 1ull << tid);
     }
     __syncthreads();
 #pragma unroll
@@ -302,6 +301,22 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
     special |= node_bits | bias_bits;
   }
   const int nb = bhi - blo;
+  auto bias_of = [&](int t) {
+    if (nb <= kBiasLds) {
+      int lo = 0, hi = nb;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (L.bias_id[mid] < t) {
+          lo = mid + 1;
+        } else {
+          hi = mid;
+        }
+      }
+      return lo < nb && L.bias_id[lo] == t ? L.bias_value[lo] : 0.f;
+    }
+    const int j = lower_bound(R.bias_ids, blo, bhi, t);
+    return j < bhi && R.bias_ids[j] == t ? R.bias_values[j] : 0.f;
+  };
   // The processed value of a special element: logit x of token t with history word
   // `word`, in row i.
   auto value = [&](float x, unsigned word, bool node, bool biased, int t, int i) {
@@ -309,23 +324,7 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
       const int extra = node ? times_on_path(L, q.tree, q.n, i, t) : 0;
       x = apply_penalties(x, word, extra, pen);
     }
-    if (biased) {
-      if (nb <= kBiasLds) {
-        int lo = 0, hi = nb;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (L.bias_id[mid] < t) {
-            lo = mid + 1;
-          } else {
-            hi = mid;
-          }
-        }
-        if (lo < nb && L.bias_id[lo] == t) x += L.bias_value[lo];
-      } else {
-        const int j = lower_bound(R.bias_ids, blo, bhi, t);
-        if (j < bhi && R.bias_ids[j] == t) x += R.bias_values[j];
-      }
-    }
+    if (biased) x += bias_of(t);
     return x;
   };
   // The same for element k of the lane's own vector u.
@@ -357,6 +356,38 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
             *p++ = word_at<DT>(hw[u], k) | ((u * 64 + lane) * kPer + k) << 16 |
                    ((node_bits & bit) ? 1u << 27 : 0u) | ((bias_bits & bit) ? 1u << 28 : 0u);
         }
+      }
+    }
+  }
+
+  // The lane's first listed element, decoded once for all rows: its place and token, its
+  // bias, and the rows that have its node on their path (one node drafted it, of up to
+  // 64 rows; else `ask` has them looked up in each row).
+  int first_at = 0, first_t = 0;
+  unsigned first_word = 0;
+  float first_bias = 0.f;
+  unsigned long long first_rows = 0;
+  bool first = false, first_biased = false, ask = false;
+  if constexpr (OUT == kArgmax) {
+    wave_sync();
+    first = listed <= kListMax && lane < listed;
+    if (first) {
+      const unsigned e = list_s[wave][lane];
+      first_at = (e >> 16) & 0x7ffu;
+      first_word = e & 0xffffu;
+      first_t = (c * kChunkVecs + first_at / (64 * kPer) * kThreads + wave * 64) * kPer +
+                first_at % (64 * kPer);
+      first_biased = e >> 28 & 1u;
+      if (first_biased) first_bias = bias_of(first_t);
+      if (e >> 27 & 1u) {
+        int times = 0;
+        for (int j = 0; j < L.count; ++j) {
+          const int u = L.node[j];
+          if (L.tok[u] != first_t) continue;
+          ++times;
+          if (q.n <= 64) first_rows = L.rows[u];
+        }
+        ask = times > 1 || q.n > 64;
       }
     }
   }
@@ -407,10 +438,24 @@ __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
         for (int u = 0; u < kVecsPer; ++u) stage_s[wave][u * 64 + lane] = d[u];
         wave_sync();
         const unsigned char* stage = reinterpret_cast<const unsigned char*>(stage_s[wave]);
-        // Listed: lane j takes entries j, j + 64, ...; else each lane its own elements.
         const bool list = listed <= kListMax;
+        if (list) {
+          const unsigned theirs = __shfl(allowed, first_at / kPer & 63);
+          if (first && (theirs >> (first_at / (64 * kPer) * 8 + first_at % kPer) & 1u)) {
+            float x = E::scalar(stage, first_at);
+            if (penal) {
+              const int extra = ask ? times_on_path(L, q.tree, q.n, i, first_t)
+                                    : static_cast<int>(first_rows >> (i & 63)) & 1;
+              x = apply_penalties(x, first_word, extra, pen);
+            }
+            if (first_biased) x += first_bias;
+            hv = fmaxf(hv, x);  // (a NaN never wins)
+            hi = first_t;
+          }
+        }
+        // The others of a list, 64 at a time; without one each lane takes its own elements.
         unsigned h = hits;
-        for (int j0 = 0; list ? j0 < listed : __any(h != 0); j0 += 64) {
+        for (int j0 = 64; list ? j0 < listed : __any(h != 0); j0 += 64) {
           int owner = lane, u = 0, k = 0;
           unsigned word = 0;
           bool node = false, biased = false, on;
