@@ -287,6 +287,9 @@ int32_t whiflash_attend(const void* q, int64_t q_row_stride, int32_t q_heads,
   if (rows->B == 0 || total == 0) return WF_OK;
   if (!out) return WF_ERR_NULL;
   if (!aligned16(out)) return WF_ERR_ALIGN;
+  if (wf::attend_blocks(*cache, a, q_heads, max_context) > kMaxBlocks ||
+      static_cast<int64_t>(a.B) * a.rmax * q_heads > kMaxBlocks * 4)
+    return WF_ERR_SHAPE;
   if ((s = check_workspace(workspace, workspace_bytes,
                            whiflash_attend_workspace_bytes(cache, rows, q_heads, max_context))) !=
       WF_OK)

@@ -1,4 +1,16 @@
-// Attention of a round's rows over the paged cache.
+// Attention of a round's rows over the paged cache (whiflash_attend).
+//
+// Per sequence and key-value head, the M = rows x (q_heads / heads) queries that share
+// its keys form tiles of 16, and a wave walks its share of the positions in tiles of
+// 16 or 32, keeping each query's running maximum m, sum l and output O in registers:
+//   S^T = K Q^T           (MFMA; a lane holds one query's scores of four positions)
+//   p = 2^(s - m), l += p (the softmax in base 2, one pass)
+//   O^T += V^T P^T        (MFMA)
+// The transposed products keep everything in registers.  A lane's scores all belong to
+// query lane % 16, so m, l and the rescaling of O are one value a lane, and the scores'
+// layout is the second product's operand layout if V's positions take the same order.
+// K is loaded from its page in operand layout; V in rows, and transposed by byte
+// permutes (bfloat16) or used as it lies (float32).
 #include <math.h>
 
 #include "elem.h"
@@ -7,9 +19,16 @@
 namespace wf {
 namespace {
 
-constexpr int kKeys = 64;      // positions a wave takes at once, one per lane
-constexpr int kMaxDim = 128;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLowest = -3.0e38f;  // a maximum of nothing: finite, so that no inf - inf arises
+// O is rescaled only when a maximum grows by more than this (base 2): the weights then
+// stay below 2^8, and most tiles need no rescaling.
+constexpr float kSlack = 8.f;
+constexpr int kMinSpan = 128;
+constexpr int kTargetBlocks = 2048;
 
 struct AttendArgs {
   RowsArgs rows;
@@ -18,126 +37,597 @@ struct AttendArgs {
   int q_heads, group;
   const unsigned char* k;  // the layer
   const unsigned char* v;
-  int64_t page_elems;
+  int64_t page_bytes;
   int pages, heads, page_log, seqs, max_pages;
   const int32_t* table;
   const int32_t* context;
   const int32_t* seq;
   int max_context;
-  float scale_log2;
+  float scale_log2;  // |scale| log2(e)
+  unsigned flip;     // the sign bits to flip in q (scale < 0)
   unsigned char* out;
+  int splits, span, mgroups;
+  int64_t units;     // sequences x heads x splits
+  float* part_o;     // [splits][rows x q_heads][D]
+  float2* part_ml;   // [splits][rows x q_heads]
+  int64_t row_heads;
 };
 
-// One workgroup per (sequence, row, query head); each wave takes every fourth tile of
-// 64 positions, one per lane, and the waves' running maxima, sums and outputs join at
-// the end.
+// One sequence's part of a launch: its rows, cache sequence and committed length
+// (-1: its rows get zeros).
+struct SeqCall {
+  SeqRows q;
+  int s, c;
+};
+
+__device__ inline SeqCall seq_call(const AttendArgs& a, int b) {
+  SeqCall x;
+  x.q = seq_rows(a.rows, b);
+  x.s = slot_of(a.seq, b, a.seqs);
+  x.c = x.s < 0 ? -1 : a.context[x.s];
+  if (x.c > a.max_context ||
+      static_cast<int64_t>(x.c) + x.q.n > static_cast<int64_t>(a.max_pages) << a.page_log)
+    x.c = -1;
+  if (x.c < 0) x.c = -1;
+  return x;
+}
+
+// Max over the four 16-lane rows of a wave, for each of their 16 places.
+__device__ inline float rows_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ inline float rows_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Two float32 values as bfloat16, rounded to nearest even.
+__device__ inline unsigned pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 r = __builtin_convertvector((f32x2{lo, hi}), bf16x2);
+  return __builtin_bit_cast(unsigned, r);
+}
+
+// What differs between the types: operand fragments, the two products and their tiles.
+// Lane l is place n = l % 16 of group g = l / 16.  kSub positions sub-tiles of 16 make
+// a tile; a lane's scores of sub-tile t are positions 16 t + 4 g + i, i < 4.  The
+// output tile j, element i is dimension dim(g, i, j) of query n.
 template <int DT, int D>
-__global__ __launch_bounds__(kThreads) void attend_kernel(AttendArgs a) {
-  using E = Elem<DT>;
-  constexpr int kVecs = D / E::kPerVec;
-  constexpr int kPer = D / 64;
-  __shared__ float q_s[D];
-  __shared__ float p_s[kWaves][kKeys];
-  __shared__ int64_t at_s[kWaves][kKeys];
-  __shared__ unsigned char see_s[kMaxSeqRows];
-  __shared__ float m_s[kWaves], l_s[kWaves], o_s[kWaves][D];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.y;
-  const int b = blockIdx.x / a.rows.rmax, i = blockIdx.x - b * a.rows.rmax;
-  const SeqRows q = seq_rows(a.rows, b);
-  if (i >= q.n) return;
-  const int64_t r = static_cast<int64_t>(q.row0) + i;
-  const int s = slot_of(a.seq, b, a.seqs);
-  int c = s < 0 ? -1 : a.context[s];
-  if (c > a.max_context || static_cast<int64_t>(c) + q.n > static_cast<int64_t>(a.max_pages) << a.page_log)
-    c = -1;
-  for (int u = tid; u < q.n; u += kThreads) see_s[u] = 0;
-  if (tid < D) q_s[tid] = E::scalar(a.q + r * a.q_bytes, h * D + tid) * a.scale_log2;
-  __syncthreads();
-  if (tid == 0)
-    for (int u = i; u >= 0; u = u > 0 ? node_parent(a.rows, b, q.tree, u) : -1) see_s[u] = 1;
-  __syncthreads();
-  const int64_t head = static_cast<int64_t>(h / a.group) * D << a.page_log;
-  const int end = c < 0 ? 0 : c + q.n;
-  float m = -INFINITY, l = 0.f, o[kPer] = {};
-  for (int j0 = wave * kKeys; j0 < end; j0 += kWaves * kKeys) {
-    const int j = j0 + lane;
-    float x = -INFINITY;
-    int64_t at = -1;
-    if (j < end && (j < c || see_s[j - c])) {
-      const int p = a.table[static_cast<int64_t>(s) * a.max_pages + (j >> a.page_log)];
-      if (p >= 0 && p < a.pages) {
-        at = p * a.page_elems + head + static_cast<int64_t>(j & ((1 << a.page_log) - 1)) * D;
-        const u32x4* kp = reinterpret_cast<const u32x4*>(a.k + at * E::kBytes);
-        x = 0.f;
-        for (int e = 0; e < kVecs; ++e) {
-          const u32x4 d = kp[e];
+struct Ops;
+
+template <int D>
+struct Ops<WF_BF16, D> {
+  static constexpr int kSub = 2;
+  static constexpr int kFrags = D / 32;  // 16-byte operand vectors of a query or key
+  static constexpr int kOut = D / 16;    // output tiles
+  static constexpr int kBytes = 2;
+  static constexpr int kVecV = D / 64;   // 8-byte pieces of a lane's share of a row of V
+  struct V {
+    unsigned w[2 * 4][kVecV * 2];        // [position][dimension pairs]
+  };
+
+  // Byte offset of fragment f of place n, group g within a row.
+  __device__ static inline int frag_at(int g, int f) { return f * 64 + g * 16; }
+  __device__ static inline f32x4 scores(const u32x4* k, const u32x4* q) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = 0; t < E::kPerVec; ++t) x += q_s[e * E::kPerVec + t] * E::at(d, t);
+    for (int f = 0; f < kFrags; ++f)
+      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[f]),
+                                                  __builtin_bit_cast(bf16x8, q[f]), s, 0, 0, 0);
+    return s;
+  }
+  // Rows 4 g + i of sub-tile t, dimensions [n D / 16, (n + 1) D / 16).
+  __device__ static inline void load_v(V& v, int t, const unsigned char* p, unsigned lane_off) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (D == 128) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(p + lane_off + i * D * 2);
+        v.w[4 * t + i][0] = x.x;
+        v.w[4 * t + i][1] = x.y;
+        v.w[4 * t + i][2] = x.z;
+        v.w[4 * t + i][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + lane_off + i * D * 2);
+        v.w[4 * t + i][0] = x.x;
+        v.w[4 * t + i][1] = x.y;
+      }
+    }
+  }
+  __device__ static inline unsigned v_lane(int n, int g) { return (4 * g * D + n * (D / 16)) * 2; }
+  __device__ static inline void zero_v(V& v, int t, int i) {
+#pragma unroll
+    for (int x = 0; x < kVecV * 2; ++x) v.w[4 * t + i][x] = 0;
+  }
+  // o += V^T P^T for MT query tiles; p[m][t][i] the weights.
+  template <int MT>
+  __device__ static inline void outputs(f32x4 (*o)[kOut], const V& v, const float (*p)[kSub][4]) {
+    bf16x8 pb[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const u32x4 x = {pack_bf16(p[m][0][0], p[m][0][1]), pack_bf16(p[m][0][2], p[m][0][3]),
+                       pack_bf16(p[m][1][0], p[m][1][1]), pack_bf16(p[m][1][2], p[m][1][3])};
+      pb[m] = __builtin_bit_cast(bf16x8, x);
+    }
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      // Element j of each position's dimensions, two positions a word.
+      u32x4 a;
+      unsigned w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        w[x] = __builtin_amdgcn_perm(v.w[2 * x + 1][j >> 1], v.w[2 * x][j >> 1],
+                                     (j & 1) ? 0x07060302u : 0x05040100u);
+      a = u32x4{w[0], w[1], w[2], w[3]};
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        o[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), pb[m],
+                                                          o[m][j], 0, 0, 0);
+    }
+  }
+  __device__ static inline u32x4 flip_sign(u32x4 x, unsigned bits) { return x ^ bits; }
+  static constexpr unsigned kFlip = 0x80008000u;
+  // Element i of the output tiles holds dimensions (4 g + i) kOut + [0, kOut).
+  __device__ static inline int out_at(int g, int i) { return (4 * g + i) * kOut; }
+};
+
+template <int D>
+struct Ops<WF_F32, D> {
+  static constexpr int kSub = 1;
+  static constexpr int kFrags = D / 16;
+  static constexpr int kOut = D / 16;
+  static constexpr int kBytes = 4;
+  struct V {
+    f32x4 w[4][D / 64];
+  };
+  __device__ static inline int frag_at(int g, int f) { return f * 64 + g * 16; }
+  __device__ static inline f32x4 scores(const u32x4* k, const u32x4* q) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+      const f32x4 kf = __builtin_bit_cast(f32x4, k[f]), qf = __builtin_bit_cast(f32x4, q[f]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[e], qf[e], s, 0, 0, 0);
+    }
+    return s;
+  }
+  // Rows 4 g + i, dimensions 64 h + 4 n + [0, 4).
+  __device__ static inline void load_v(V& v, int, const unsigned char* p, unsigned lane_off) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        v.w[i][h] = *reinterpret_cast<const f32x4*>(p + lane_off + i * D * 4 + h * 256);
+  }
+  __device__ static inline unsigned v_lane(int n, int g) { return (4 * g * D + n * 4) * 4; }
+  __device__ static inline void zero_v(V& v, int, int i) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) v.w[i][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  template <int MT>
+  __device__ static inline void outputs(f32x4 (*o)[kOut], const V& v, const float (*p)[kSub][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            o[m][4 * h + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.w[i][h][e], p[m][0][i],
+                                                                   o[m][4 * h + e], 0, 0, 0);
+  }
+  __device__ static inline u32x4 flip_sign(u32x4 x, unsigned bits) { return x ^ bits; }
+  static constexpr unsigned kFlip = 0x80000000u;
+};
+
+// Writes a lane's outputs of one query tile (element i of every output tile) scaled by
+// `f`: to out in the call's type, or float32.
+template <int DT, int D>
+__device__ inline void store_query(unsigned char* out, const f32x4* o, int g, float f) {
+  constexpr int kOut = Ops<DT, D>::kOut;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == WF_BF16) {
+      unsigned w[kOut / 2];
+#pragma unroll
+      for (int j = 0; j < kOut / 2; ++j) w[j] = pack_bf16(o[2 * j][i] * f, o[2 * j + 1][i] * f);
+      unsigned char* p = out + (4 * g + i) * kOut * 2;
+      if constexpr (kOut == 8) {
+        *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        *reinterpret_cast<f32x4*>(out + (64 * h + (4 * g + i) * 4) * 4) =
+            f32x4{o[4 * h][i] * f, o[4 * h + 1][i] * f, o[4 * h + 2][i] * f, o[4 * h + 3][i] * f};
+    }
+  }
+}
+
+// ... the partial output, float32 in the order of the dimensions.
+template <int DT, int D>
+__device__ inline void store_partial(float* out, const f32x4* o, int g) {
+  constexpr int kOut = Ops<DT, D>::kOut;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == WF_BF16) {
+#pragma unroll
+      for (int j = 0; j < kOut; j += 4)
+        *reinterpret_cast<f32x4*>(out + (4 * g + i) * kOut + j) =
+            f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        *reinterpret_cast<f32x4*>(out + 64 * h + (4 * g + i) * 4) =
+            f32x4{o[4 * h][i], o[4 * h + 1][i], o[4 * h + 2][i], o[4 * h + 3][i]};
+    }
+  }
+}
+
+// One workgroup per (sequence, key-value head, piece of its positions, MT * WM query
+// tiles): WM waves take MT tiles each, and the 4 / WM waves of one tile set share the
+// piece's positions and join their m, l and O in LDS.
+template <int DT, int D, int MT, int WM>
+__global__ __launch_bounds__(kThreads) void attend_kernel(AttendArgs a) {
+  using X = Ops<DT, D>;
+  constexpr int kTile = 16 * X::kSub;
+  constexpr int WK = kWaves / WM;
+  __shared__ int16_t par_s[kMaxSeqRows];
+  __shared__ f32x4 join_o[WK > 1 ? WK / 2 * WM : 1][WK > 1 ? MT * X::kOut : 1][64];
+  __shared__ float2 join_ml[WK > 1 ? WK / 2 * WM : 1][MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = lane & 15, g = lane >> 4;
+  const int wm = wave % WM, wk = wave / WM;
+  // The query groups of one piece go to the same XCD (every eighth workgroup does), so
+  // that they find its keys in that XCD's L2.
+  const int64_t id = blockIdx.x;
+  const int64_t unit = id / (8 * a.mgroups) * 8 + id % 8;
+  const int mg = static_cast<int>(id / 8 % a.mgroups);
+  if (unit >= a.units) return;
+  const int split = static_cast<int>(unit % a.splits);
+  const int64_t bh = unit / a.splits;
+  const int b = static_cast<int>(bh / a.heads), kvh = static_cast<int>(bh % a.heads);
+  const SeqCall call = seq_call(a, b);
+  const int rows = call.q.n, M = rows * a.group;
+  const int m0 = (mg * WM + wm) * MT * 16;  // the wave's first query
+  if (mg * WM * MT * 16 >= M) return;
+  const int end = call.c < 0 ? 0 : call.c + rows;
+  const int k0 = split * a.span;
+  if (split > 0 && k0 >= end) return;
+  const int k1 = min(k0 + a.span, end);
+  if (call.q.tree && k1 > call.c && call.c >= 0) {
+    for (int u = 1 + tid; u < rows; u += kThreads)
+      par_s[u] = static_cast<int16_t>(node_parent(a.rows, b, true, u));
+    __syncthreads();
+  }
+
+  // The queries, in operand layout; places past the last query are zero.
+  u32x4 q[MT][X::kFrags];
+  int64_t to[MT];  // row and head of query place n, or -1
+  int row[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int x = m0 + 16 * m + n;
+    row[m] = x < M ? x / a.group : -1;
+    const int h = kvh * a.group + x % a.group;
+    to[m] = x < M ? (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_heads + h : -1;
+    const unsigned char* p =
+        a.q + (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_bytes + h * D * X::kBytes;
+#pragma unroll
+    for (int f = 0; f < X::kFrags; ++f) {
+      q[m][f] = u32x4{0u, 0u, 0u, 0u};
+      if (x < M) q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + X::frag_at(g, f)), a.flip);
+    }
+  }
+
+  f32x4 o[MT][X::kOut];
+  float mx[MT], sum[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    mx[m] = kLowest;
+    sum[m] = 0.f;
+#pragma unroll
+    for (int j = 0; j < X::kOut; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // The wave's positions [w0, w1), in whole tiles of the piece.
+  const int share = (a.span / kTile + WK - 1) / WK * kTile;
+  const int w0 = min(k0 + wk * share, k1), w1 = min(w0 + share, k1);
+  const unsigned k_lane = n * D * X::kBytes + g * 16;
+  const unsigned v_lane = X::v_lane(n, g);
+  const int64_t head_bytes = static_cast<int64_t>(kvh) * D * X::kBytes << a.page_log;
+  const int32_t* table = a.table + static_cast<int64_t>(max(call.s, 0)) * a.max_pages;
+  // Pages of the next 64 sub-tiles, one a lane (-1: none).
+  int ids = -1;
+  auto fetch_ids = [&](int from) {
+    const int j = from + 16 * lane;
+    ids = j < w1 ? table[j >> a.page_log] : -1;
+    if (ids >= a.pages) ids = -1;
+  };
+  // Byte offset of a sub-tile's first row in the layer (of page 0 where it has none).
+  auto sub_at = [&](int j, int base, bool* ok) {
+    const int id = __builtin_amdgcn_readlane(ids, ((j - base) >> 4) & 63);
+    *ok = id >= 0;
+    return max(id, 0) * a.page_bytes + head_bytes +
+           static_cast<int64_t>(j & ((1 << a.page_log) - 1)) * (D * X::kBytes);
+  };
+
+  int base = w0;
+  if (w0 < w1) fetch_ids(w0);
+  for (int j0 = w0; j0 < w1; j0 += kTile) {
+    if (j0 - base >= 64 * 16) {
+      base = j0;
+      fetch_ids(j0);
+    }
+    u32x4 k[X::kSub][X::kFrags];
+    typename X::V v;
+    bool ok[X::kSub];
+    int64_t at[X::kSub];
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) at[t] = sub_at(j0 + 16 * t, base, &ok[t]);
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) {
+#pragma unroll
+      for (int f = 0; f < X::kFrags; ++f)
+        k[t][f] = *reinterpret_cast<const u32x4*>(a.k + at[t] + k_lane + f * 64);
+    }
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) X::load_v(v, t, a.v + at[t], v_lane);
+    bool whole = j0 + kTile <= call.c;
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) whole = whole && ok[t];
+
+    float p[MT][X::kSub][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t) {
+        const f32x4 s = X::scores(k[t], q[m]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[m][t][i] = s[i] * a.scale_log2;
+      }
+    }
+    if (!whole) {
+      // Positions past the rows, without a page, or of rows that a query does not follow.
+      unsigned pages = 0;
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t) pages |= ok[t] ? 0xffffu << (16 * t) : 0u;
+      const int old = min(max(call.c - j0, 0), 32), have = min(max(end - j0, 0), 32);
+      const unsigned any = pages & (have >= 32 ? ~0u : (1u << have) - 1u);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        unsigned see = old >= 32 ? ~0u : (1u << old) - 1u;
+        for (int u = row[m]; u >= 0 && call.c + u >= j0;
+             u = u == 0 ? -1 : call.q.tree ? par_s[u] : u - 1) {
+          const int x = call.c + u - j0;
+          if (x < 32) see |= 1u << x;
+        }
+        see &= any;
+#pragma unroll
+        for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(see >> (16 * t + 4 * g + i) & 1u)) p[m][t][i] = -INFINITY;
+      }
+      // Whatever lies there must not meet a weight of zero: it may be NaN.
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
+    }
+    bool grown = false;
+    float top[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float x = p[m][0][0];
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = fmaxf(x, p[m][t][i]);
+      top[m] = rows_max(x);
+      grown = grown || top[m] > mx[m] + kSlack;
+    }
+    if (__any(grown)) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float now = fmaxf(mx[m], top[m]);
+        const float f = __builtin_amdgcn_exp2f(mx[m] - now);
+        mx[m] = now;
+        sum[m] *= f;
+#pragma unroll
+        for (int j = 0; j < X::kOut; ++j) o[m][j] *= f;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[m][t][i] = __builtin_amdgcn_exp2f(p[m][t][i] - mx[m]);
+          sum[m] += p[m][t][i];
+        }
+    }
+    X::template outputs<MT>(o, v, p);
+  }
+  // Each of a query's four lanes has summed its own positions.
+#pragma unroll
+  for (int m = 0; m < MT; ++m) sum[m] = rows_sum(sum[m]);
+
+  // The waves of one tile set join, halves at a time.
+  if constexpr (WK > 1) {
+#pragma unroll
+    for (int half = WK / 2; half > 0; half /= 2) {
+      __syncthreads();
+      if (wk >= half && wk < 2 * half) {
+        const int at = (wk - half) * WM + wm;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          join_ml[at][m][lane] = make_float2(mx[m], sum[m]);
+#pragma unroll
+          for (int j = 0; j < X::kOut; ++j) join_o[at][m * X::kOut + j][lane] = o[m][j];
+        }
+      }
+      __syncthreads();
+      if (wk < half) {
+        const int at = wk * WM + wm;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float2 y = join_ml[at][m][lane];
+          const float now = fmaxf(mx[m], y.x);
+          const float fa = __builtin_amdgcn_exp2f(mx[m] - now);
+          const float fb = __builtin_amdgcn_exp2f(y.x - now);
+          mx[m] = now;
+          sum[m] = sum[m] * fa + y.y * fb;
+#pragma unroll
+          for (int j = 0; j < X::kOut; ++j)
+            o[m][j] = o[m][j] * fa + join_o[at][m * X::kOut + j][lane] * fb;
         }
       }
     }
-    float top = x;
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    const float mn = fmaxf(m, top);
-    if (mn == -INFINITY) continue;
-    const float f = exp2f(m - mn);
-    const float p = at >= 0 ? exp2f(x - mn) : 0.f;
-    m = mn;
-    float sum = p;
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-    l = l * f + sum;
-    p_s[wave][lane] = p;
-    at_s[wave][lane] = at;
-    for (int t = 0; t < kPer; ++t) o[t] *= f;
-    for (int k = 0; k < kKeys; ++k) {
-      const int64_t w = at_s[wave][k];
-      if (w < 0) continue;
-      for (int t = 0; t < kPer; ++t)
-        o[t] += p_s[wave][k] * E::scalar(a.v + w * E::kBytes, lane + 64 * t);
+    if (wk > 0) return;
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (to[m] < 0) continue;
+    if (a.splits == 1) {
+      store_query<DT, D>(a.out + to[m] * D * X::kBytes, o[m], g, sum[m] > 0.f ? 1.f / sum[m] : 0.f);
+    } else {
+      const int64_t at = split * a.row_heads + to[m];
+      store_partial<DT, D>(a.part_o + at * D, o[m], g);
+      if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m]);
     }
   }
-  if (lane == 0) {
-    m_s[wave] = m;
-    l_s[wave] = l;
+}
+
+// Joins the pieces of every row and head: one wave each, in the pieces' order.
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
+  constexpr int kPer = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int h = static_cast<int>(x % a.q_heads);
+  const int64_t bi = x / a.q_heads;
+  const int b = static_cast<int>(bi / a.rows.rmax), i = static_cast<int>(bi % a.rows.rmax);
+  if (b >= a.rows.B) return;
+  const SeqCall call = seq_call(a, b);
+  if (i >= call.q.n) return;
+  const int64_t r = (static_cast<int64_t>(call.q.row0) + i) * a.q_heads + h;
+  const int end = call.c < 0 ? 0 : call.c + call.q.n;
+  const int used = end > 0 ? (end + a.span - 1) / a.span : 0;
+  float m = kLowest, l = 0.f, o[kPer] = {};
+  for (int s = 0; s < used; ++s) {
+    const int64_t at = s * a.row_heads + r;
+    const float2 y = a.part_ml[at];
+    const float now = fmaxf(m, y.x);
+    const float fa = __builtin_amdgcn_exp2f(m - now), fb = __builtin_amdgcn_exp2f(y.x - now);
+    m = now;
+    l = l * fa + y.y * fb;
+#pragma unroll
+    for (int t = 0; t < kPer; ++t) o[t] = o[t] * fa + a.part_o[at * D + lane * kPer + t] * fb;
   }
-  for (int t = 0; t < kPer; ++t) o_s[wave][lane + 64 * t] = o[t];
-  __syncthreads();
-  if (tid >= D) return;
-  float top = m_s[0];
-  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_s[w]);
-  float x = 0.f, sum = 0.f;
-  for (int w = 0; w < kWaves; ++w) {
-    const float f = m_s[w] == -INFINITY ? 0.f : exp2f(m_s[w] - top);
-    x += f * o_s[w][tid];
-    sum += f * l_s[w];
-  }
-  x = sum > 0.f ? x / sum : 0.f;
-  const int64_t to = (r * a.q_heads + h) * D + tid;
+  const float f = l > 0.f ? 1.f / l : 0.f;
   if constexpr (DT == WF_F32) {
-    reinterpret_cast<float*>(a.out)[to] = x;
+#pragma unroll
+    for (int t = 0; t < kPer; ++t)
+      reinterpret_cast<float*>(a.out)[r * D + lane * kPer + t] = o[t] * f;
+  } else if constexpr (kPer == 2) {
+    reinterpret_cast<unsigned*>(a.out)[r * (D / 2) + lane] = pack_bf16(o[0] * f, o[1] * f);
   } else {
-    const unsigned u = __float_as_uint(x);
-    reinterpret_cast<uint16_t*>(a.out)[to] =
-        static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+    reinterpret_cast<uint16_t*>(a.out)[r * D + lane] = static_cast<uint16_t>(pack_bf16(o[0] * f, 0.f));
   }
+}
+
+// Query tiles per wave and waves side by side along the queries.
+struct Shape {
+  int mt, wm;
+};
+
+Shape attend_shape(int tiles) {
+  if (tiles <= 1) return Shape{1, 1};
+  if (tiles <= 2) return Shape{2, 1};
+  if (tiles <= 4) return Shape{2, 2};
+  return Shape{2, 4};
+}
+
+template <int DT, int D>
+void launch_typed(const AttendArgs& a, Shape shape, int64_t blocks, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  if (shape.wm == 1 && shape.mt == 1) {
+    hipLaunchKernelGGL((attend_kernel<DT, D, 1, 1>), grid, block, 0, stream, a);
+  } else if (shape.wm == 1) {
+    hipLaunchKernelGGL((attend_kernel<DT, D, 2, 1>), grid, block, 0, stream, a);
+  } else if (shape.wm == 2) {
+    hipLaunchKernelGGL((attend_kernel<DT, D, 2, 2>), grid, block, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((attend_kernel<DT, D, 2, 4>), grid, block, 0, stream, a);
+  }
+}
+
+template <int DT, int D>
+void launch_join(const AttendArgs& a, hipStream_t stream) {
+  const int64_t n = static_cast<int64_t>(a.rows.B) * a.rows.rmax * a.q_heads;
+  hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(static_cast<unsigned>((n + kWaves - 1) / kWaves)),
+                     dim3(kThreads), 0, stream, a);
+}
+
+int query_tiles(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads) {
+  return static_cast<int>((static_cast<int64_t>(rows.rmax) * (q_heads / cache.heads) + 15) / 16);
+}
+
+int query_groups(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads) {
+  const int tiles = query_tiles(cache, rows, q_heads);
+  const Shape s = attend_shape(tiles);
+  return (tiles + s.mt * s.wm - 1) / (s.mt * s.wm);
 }
 
 }  // namespace
 
-AttendPlan attend_plan(const wf_page_cache&, const RowsArgs&, int32_t, int32_t) {
-  return AttendPlan{1, 0};
+AttendPlan attend_plan(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
+                       int32_t max_context) {
+  int64_t most = static_cast<int64_t>(max_context) + rows.rmax;
+  const int64_t room = static_cast<int64_t>(cache.max_pages) * cache.page_size;
+  most = most < room ? most : room;
+  const int64_t one =
+      static_cast<int64_t>(rows.B) * cache.heads * query_groups(cache, rows, q_heads);
+  int64_t splits = (kTargetBlocks + one - 1) / one;
+  int64_t span = (most + splits - 1) / splits;
+  span = (span + kMinSpan - 1) / kMinSpan * kMinSpan;
+  span = span < kMinSpan ? kMinSpan : span;
+  splits = (most + span - 1) / span;
+  return AttendPlan{static_cast<int32_t>(splits < 1 ? 1 : splits), static_cast<int32_t>(span)};
 }
 
-size_t attend_workspace(const wf_page_cache&, const RowsArgs&, int32_t, int32_t, int64_t) {
-  return 0;
+int64_t attend_blocks(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
+                      int32_t max_context) {
+  const AttendPlan p = attend_plan(cache, rows, q_heads, max_context);
+  const int64_t units = static_cast<int64_t>(rows.B) * cache.heads * p.splits;
+  return (units + 7) / 8 * 8 * query_groups(cache, rows, q_heads);
+}
+
+size_t attend_workspace(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
+                        int32_t max_context, int64_t total_rows) {
+  const AttendPlan p = attend_plan(cache, rows, q_heads, max_context);
+  if (p.splits == 1) return 0;
+  return static_cast<size_t>(p.splits) * total_rows * q_heads * (cache.head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
                          const wf_page_cache& cache, int32_t layer, const RowsArgs& rows,
-                         const int32_t* seq, int32_t max_context, float scale, void* out, void*,
-                         int64_t, hipStream_t stream) {
+                         const int32_t* seq, int32_t max_context, float scale, void* out,
+                         void* workspace, int64_t total_rows, hipStream_t stream) {
   const int bytes = cache.dtype == WF_BF16 ? 2 : 4;
+  const AttendPlan plan = attend_plan(cache, rows, q_heads, max_context);
   AttendArgs a{};
   a.rows = rows;
   a.q = static_cast<const unsigned char*>(q);
@@ -146,7 +636,7 @@ hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
   a.group = q_heads / cache.heads;
   a.k = static_cast<const unsigned char*>(cache.k) + layer * cache.layer_stride * bytes;
   a.v = static_cast<const unsigned char*>(cache.v) + layer * cache.layer_stride * bytes;
-  a.page_elems = cache.page_stride;
+  a.page_bytes = cache.page_stride * bytes;
   a.pages = cache.pages;
   a.heads = cache.heads;
   a.page_log = __builtin_ctz(static_cast<unsigned>(cache.page_size));
@@ -156,20 +646,30 @@ hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
   a.context = cache.context;
   a.seq = seq;
   a.max_context = max_context;
-  a.scale_log2 = scale * kLog2E;
+  a.scale_log2 = fabsf(scale) * kLog2E;
+  a.flip = scale < 0.f ? (cache.dtype == WF_BF16 ? 0x80008000u : 0x80000000u) : 0u;
   a.out = static_cast<unsigned char*>(out);
-  const dim3 grid(static_cast<unsigned>(rows.B) * rows.rmax, q_heads);
-  if (cache.dtype == WF_BF16) {
-    if (cache.head_dim == 64) {
-      hipLaunchKernelGGL((attend_kernel<WF_BF16, 64>), grid, dim3(kThreads), 0, stream, a);
-    } else {
-      hipLaunchKernelGGL((attend_kernel<WF_BF16, 128>), grid, dim3(kThreads), 0, stream, a);
-    }
-  } else if (cache.head_dim == 64) {
-    hipLaunchKernelGGL((attend_kernel<WF_F32, 64>), grid, dim3(kThreads), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((attend_kernel<WF_F32, 128>), grid, dim3(kThreads), 0, stream, a);
-  }
+  a.splits = plan.splits;
+  a.span = plan.span;
+  a.mgroups = query_groups(cache, rows, q_heads);
+  a.units = static_cast<int64_t>(rows.B) * cache.heads * plan.splits;
+  a.row_heads = total_rows * q_heads;
+  a.part_o = static_cast<float*>(workspace);
+  if (plan.splits > 1)
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + plan.splits * a.row_heads * cache.head_dim);
+  const Shape shape = attend_shape(query_tiles(cache, rows, q_heads));
+  const int64_t blocks = attend_blocks(cache, rows, q_heads, max_context);
+  const bool bf16 = cache.dtype == WF_BF16, wide = cache.head_dim == 128;
+  if (bf16 && wide) launch_typed<WF_BF16, 128>(a, shape, blocks, stream);
+  if (bf16 && !wide) launch_typed<WF_BF16, 64>(a, shape, blocks, stream);
+  if (!bf16 && wide) launch_typed<WF_F32, 128>(a, shape, blocks, stream);
+  if (!bf16 && !wide) launch_typed<WF_F32, 64>(a, shape, blocks, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.splits == 1) return e;
+  if (bf16 && wide) launch_join<WF_BF16, 128>(a, stream);
+  if (bf16 && !wide) launch_join<WF_BF16, 64>(a, stream);
+  if (!bf16 && wide) launch_join<WF_F32, 128>(a, stream);
+  if (!bf16 && !wide) launch_join<WF_F32, 64>(a, stream);
   return hipGetLastError();
 }
 

@@ -38,6 +38,9 @@ struct AttendPlan {
 
 AttendPlan attend_plan(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
                        int32_t max_context);
+// Workgroups of the launch.
+int64_t attend_blocks(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
+                      int32_t max_context);
 size_t attend_workspace(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
                         int32_t max_context, int64_t total_rows);
 hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
