@@ -273,158 +273,84 @@ __device__ inline void store_partial(float* out, const f32x4* o, int g) {
   }
 }
 
-// One workgroup per (sequence, key-value head, piece of its positions, MT * WM query
-// tiles): WM waves take MT tiles each, and the 4 / WM waves of one tile set share the
-// piece's positions and join their m, l and O in LDS.
-template <int DT, int D, int MT, int WM>
-__global__ __launch_bounds__(kThreads) void attend_kernel(AttendArgs a) {
+// What a wave keeps of MT tiles of 16 queries: the queries in operand layout, and for
+// query place n of each tile its row, where its output goes, m, l and O.
+template <int DT, int D, int MT>
+struct Queries {
   using X = Ops<DT, D>;
-  constexpr int kTile = 16 * X::kSub;
-  constexpr int WK = kWaves / WM;
-  __shared__ int16_t par_s[kMaxSeqRows];
-  __shared__ f32x4 join_o[WK > 1 ? WK / 2 * WM : 1][WK > 1 ? MT * X::kOut : 1][64];
-  __shared__ float2 join_ml[WK > 1 ? WK / 2 * WM : 1][MT][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = lane & 15, g = lane >> 4;
-  const int wm = wave % WM, wk = wave / WM;
-  // The query groups of one piece go to the same XCD (every eighth workgroup does), so
-  // that they find its keys in that XCD's L2.
-  const int64_t id = blockIdx.x;
-  const int64_t unit = id / (8 * a.mgroups) * 8 + id % 8;
-  const int mg = static_cast<int>(id / 8 % a.mgroups);
-  if (unit >= a.units) return;
-  const int split = static_cast<int>(unit % a.splits);
-  const int64_t bh = unit / a.splits;
-  const int b = static_cast<int>(bh / a.heads), kvh = static_cast<int>(bh % a.heads);
-  const SeqCall call = seq_call(a, b);
-  const int rows = call.q.n, M = rows * a.group;
-  const int m0 = (mg * WM + wm) * MT * 16;  // the wave's first query
-  if (mg * WM * MT * 16 >= M) return;
-  const int end = call.c < 0 ? 0 : call.c + rows;
-  const int k0 = split * a.span;
-  if (split > 0 && k0 >= end) return;
-  const int k1 = min(k0 + a.span, end);
-  if (call.q.tree && k1 > call.c && call.c >= 0) {
-    for (int u = 1 + tid; u < rows; u += kThreads)
-      par_s[u] = static_cast<int16_t>(node_parent(a.rows, b, true, u));
-    __syncthreads();
-  }
-
-  // The queries, in operand layout; places past the last query are zero.
   u32x4 q[MT][X::kFrags];
-  int64_t to[MT];  // row and head of query place n, or -1
-  int row[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int x = m0 + 16 * m + n;
-    row[m] = x < M ? x / a.group : -1;
-    const int h = kvh * a.group + x % a.group;
-    to[m] = x < M ? (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_heads + h : -1;
-    const unsigned char* p =
-        a.q + (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_bytes + h * D * X::kBytes;
-#pragma unroll
-    for (int f = 0; f < X::kFrags; ++f) {
-      q[m][f] = u32x4{0u, 0u, 0u, 0u};
-      if (x < M) q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + X::frag_at(g, f)), a.flip);
-    }
-  }
-
   f32x4 o[MT][X::kOut];
   float mx[MT], sum[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mx[m] = kLowest;
-    sum[m] = 0.f;
-#pragma unroll
-    for (int j = 0; j < X::kOut; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  int row[MT];     // row of the round, -1 past the last query
+  int64_t to[MT];  // packed row and head, or -1
 
-  // The wave's positions [w0, w1), in whole tiles of the piece.
-  const int share = (a.span / kTile + WK - 1) / WK * kTile;
-  const int w0 = min(k0 + wk * share, k1), w1 = min(w0 + share, k1);
-  const unsigned k_lane = n * D * X::kBytes + g * 16;
-  const unsigned v_lane = X::v_lane(n, g);
-  const int64_t head_bytes = static_cast<int64_t>(kvh) * D * X::kBytes << a.page_log;
-  const int32_t* table = a.table + static_cast<int64_t>(max(call.s, 0)) * a.max_pages;
-  // Pages of the next 64 sub-tiles, one a lane (-1: none).
-  int ids = -1;
-  auto fetch_ids = [&](int from) {
-    const int j = from + 16 * lane;
-    ids = j < w1 ? table[j >> a.page_log] : -1;
-    if (ids >= a.pages) ids = -1;
-  };
-  // Byte offset of a sub-tile's first row in the layer (of page 0 where it has none).
-  auto sub_at = [&](int j, int base, bool* ok) {
-    const int id = __builtin_amdgcn_readlane(ids, ((j - base) >> 4) & 63);
-    *ok = id >= 0;
-    return max(id, 0) * a.page_bytes + head_bytes +
-           static_cast<int64_t>(j & ((1 << a.page_log) - 1)) * (D * X::kBytes);
-  };
-
-  int base = w0;
-  if (w0 < w1) fetch_ids(w0);
-  for (int j0 = w0; j0 < w1; j0 += kTile) {
-    if (j0 - base >= 64 * 16) {
-      base = j0;
-      fetch_ids(j0);
-    }
-    u32x4 k[X::kSub][X::kFrags];
-    typename X::V v;
-    bool ok[X::kSub];
-    int64_t at[X::kSub];
-#pragma unroll
-    for (int t = 0; t < X::kSub; ++t) at[t] = sub_at(j0 + 16 * t, base, &ok[t]);
-#pragma unroll
-    for (int t = 0; t < X::kSub; ++t) {
-#pragma unroll
-      for (int f = 0; f < X::kFrags; ++f)
-        k[t][f] = *reinterpret_cast<const u32x4*>(a.k + at[t] + k_lane + f * 64);
-    }
-#pragma unroll
-    for (int t = 0; t < X::kSub; ++t) X::load_v(v, t, a.v + at[t], v_lane);
-    bool whole = j0 + kTile <= call.c;
-#pragma unroll
-    for (int t = 0; t < X::kSub; ++t) whole = whole && ok[t];
-
-    float p[MT][X::kSub][4];
+  __device__ inline void load(const AttendArgs& a, const SeqCall& call, int kvh, int first) {
+    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const int M = call.q.n * a.group;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      const int x = first + 16 * m + n;
+      row[m] = x < M ? x / a.group : -1;
+      const int h = kvh * a.group + x % a.group;
+      const int64_t r = static_cast<int64_t>(call.q.row0) + max(row[m], 0);
+      to[m] = x < M ? r * a.q_heads + h : -1;
+      const unsigned char* p = a.q + r * a.q_bytes + h * D * X::kBytes;
 #pragma unroll
-      for (int t = 0; t < X::kSub; ++t) {
-        const f32x4 s = X::scores(k[t], q[m]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[m][t][i] = s[i] * a.scale_log2;
+      for (int f = 0; f < X::kFrags; ++f) {
+        q[m][f] = u32x4{0u, 0u, 0u, 0u};
+        if (x < M)
+          q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + X::frag_at(g, f)), a.flip);
       }
+      mx[m] = kLowest;
+      sum[m] = 0.f;
+#pragma unroll
+      for (int j = 0; j < X::kOut; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    if (!whole) {
-      // Positions past the rows, without a page, or of rows that a query does not follow.
-      unsigned pages = 0;
+  }
+
+  using Weights = float[MT][X::kSub][4];
+
+  // The scores of sub-tile t, in base 2.
+  __device__ inline void score(Weights& p, int t, const u32x4* k, float scale) const {
 #pragma unroll
-      for (int t = 0; t < X::kSub; ++t) pages |= ok[t] ? 0xffffu << (16 * t) : 0u;
-      const int old = min(max(call.c - j0, 0), 32), have = min(max(end - j0, 0), 32);
-      const unsigned any = pages & (have >= 32 ? ~0u : (1u << have) - 1u);
+    for (int m = 0; m < MT; ++m) {
+      const f32x4 s = X::scores(k, q[m]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        unsigned see = old >= 32 ? ~0u : (1u << old) - 1u;
-        for (int u = row[m]; u >= 0 && call.c + u >= j0;
-             u = u == 0 ? -1 : call.q.tree ? par_s[u] : u - 1) {
-          const int x = call.c + u - j0;
-          if (x < 32) see |= 1u << x;
-        }
-        see &= any;
+      for (int i = 0; i < 4; ++i) p[m][t][i] = s[i] * scale;
+    }
+  }
+
+  // Of the 32 positions from j0 on, those that can be seen at all: before `end` and with
+  // a page (`pages`: a bit each).
+  __device__ static inline unsigned visible(int j0, int end, unsigned pages) {
+    const int have = min(max(end - j0, 0), 32);
+    return pages & (have >= 32 ? ~0u : (1u << have) - 1u);
+  }
+
+  // Takes out of a tile's scores what its query does not see: positions outside `any`,
+  // and of the round's own positions those of rows that are not on its path.
+  __device__ inline void mask(Weights& p, int j0, unsigned any, const SeqCall& call,
+                              const int16_t* par) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    const int old = min(max(call.c - j0, 0), 32);
 #pragma unroll
-        for (int t = 0; t < X::kSub; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(see >> (16 * t + 4 * g + i) & 1u)) p[m][t][i] = -INFINITY;
+    for (int m = 0; m < MT; ++m) {
+      unsigned see = old >= 32 ? ~0u : (1u << old) - 1u;
+      for (int u = row[m]; u >= 0 && call.c + u >= j0; u = u == 0 ? -1 : call.q.tree ? par[u] : u - 1) {
+        const int x = call.c + u - j0;
+        if (x < 32) see |= 1u << x;
       }
-      // Whatever lies there must not meet a weight of zero: it may be NaN.
+      see &= any;
 #pragma unroll
       for (int t = 0; t < X::kSub; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
+          if (!(see >> (16 * t + 4 * g + i) & 1u)) p[m][t][i] = -INFINITY;
     }
+  }
+
+  // Scores to weights, with the running maxima and sums.
+  __device__ inline void soften(Weights& p) {
     bool grown = false;
     float top[MT];
 #pragma unroll
@@ -458,56 +384,317 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendArgs a) {
           sum[m] += p[m][t][i];
         }
     }
-    X::template outputs<MT>(o, v, p);
   }
-  // Each of a query's four lanes has summed its own positions.
-#pragma unroll
-  for (int m = 0; m < MT; ++m) sum[m] = rows_sum(sum[m]);
 
-  // The waves of one tile set join, halves at a time.
-  if constexpr (WK > 1) {
+  // The result of a piece: the output if it is the only one, else its part.  Each of a
+  // query's four lanes has summed its own positions.
+  __device__ inline void store(const AttendArgs& a, int split) const {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-    for (int half = WK / 2; half > 0; half /= 2) {
-      __syncthreads();
-      if (wk >= half && wk < 2 * half) {
-        const int at = (wk - half) * WM + wm;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          join_ml[at][m][lane] = make_float2(mx[m], sum[m]);
-#pragma unroll
-          for (int j = 0; j < X::kOut; ++j) join_o[at][m * X::kOut + j][lane] = o[m][j];
-        }
-      }
-      __syncthreads();
-      if (wk < half) {
-        const int at = wk * WM + wm;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float2 y = join_ml[at][m][lane];
-          const float now = fmaxf(mx[m], y.x);
-          const float fa = __builtin_amdgcn_exp2f(mx[m] - now);
-          const float fb = __builtin_amdgcn_exp2f(y.x - now);
-          mx[m] = now;
-          sum[m] = sum[m] * fa + y.y * fb;
-#pragma unroll
-          for (int j = 0; j < X::kOut; ++j)
-            o[m][j] = o[m][j] * fa + join_o[at][m * X::kOut + j][lane] * fb;
-        }
+    for (int m = 0; m < MT; ++m) {
+      if (to[m] < 0) continue;
+      if (a.splits == 1) {
+        store_query<DT, D>(a.out + to[m] * D * X::kBytes, o[m], g, sum[m] > 0.f ? 1.f / sum[m] : 0.f);
+      } else {
+        const int64_t at = split * a.row_heads + to[m];
+        store_partial<DT, D>(a.part_o + at * D, o[m], g);
+        if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m]);
       }
     }
-    if (wk > 0) return;
+  }
+};
+
+// The pages of one sequence as a wave walks it: the ids of 64 sub-tiles at a time, one a
+// lane (-1: none).
+struct PageWalk {
+  const int32_t* table;
+  int log, pages, stop, base, ids;
+
+  __device__ inline void fetch(int from) {
+    const int j = from + 16 * static_cast<int>(threadIdx.x & 63);
+    base = from;
+    ids = j < stop ? table[j >> log] : -1;
+    if (ids >= pages) ids = -1;
+  }
+  __device__ inline PageWalk(const AttendArgs& a, const SeqCall& call, int from, int to)
+      : table(a.table + static_cast<int64_t>(max(call.s, 0)) * a.max_pages), log(a.page_log),
+        pages(a.pages), stop(to), base(from), ids(-1) {
+    if (from < to) fetch(from);
+  }
+  // The tile from j0 on (j0 grows by no more than 1,024 between calls).
+  __device__ inline void reach(int j0, int tile) {
+    if (j0 + tile - base > 64 * 16) fetch(j0);
+  }
+  // The page of sub-tile j, uniform, or -1.
+  __device__ inline int at(int j) const {
+    return __builtin_amdgcn_readlane(ids, ((j - base) >> 4) & 63);
+  }
+};
+
+struct Unit {
+  int split, b, kvh, mg;
+  bool ok;
+};
+
+// Workgroup -> (sequence, key-value head, piece, query group).  The query groups of one
+// piece go to the same XCD (every eighth workgroup does), so that they find its keys in
+// that XCD's L2.
+__device__ inline Unit unit_of(const AttendArgs& a) {
+  Unit x;
+  const int64_t id = blockIdx.x;
+  const int64_t unit = id / (8 * a.mgroups) * 8 + id % 8;
+  x.mg = static_cast<int>(id / 8 % a.mgroups);
+  x.ok = unit < a.units;
+  x.split = static_cast<int>(unit % a.splits);
+  const int64_t bh = unit / a.splits;
+  x.b = static_cast<int>(bh / a.heads);
+  x.kvh = static_cast<int>(bh % a.heads);
+  return x;
+}
+
+// Up to 16 MT queries: one workgroup per (sequence, key-value head, piece, query group),
+// whose four waves share the piece's positions and join their m, l and O in LDS.  Each
+// wave reads its keys and values straight from their pages; the next tile's keys are
+// fetched as soon as this one's are used, its values after the second product.
+template <int DT, int D, int MT>
+__global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
+  using X = Ops<DT, D>;
+  constexpr int kTile = 16 * X::kSub;
+  __shared__ int16_t par_s[kMaxSeqRows];
+  __shared__ f32x4 join_o[kWaves / 2][MT * X::kOut][64];
+  __shared__ float2 join_ml[kWaves / 2][MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = lane & 15, g = lane >> 4;
+  const Unit x = unit_of(a);
+  if (!x.ok) return;
+  const SeqCall call = seq_call(a, x.b);
+  const int rows = call.q.n, first = x.mg * MT * 16;
+  if (first >= rows * a.group) return;
+  const int end = call.c < 0 ? 0 : call.c + rows;
+  const int k0 = x.split * a.span;
+  if (x.split > 0 && k0 >= end) return;
+  const int k1 = min(k0 + a.span, end);
+  // The wave's positions [w0, w1), in whole tiles of the piece.
+  const int share = (a.span / kTile + kWaves - 1) / kWaves * kTile;
+  const int w0 = min(k0 + wave * share, k1), w1 = min(w0 + share, k1);
+  PageWalk walk(a, call, w0, w1);
+  if (call.q.tree && k1 > call.c && call.c >= 0) {
+    for (int u = 1 + tid; u < rows; u += kThreads)
+      par_s[u] = static_cast<int16_t>(node_parent(a.rows, x.b, true, u));
+    __syncthreads();
+  }
+  Queries<DT, D, MT> Q;
+  Q.load(a, call, x.kvh, first);
+
+  const unsigned k_lane = n * D * X::kBytes + g * 16, v_lane = X::v_lane(n, g);
+  const int64_t head_bytes = static_cast<int64_t>(x.kvh) * D * X::kBytes << a.page_log;
+  const int in_page = (1 << a.page_log) - 1;
+  u32x4 k[X::kSub][X::kFrags];
+  typename X::V v;
+  int64_t at[X::kSub];
+  // Places the tile from j on; its bits that have a page.
+  auto place = [&](int j) {
+    unsigned pages = 0;
+    walk.reach(j, kTile);
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) {
+      const int id = walk.at(j + 16 * t);
+      pages |= id >= 0 ? 0xffffu << (16 * t) : 0u;
+      at[t] = max(id, 0) * a.page_bytes + head_bytes +
+              static_cast<int64_t>((j + 16 * t) & in_page) * (D * X::kBytes);
+    }
+    return pages;
+  };
+  auto load_k = [&]() {
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+      for (int f = 0; f < X::kFrags; ++f)
+        k[t][f] = *reinterpret_cast<const u32x4*>(a.k + at[t] + k_lane + f * 64);
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) X::load_v(v, t, a.v + at[t], v_lane);
+  };
+  unsigned pages = 0;
+  if (w0 < w1) {
+    pages = place(w0);
+    load_k();
+    load_v();
+  }
+  for (int j0 = w0; j0 < w1; j0 += kTile) {
+    typename Queries<DT, D, MT>::Weights p;
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) Q.score(p, t, k[t], a.scale_log2);
+    const unsigned here = pages;
+    const bool more = j0 + kTile < w1;
+    if (more) {
+      pages = place(j0 + kTile);
+      load_k();
+    }
+    if (j0 + kTile > call.c || here != (X::kSub == 2 ? ~0u : 0xffffu)) {
+      const unsigned any = Q.visible(j0, end, here);
+      Q.mask(p, j0, any, call, par_s);
+      // Whatever lies there must not meet a weight of zero: it may be NaN.
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
+    }
+    Q.soften(p);
+    X::template outputs<MT>(Q.o, v, p);
+    if (more) load_v();
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (to[m] < 0) continue;
-    if (a.splits == 1) {
-      store_query<DT, D>(a.out + to[m] * D * X::kBytes, o[m], g, sum[m] > 0.f ? 1.f / sum[m] : 0.f);
-    } else {
-      const int64_t at = split * a.row_heads + to[m];
-      store_partial<DT, D>(a.part_o + at * D, o[m], g);
-      if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m]);
+  for (int m = 0; m < MT; ++m) Q.sum[m] = rows_sum(Q.sum[m]);
+
+  // The waves join, halves at a time.
+#pragma unroll
+  for (int half = kWaves / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        join_ml[wave - half][m][lane] = make_float2(Q.mx[m], Q.sum[m]);
+#pragma unroll
+        for (int j = 0; j < X::kOut; ++j) join_o[wave - half][m * X::kOut + j][lane] = Q.o[m][j];
+      }
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float2 y = join_ml[wave][m][lane];
+        const float now = fmaxf(Q.mx[m], y.x);
+        const float fa = __builtin_amdgcn_exp2f(Q.mx[m] - now);
+        const float fb = __builtin_amdgcn_exp2f(y.x - now);
+        Q.mx[m] = now;
+        Q.sum[m] = Q.sum[m] * fa + y.y * fb;
+#pragma unroll
+        for (int j = 0; j < X::kOut; ++j)
+          Q.o[m][j] = Q.o[m][j] * fa + join_o[wave][m * X::kOut + j][lane] * fb;
+      }
     }
   }
+  if (wave == 0) Q.store(a, x.split);
+}
+
+// Many queries: one workgroup per (sequence, key-value head, piece, query group) whose
+// four waves take MT tiles of 16 queries each and share every tile of keys and values
+// through LDS, where the next one is put while this one is used.
+template <int DT, int D, int MT>
+__global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) {
+  using X = Ops<DT, D>;
+  constexpr int kStep = 16 * X::kSub;                // positions per product
+  constexpr int kTile = 2 * kStep;                   // positions in LDS at a time
+  constexpr int kRow = D * X::kBytes / 16;           // 16-byte pieces of a row
+  constexpr int kLoads = kTile * kRow / kThreads;    // ... of k (and of v) per thread
+  constexpr int kSwizzle = kRow < 16 ? kRow - 1 : 15;
+  __shared__ int16_t par_s[kMaxSeqRows];
+  __shared__ u32x4 k_s[2][kTile * kRow], v_s[2][kTile * kRow];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = lane & 15, g = lane >> 4;
+  const Unit x = unit_of(a);
+  if (!x.ok) return;
+  const SeqCall call = seq_call(a, x.b);
+  const int rows = call.q.n, first = x.mg * kWaves * MT * 16;
+  if (first >= rows * a.group) return;
+  const int end = call.c < 0 ? 0 : call.c + rows;
+  const int k0 = x.split * a.span;
+  if (x.split > 0 && k0 >= end) return;
+  const int k1 = min(k0 + a.span, end);
+  PageWalk walk(a, call, k0, k1);
+  if (call.q.tree && k1 > call.c && call.c >= 0)
+    for (int u = 1 + tid; u < rows; u += kThreads)
+      par_s[u] = static_cast<int16_t>(node_parent(a.rows, x.b, true, u));
+  Queries<DT, D, MT> Q;
+  Q.load(a, call, x.kvh, first + wave * MT * 16);
+
+  const int64_t head_bytes = static_cast<int64_t>(x.kvh) * D * X::kBytes << a.page_log;
+  const int in_page = (1 << a.page_log) - 1;
+  u32x4 stage_k[kLoads], stage_v[kLoads];
+  // Piece i of a thread: row (i * 256 + tid) / kRow of the tile.  The rows of a wave's
+  // load lie in one sub-tile, so their page is uniform.
+  auto fetch = [&](int j) {
+    walk.reach(j, kTile);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (i * kThreads + tid) / kRow, piece = (i * kThreads + tid) % kRow;
+      const int sub = __builtin_amdgcn_readfirstlane(row >> 4);
+      const int id = walk.at(j + 16 * sub);
+      const int64_t at = max(id, 0) * a.page_bytes + head_bytes +
+                         static_cast<int64_t>((j + 16 * sub) & in_page) * (D * X::kBytes);
+      const unsigned off = ((row & 15) * kRow + piece) * 16;
+      stage_k[i] = *reinterpret_cast<const u32x4*>(a.k + at + off);
+      stage_v[i] = *reinterpret_cast<const u32x4*>(a.v + at + off);
+    }
+    unsigned long long pages = 0;
+#pragma unroll
+    for (int t = 0; t < kTile / 16; ++t)
+      pages |= walk.at(j + 16 * t) >= 0 ? 0xffffull << (16 * t) : 0ull;
+    return pages;
+  };
+  // Keys are read a row per lane: a row's pieces are rotated among each other by the row
+  // so that 16 rows' pieces spread over the banks.  Values are read 16 lanes a row.
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (i * kThreads + tid) / kRow, piece = (i * kThreads + tid) % kRow;
+      k_s[buf][row * kRow + (piece ^ (row & kSwizzle))] = stage_k[i];
+      v_s[buf][row * kRow + piece] = stage_v[i];
+    }
+  };
+  unsigned long long pages = 0;
+  if (k0 < k1) {
+    pages = fetch(k0);
+    put(0);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int j0 = k0; j0 < k1; j0 += kTile) {
+    const unsigned long long here = pages;
+    const bool more = j0 + kTile < k1;
+    if (more) pages = fetch(j0 + kTile);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = j0 + h * kStep;
+      if (j >= k1) break;
+      typename Queries<DT, D, MT>::Weights p;
+      typename X::V v;
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t) {
+        u32x4 k[X::kFrags];
+        const int row = h * kStep + 16 * t + n;
+#pragma unroll
+        for (int f = 0; f < X::kFrags; ++f)
+          k[f] = k_s[buf][row * kRow + ((f * 4 + g) ^ (n & kSwizzle))];
+        Q.score(p, t, k, a.scale_log2);
+      }
+      const unsigned char* vp = reinterpret_cast<const unsigned char*>(v_s[buf]);
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+        X::load_v(v, t, vp + (h * kStep + 16 * t) * kRow * 16, X::v_lane(n, g));
+      const unsigned have = static_cast<unsigned>(here >> (h * kStep));
+      if (j + kStep > call.c || (have & (X::kSub == 2 ? ~0u : 0xffffu)) != (X::kSub == 2 ? ~0u : 0xffffu)) {
+        const unsigned any = Q.visible(j, end, have);
+        Q.mask(p, j, any, call, par_s);
+#pragma unroll
+        for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
+      }
+      Q.soften(p);
+      X::template outputs<MT>(Q.o, v, p);
+    }
+    if (more) put(buf ^ 1);
+    __syncthreads();
+    buf ^= 1;
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) Q.sum[m] = rows_sum(Q.sum[m]);
+  Q.store(a, x.split);
 }
 
 // Joins the pieces of every row and head: one wave each, in the pieces' order.
@@ -525,16 +712,29 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
   const int64_t r = (static_cast<int64_t>(call.q.row0) + i) * a.q_heads + h;
   const int end = call.c < 0 ? 0 : call.c + call.q.n;
   const int used = end > 0 ? (end + a.span - 1) / a.span : 0;
+  // Lane s holds piece s's maximum and sum, 64 pieces at a time, so that the loads of
+  // the outputs depend on nothing.
   float m = kLowest, l = 0.f, o[kPer] = {};
-  for (int s = 0; s < used; ++s) {
-    const int64_t at = s * a.row_heads + r;
-    const float2 y = a.part_ml[at];
-    const float now = fmaxf(m, y.x);
-    const float fa = __builtin_amdgcn_exp2f(m - now), fb = __builtin_amdgcn_exp2f(y.x - now);
+  for (int s0 = 0; s0 < used; s0 += 64) {
+    const int many = min(used - s0, 64);
+    float2 y = make_float2(kLowest, 0.f);
+    if (lane < many) y = a.part_ml[(s0 + lane) * a.row_heads + r];
+    float top = y.x;
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const float now = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - now);
+    const float w = __builtin_amdgcn_exp2f(y.x - now);
+    float sum = y.y * w;
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
     m = now;
-    l = l * fa + y.y * fb;
+    l = l * f + sum;
 #pragma unroll
-    for (int t = 0; t < kPer; ++t) o[t] = o[t] * fa + a.part_o[at * D + lane * kPer + t] * fb;
+    for (int t = 0; t < kPer; ++t) o[t] *= f;
+    for (int s = 0; s < many; ++s) {
+      const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
+      const float* p = a.part_o + ((s0 + s) * a.row_heads + r) * D + lane * kPer;
+#pragma unroll
+      for (int t = 0; t < kPer; ++t) o[t] += p[t] * ws;
+    }
   }
   const float f = l > 0.f ? 1.f / l : 0.f;
   if constexpr (DT == WF_F32) {
@@ -548,29 +748,31 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
   }
 }
 
-// Query tiles per wave and waves side by side along the queries.
+// Query tiles per wave, and whether the waves take tiles of their own.
 struct Shape {
-  int mt, wm;
+  int mt;
+  bool wide;
 };
 
-Shape attend_shape(int tiles) {
-  if (tiles <= 1) return Shape{1, 1};
-  if (tiles <= 2) return Shape{2, 1};
-  if (tiles <= 4) return Shape{2, 2};
-  return Shape{2, 4};
+Shape attend_shape(int tiles, int dtype) {
+  if (tiles <= 1) return Shape{1, false};
+  if (tiles <= 2) return Shape{2, false};
+  // (float32 operands of two tiles a wave do not fit the registers of two waves a SIMD.)
+  if (tiles <= 4 || dtype == WF_F32) return Shape{1, true};
+  return Shape{2, true};
 }
 
 template <int DT, int D>
 void launch_typed(const AttendArgs& a, Shape shape, int64_t blocks, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
-  if (shape.wm == 1 && shape.mt == 1) {
-    hipLaunchKernelGGL((attend_kernel<DT, D, 1, 1>), grid, block, 0, stream, a);
-  } else if (shape.wm == 1) {
-    hipLaunchKernelGGL((attend_kernel<DT, D, 2, 1>), grid, block, 0, stream, a);
-  } else if (shape.wm == 2) {
-    hipLaunchKernelGGL((attend_kernel<DT, D, 2, 2>), grid, block, 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((attend_kernel<DT, D, 2, 4>), grid, block, 0, stream, a);
+  if (!shape.wide && shape.mt == 1) {
+    hipLaunchKernelGGL((attend_kernel<DT, D, 1>), grid, block, 0, stream, a);
+  } else if (!shape.wide) {
+    hipLaunchKernelGGL((attend_kernel<DT, D, 2>), grid, block, 0, stream, a);
+  } else if (shape.mt == 1) {
+    hipLaunchKernelGGL((attend_wide_kernel<DT, D, 1>), grid, block, 0, stream, a);
+  } else if constexpr (DT == WF_BF16) {
+    hipLaunchKernelGGL((attend_wide_kernel<DT, D, 2>), grid, block, 0, stream, a);
   }
 }
 
@@ -587,8 +789,9 @@ int query_tiles(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_head
 
 int query_groups(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads) {
   const int tiles = query_tiles(cache, rows, q_heads);
-  const Shape s = attend_shape(tiles);
-  return (tiles + s.mt * s.wm - 1) / (s.mt * s.wm);
+  const Shape s = attend_shape(tiles, cache.dtype);
+  const int each = s.mt * (s.wide ? kWaves : 1);
+  return (tiles + each - 1) / each;
 }
 
 }  // namespace
@@ -657,7 +860,7 @@ hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
   a.part_o = static_cast<float*>(workspace);
   if (plan.splits > 1)
     a.part_ml = reinterpret_cast<float2*>(a.part_o + plan.splits * a.row_heads * cache.head_dim);
-  const Shape shape = attend_shape(query_tiles(cache, rows, q_heads));
+  const Shape shape = attend_shape(query_tiles(cache, rows, q_heads), cache.dtype);
   const int64_t blocks = attend_blocks(cache, rows, q_heads, max_context);
   const bool bf16 = cache.dtype == WF_BF16, wide = cache.head_dim == 128;
   if (bf16 && wide) launch_typed<WF_BF16, 128>(a, shape, blocks, stream);
