@@ -29,6 +29,8 @@ constexpr float kLowest = -3.0e38f;  // a maximum of nothing: finite, so that no
 constexpr float kSlack = 8.f;
 constexpr int kMinSpan = 128;
 constexpr int kTargetBlocks = 2048;
+constexpr int kTargetWide = 512;   // two workgroups a CU fit
+constexpr int kJoinAhead = 8;      // pieces whose outputs are fetched at once
 
 struct AttendArgs {
   RowsArgs rows;
@@ -47,7 +49,6 @@ struct AttendArgs {
   unsigned flip;     // the sign bits to flip in q (scale < 0)
   unsigned char* out;
   int splits, span, mgroups;
-  int64_t units;     // sequences x heads x splits
   float* part_o;     // [splits][rows x q_heads][D]
   float2* part_ml;   // [splits][rows x q_heads]
   int64_t row_heads;
@@ -95,6 +96,7 @@ __device__ inline unsigned pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(unsigned, r);
 }
 
+// Operand fragment f of group g is the piece of sixteen bytes 4 f + g of a query or key.
 // What differs between the types: operand fragments, the two products and their tiles.
 // Lane l is place n = l % 16 of group g = l / 16.  kSub positions sub-tiles of 16 make
 // a tile; a lane's scores of sub-tile t are positions 16 t + 4 g + i, i < 4.  The
@@ -113,8 +115,6 @@ struct Ops<WF_BF16, D> {
     unsigned w[2 * 4][kVecV * 2];        // [position][dimension pairs]
   };
 
-  // Byte offset of fragment f of place n, group g within a row.
-  __device__ static inline int frag_at(int g, int f) { return f * 64 + g * 16; }
   __device__ static inline f32x4 scores(const u32x4* k, const u32x4* q) {
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -124,11 +124,13 @@ struct Ops<WF_BF16, D> {
     return s;
   }
   // Rows 4 g + i of sub-tile t, dimensions [n D / 16, (n + 1) D / 16).
+  template <bool STREAM>
   __device__ static inline void load_v(V& v, int t, const unsigned char* p, unsigned lane_off) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (D == 128) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(p + lane_off + i * D * 2);
+        const u32x4 x = STREAM ? load16(reinterpret_cast<const u32x4*>(p + lane_off + i * D * 2))
+                               : *reinterpret_cast<const u32x4*>(p + lane_off + i * D * 2);
         v.w[4 * t + i][0] = x.x;
         v.w[4 * t + i][1] = x.y;
         v.w[4 * t + i][2] = x.z;
@@ -186,7 +188,6 @@ struct Ops<WF_F32, D> {
   struct V {
     f32x4 w[4][D / 64];
   };
-  __device__ static inline int frag_at(int g, int f) { return f * 64 + g * 16; }
   __device__ static inline f32x4 scores(const u32x4* k, const u32x4* q) {
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -198,12 +199,15 @@ struct Ops<WF_F32, D> {
     return s;
   }
   // Rows 4 g + i, dimensions 64 h + 4 n + [0, 4).
+  template <bool STREAM>
   __device__ static inline void load_v(V& v, int, const unsigned char* p, unsigned lane_off) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
-        v.w[i][h] = *reinterpret_cast<const f32x4*>(p + lane_off + i * D * 4 + h * 256);
+        v.w[i][h] = __builtin_bit_cast(
+            f32x4, STREAM ? load16(reinterpret_cast<const u32x4*>(p + lane_off + i * D * 4 + h * 256))
+                          : *reinterpret_cast<const u32x4*>(p + lane_off + i * D * 4 + h * 256));
   }
   __device__ static inline unsigned v_lane(int n, int g) { return (4 * g * D + n * 4) * 4; }
   __device__ static inline void zero_v(V& v, int, int i) {
@@ -273,16 +277,22 @@ __device__ inline void store_partial(float* out, const f32x4* o, int g) {
   }
 }
 
+// Orders a wave's LDS accesses: what a lane wrote before, every lane reads after.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // What a wave keeps of MT tiles of 16 queries: the queries in operand layout, and for
-// query place n of each tile its row, where its output goes, m, l and O.
+// query place n of each tile its row, m, l and O.
 template <int DT, int D, int MT>
 struct Queries {
   using X = Ops<DT, D>;
   u32x4 q[MT][X::kFrags];
   f32x4 o[MT][X::kOut];
   float mx[MT], sum[MT];
-  int row[MT];     // row of the round, -1 past the last query
-  int64_t to[MT];  // packed row and head, or -1
+  int row[MT];  // row of the round, -1 past the last query
 
   __device__ inline void load(const AttendArgs& a, const SeqCall& call, int kvh, int first) {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
@@ -293,13 +303,12 @@ struct Queries {
       row[m] = x < M ? x / a.group : -1;
       const int h = kvh * a.group + x % a.group;
       const int64_t r = static_cast<int64_t>(call.q.row0) + max(row[m], 0);
-      to[m] = x < M ? r * a.q_heads + h : -1;
       const unsigned char* p = a.q + r * a.q_bytes + h * D * X::kBytes;
 #pragma unroll
       for (int f = 0; f < X::kFrags; ++f) {
         q[m][f] = u32x4{0u, 0u, 0u, 0u};
         if (x < M)
-          q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + X::frag_at(g, f)), a.flip);
+          q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + (4 * f + g) * 16), a.flip);
       }
       mx[m] = kLowest;
       sum[m] = 0.f;
@@ -388,15 +397,18 @@ struct Queries {
 
   // The result of a piece: the output if it is the only one, else its part.  Each of a
   // query's four lanes has summed its own positions.
-  __device__ inline void store(const AttendArgs& a, int split) const {
-    const int g = (threadIdx.x & 63) >> 4;
+  __device__ inline void store(const AttendArgs& a, const SeqCall& call, int kvh, int first,
+                               int split) const {
+    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (to[m] < 0) continue;
+      if (row[m] < 0) continue;
+      const int64_t to = (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_heads +
+                         kvh * a.group + (first + 16 * m + n) % a.group;
       if (a.splits == 1) {
-        store_query<DT, D>(a.out + to[m] * D * X::kBytes, o[m], g, sum[m] > 0.f ? 1.f / sum[m] : 0.f);
+        store_query<DT, D>(a.out + to * D * X::kBytes, o[m], g, sum[m] > 0.f ? 1.f / sum[m] : 0.f);
       } else {
-        const int64_t at = split * a.row_heads + to[m];
+        const int64_t at = split * a.row_heads + to;
         store_partial<DT, D>(a.part_o + at * D, o[m], g);
         if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m]);
       }
@@ -436,33 +448,39 @@ struct Unit {
   bool ok;
 };
 
-// Workgroup -> (sequence, key-value head, piece, query group).  The query groups of one
-// piece go to the same XCD (every eighth workgroup does), so that they find its keys in
-// that XCD's L2.
+// Workgroup -> (sequence, piece, key-value head, query group), such that all heads and
+// query groups of a piece go to the same XCD (every eighth workgroup does).
 __device__ inline Unit unit_of(const AttendArgs& a) {
   Unit x;
-  const int64_t id = blockIdx.x;
-  const int64_t unit = id / (8 * a.mgroups) * 8 + id % 8;
-  x.mg = static_cast<int>(id / 8 % a.mgroups);
-  x.ok = unit < a.units;
-  x.split = static_cast<int>(unit % a.splits);
-  const int64_t bh = unit / a.splits;
-  x.b = static_cast<int>(bh / a.heads);
-  x.kvh = static_cast<int>(bh % a.heads);
+  int64_t y = blockIdx.x / 8;
+  x.mg = static_cast<int>(y % a.mgroups);
+  y /= a.mgroups;
+  x.kvh = static_cast<int>(y % a.heads);
+  const int64_t piece = y / a.heads * 8 + blockIdx.x % 8;
+  x.split = static_cast<int>(piece % a.splits);
+  x.b = static_cast<int>(piece / a.splits);
+  x.ok = x.b < a.rows.B;
   return x;
 }
 
 // Up to 16 MT queries: one workgroup per (sequence, key-value head, piece, query group),
-// whose four waves share the piece's positions and join their m, l and O in LDS.  Each
-// wave reads its keys and values straight from their pages; the next tile's keys are
-// fetched as soon as this one's are used, its values after the second product.
+// whose four waves share the piece's positions and join their m, l and O in LDS.  Every
+// byte is read once, by loads that take whole lines and do not stay in the caches; the
+// next tile's keys are fetched as soon as this one's are in LDS, its values after the
+// second product.
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   using X = Ops<DT, D>;
   constexpr int kTile = 16 * X::kSub;
   __shared__ int16_t par_s[kMaxSeqRows];
-  __shared__ f32x4 join_o[kWaves / 2][MT * X::kOut][64];
-  __shared__ float2 join_ml[kWaves / 2][MT][64];
+  // The keys of each wave's tile, and after the last one what the waves join.
+  __shared__ union {
+    u32x4 k[kWaves][kTile * D * X::kBytes / 16];
+    struct {
+      f32x4 o[kWaves / 2][MT * X::kOut][64];
+      float2 ml[kWaves / 2][MT][64];
+    } join;
+  } share_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = lane & 15, g = lane >> 4;
   const Unit x = unit_of(a);
@@ -486,10 +504,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   Queries<DT, D, MT> Q;
   Q.load(a, call, x.kvh, first);
 
-  const unsigned k_lane = n * D * X::kBytes + g * 16, v_lane = X::v_lane(n, g);
+  const unsigned v_lane = X::v_lane(n, g);
   const int64_t head_bytes = static_cast<int64_t>(x.kvh) * D * X::kBytes << a.page_log;
   const int in_page = (1 << a.page_log) - 1;
-  u32x4 k[X::kSub][X::kFrags];
+  // A tile's keys as they lie in memory: piece i of a lane is piece i * 64 + lane.
+  constexpr int kRow = D * X::kBytes / 16;         // 16-byte pieces of a row
+  constexpr int kPieces = kTile * kRow / 64;       // ... of a tile's keys per lane
+  constexpr int kSubPieces = kPieces / X::kSub;
+  constexpr int kSwizzle = kRow < 16 ? kRow - 1 : 15;
+  u32x4 k[kPieces];
   typename X::V v;
   int64_t at[X::kSub];
   // Places the tile from j on; its bits that have a page.
@@ -509,12 +532,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 #pragma unroll
     for (int t = 0; t < X::kSub; ++t)
 #pragma unroll
-      for (int f = 0; f < X::kFrags; ++f)
-        k[t][f] = *reinterpret_cast<const u32x4*>(a.k + at[t] + k_lane + f * 64);
+      for (int i = 0; i < kSubPieces; ++i)
+        k[t * kSubPieces + i] = load16(reinterpret_cast<const u32x4*>(a.k + at[t]) + i * 64 + lane);
   };
   auto load_v = [&]() {
 #pragma unroll
-    for (int t = 0; t < X::kSub; ++t) X::load_v(v, t, a.v + at[t], v_lane);
+    for (int t = 0; t < X::kSub; ++t) X::template load_v<true>(v, t, a.v + at[t], v_lane);
   };
   unsigned pages = 0;
   if (w0 < w1) {
@@ -524,14 +547,29 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   }
   for (int j0 = w0; j0 < w1; j0 += kTile) {
     typename Queries<DT, D, MT>::Weights p;
+    // Rows to operand layout through the wave's own LDS.  A row's pieces are exchanged by
+    // the row's number, so that 16 rows' pieces spread over the banks.
 #pragma unroll
-    for (int t = 0; t < X::kSub; ++t) Q.score(p, t, k[t], a.scale_log2);
+    for (int i = 0; i < kPieces; ++i) {
+      const int row = (i * 64 + lane) / kRow, piece = (i * 64 + lane) % kRow;
+      share_s.k[wave][row * kRow + (piece ^ (row & kSwizzle))] = k[i];
+    }
+    wave_sync();
     const unsigned here = pages;
     const bool more = j0 + kTile < w1;
     if (more) {
       pages = place(j0 + kTile);
       load_k();
     }
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) {
+      u32x4 kf[X::kFrags];
+#pragma unroll
+      for (int f = 0; f < X::kFrags; ++f)
+        kf[f] = share_s.k[wave][(16 * t + n) * kRow + ((4 * f + g) ^ (n & kSwizzle))];
+      Q.score(p, t, kf, a.scale_log2);
+    }
+    wave_sync();
     if (j0 + kTile > call.c || here != (X::kSub == 2 ? ~0u : 0xffffu)) {
       const unsigned any = Q.visible(j0, end, here);
       Q.mask(p, j0, any, call, par_s);
@@ -556,16 +594,16 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     if (wave >= half && wave < 2 * half) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        join_ml[wave - half][m][lane] = make_float2(Q.mx[m], Q.sum[m]);
+        share_s.join.ml[wave - half][m][lane] = make_float2(Q.mx[m], Q.sum[m]);
 #pragma unroll
-        for (int j = 0; j < X::kOut; ++j) join_o[wave - half][m * X::kOut + j][lane] = Q.o[m][j];
+        for (int j = 0; j < X::kOut; ++j) share_s.join.o[wave - half][m * X::kOut + j][lane] = Q.o[m][j];
       }
     }
     __syncthreads();
     if (wave < half) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const float2 y = join_ml[wave][m][lane];
+        const float2 y = share_s.join.ml[wave][m][lane];
         const float now = fmaxf(Q.mx[m], y.x);
         const float fa = __builtin_amdgcn_exp2f(Q.mx[m] - now);
         const float fb = __builtin_amdgcn_exp2f(y.x - now);
@@ -573,11 +611,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
         Q.sum[m] = Q.sum[m] * fa + y.y * fb;
 #pragma unroll
         for (int j = 0; j < X::kOut; ++j)
-          Q.o[m][j] = Q.o[m][j] * fa + join_o[wave][m * X::kOut + j][lane] * fb;
+          Q.o[m][j] = Q.o[m][j] * fa + share_s.join.o[wave][m * X::kOut + j][lane] * fb;
       }
     }
   }
-  if (wave == 0) Q.store(a, x.split);
+  if (wave == 0) Q.store(a, call, x.kvh, first, x.split);
 }
 
 // Many queries: one workgroup per (sequence, key-value head, piece, query group) whose
@@ -668,13 +706,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
         const int row = h * kStep + 16 * t + n;
 #pragma unroll
         for (int f = 0; f < X::kFrags; ++f)
-          k[f] = k_s[buf][row * kRow + ((f * 4 + g) ^ (n & kSwizzle))];
+          k[f] = k_s[buf][row * kRow + ((4 * f + g) ^ (n & kSwizzle))];
         Q.score(p, t, k, a.scale_log2);
       }
       const unsigned char* vp = reinterpret_cast<const unsigned char*>(v_s[buf]);
 #pragma unroll
       for (int t = 0; t < X::kSub; ++t)
-        X::load_v(v, t, vp + (h * kStep + 16 * t) * kRow * 16, X::v_lane(n, g));
+        X::template load_v<false>(v, t, vp + (h * kStep + 16 * t) * kRow * 16, X::v_lane(n, g));
       const unsigned have = static_cast<unsigned>(here >> (h * kStep));
       if (j + kStep > call.c || (have & (X::kSub == 2 ? ~0u : 0xffffu)) != (X::kSub == 2 ? ~0u : 0xffffu)) {
         const unsigned any = Q.visible(j, end, have);
@@ -694,7 +732,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) Q.sum[m] = rows_sum(Q.sum[m]);
-  Q.store(a, x.split);
+  Q.store(a, call, x.kvh, first + wave * MT * 16, x.split);
 }
 
 // Joins the pieces of every row and head: one wave each, in the pieces' order.
@@ -729,11 +767,20 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
     l = l * f + sum;
 #pragma unroll
     for (int t = 0; t < kPer; ++t) o[t] *= f;
-    for (int s = 0; s < many; ++s) {
-      const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
-      const float* p = a.part_o + ((s0 + s) * a.row_heads + r) * D + lane * kPer;
+    for (int s = 0; s < many; s += kJoinAhead) {
+      float p[kJoinAhead][kPer];
 #pragma unroll
-      for (int t = 0; t < kPer; ++t) o[t] += p[t] * ws;
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float* from = a.part_o + ((s0 + min(s + e, many - 1)) * a.row_heads + r) * D + lane * kPer;
+#pragma unroll
+        for (int t = 0; t < kPer; ++t) p[e][t] = from[t];
+      }
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), (s + e) & 63));
+#pragma unroll
+        for (int t = 0; t < kPer; ++t) o[t] += s + e < many ? p[e][t] * ws : 0.f;
+      }
     }
   }
   const float f = l > 0.f ? 1.f / l : 0.f;
@@ -756,9 +803,10 @@ struct Shape {
 
 Shape attend_shape(int tiles, int dtype) {
   if (tiles <= 1) return Shape{1, false};
-  if (tiles <= 2) return Shape{2, false};
   // (float32 operands of two tiles a wave do not fit the registers of two waves a SIMD.)
-  if (tiles <= 4 || dtype == WF_F32) return Shape{1, true};
+  if (dtype == WF_F32) return Shape{1, true};
+  if (tiles <= 2) return Shape{2, false};
+  if (tiles <= 4) return Shape{1, true};
   return Shape{2, true};
 }
 
@@ -767,12 +815,14 @@ void launch_typed(const AttendArgs& a, Shape shape, int64_t blocks, hipStream_t 
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   if (!shape.wide && shape.mt == 1) {
     hipLaunchKernelGGL((attend_kernel<DT, D, 1>), grid, block, 0, stream, a);
-  } else if (!shape.wide) {
-    hipLaunchKernelGGL((attend_kernel<DT, D, 2>), grid, block, 0, stream, a);
   } else if (shape.mt == 1) {
     hipLaunchKernelGGL((attend_wide_kernel<DT, D, 1>), grid, block, 0, stream, a);
   } else if constexpr (DT == WF_BF16) {
-    hipLaunchKernelGGL((attend_wide_kernel<DT, D, 2>), grid, block, 0, stream, a);
+    if (shape.wide) {
+      hipLaunchKernelGGL((attend_wide_kernel<DT, D, 2>), grid, block, 0, stream, a);
+    } else {
+      hipLaunchKernelGGL((attend_kernel<DT, D, 2>), grid, block, 0, stream, a);
+    }
   }
 }
 
@@ -803,7 +853,8 @@ AttendPlan attend_plan(const wf_page_cache& cache, const RowsArgs& rows, int32_t
   most = most < room ? most : room;
   const int64_t one =
       static_cast<int64_t>(rows.B) * cache.heads * query_groups(cache, rows, q_heads);
-  int64_t splits = (kTargetBlocks + one - 1) / one;
+  const bool wide = attend_shape(query_tiles(cache, rows, q_heads), cache.dtype).wide;
+  int64_t splits = ((wide ? kTargetWide : kTargetBlocks) + one - 1) / one;
   int64_t span = (most + splits - 1) / splits;
   span = (span + kMinSpan - 1) / kMinSpan * kMinSpan;
   span = span < kMinSpan ? kMinSpan : span;
@@ -814,8 +865,8 @@ AttendPlan attend_plan(const wf_page_cache& cache, const RowsArgs& rows, int32_t
 int64_t attend_blocks(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
                       int32_t max_context) {
   const AttendPlan p = attend_plan(cache, rows, q_heads, max_context);
-  const int64_t units = static_cast<int64_t>(rows.B) * cache.heads * p.splits;
-  return (units + 7) / 8 * 8 * query_groups(cache, rows, q_heads);
+  const int64_t pieces = static_cast<int64_t>(rows.B) * p.splits;
+  return (pieces + 7) / 8 * 8 * cache.heads * query_groups(cache, rows, q_heads);
 }
 
 size_t attend_workspace(const wf_page_cache& cache, const RowsArgs& rows, int32_t q_heads,
@@ -855,7 +906,6 @@ hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
   a.splits = plan.splits;
   a.span = plan.span;
   a.mgroups = query_groups(cache, rows, q_heads);
-  a.units = static_cast<int64_t>(rows.B) * cache.heads * plan.splits;
   a.row_heads = total_rows * q_heads;
   a.part_o = static_cast<float*>(workspace);
   if (plan.splits > 1)
