@@ -1,5 +1,6 @@
 // C ABI of the calls around a round: host-side validation and launches.  As in
 // api.hip, every check runs before any HIP call.
+#include <math.h>
 #include <stdint.h>
 
 #include "rounds.h"
@@ -280,7 +281,8 @@ int32_t whiflash_attend(const void* q, int64_t q_row_stride, int32_t q_heads,
   wf::RowsArgs a{};
   int32_t s = check_cache_rows(cache, rows, &total, &a);
   if (s != WF_OK) return s;
-  if (layer < 0 || layer >= cache->layers || !attend_sizes_ok(cache, q_heads, max_context))
+  if (layer < 0 || layer >= cache->layers || !attend_sizes_ok(cache, q_heads, max_context) ||
+      !isfinite(scale))
     return WF_ERR_SHAPE;
   const int64_t width = static_cast<int64_t>(q_heads) * cache->head_dim;
   if ((s = check_vectors(q, cache->dtype, total, width, q_row_stride)) != WF_OK) return s;

@@ -28,8 +28,9 @@ constexpr float kLowest = -3.0e38f;  // a maximum of nothing: finite, so that no
 // stay below 2^8, and most tiles need no rescaling.
 constexpr float kSlack = 8.f;
 constexpr int kMinSpan = 128;
-constexpr int kTargetBlocks = 2048;
-constexpr int kTargetWide = 512;   // two workgroups a CU fit
+constexpr int kSlots = 512;        // workgroups that run at a time: two a CU
+constexpr int kStart = 256;        // the start and end of a workgroup, in positions
+constexpr int kMaxSplits = 512;
 constexpr int kJoinAhead = 8;      // pieces whose outputs are fetched at once
 
 struct AttendArgs {
@@ -107,6 +108,7 @@ struct Ops;
 template <int D>
 struct Ops<WF_BF16, D> {
   static constexpr int kSub = 2;
+  static constexpr bool kSums = true;    // outputs() adds up the weights too
   static constexpr int kFrags = D / 32;  // 16-byte operand vectors of a query or key
   static constexpr int kOut = D / 16;    // output tiles
   static constexpr int kBytes = 2;
@@ -149,7 +151,8 @@ struct Ops<WF_BF16, D> {
   }
   // o += V^T P^T for MT query tiles; p[m][t][i] the weights.
   template <int MT>
-  __device__ static inline void outputs(f32x4 (*o)[kOut], const V& v, const float (*p)[kSub][4]) {
+  __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4* sum, const V& v,
+                                        const float (*p)[kSub][4]) {
     bf16x8 pb[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -157,6 +160,11 @@ struct Ops<WF_BF16, D> {
                        pack_bf16(p[m][1][0], p[m][1][1]), pack_bf16(p[m][1][2], p[m][1][3])};
       pb[m] = __builtin_bit_cast(bf16x8, x);
     }
+    // The sums of the rounded weights: a product with ones, in place of 8 additions.
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pb[m], sum[m], 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
       // Element j of each position's dimensions, two positions a word.
@@ -182,6 +190,7 @@ struct Ops<WF_BF16, D> {
 template <int D>
 struct Ops<WF_F32, D> {
   static constexpr int kSub = 1;
+  static constexpr bool kSums = false;
   static constexpr int kFrags = D / 16;
   static constexpr int kOut = D / 16;
   static constexpr int kBytes = 4;
@@ -215,7 +224,8 @@ struct Ops<WF_F32, D> {
     for (int h = 0; h < D / 64; ++h) v.w[i][h] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   template <int MT>
-  __device__ static inline void outputs(f32x4 (*o)[kOut], const V& v, const float (*p)[kSub][4]) {
+  __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4*, const V& v,
+                                        const float (*p)[kSub][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -291,7 +301,8 @@ struct Queries {
   using X = Ops<DT, D>;
   u32x4 q[MT][X::kFrags];
   f32x4 o[MT][X::kOut];
-  float mx[MT], sum[MT];
+  float mx[MT];
+  f32x4 sum[MT];  // element 0: l, where kSums; else this lane's part of it
   int row[MT];  // row of the round, -1 past the last query
 
   __device__ inline void load(const AttendArgs& a, const SeqCall& call, int kvh, int first) {
@@ -311,7 +322,7 @@ struct Queries {
           q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + (4 * f + g) * 16), a.flip);
       }
       mx[m] = kLowest;
-      sum[m] = 0.f;
+      sum[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < X::kOut; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -319,13 +330,13 @@ struct Queries {
 
   using Weights = float[MT][X::kSub][4];
 
-  // The scores of sub-tile t, in base 2.
-  __device__ inline void score(Weights& p, int t, const u32x4* k, float scale) const {
+  // The products q . k of sub-tile t.
+  __device__ inline void score(Weights& p, int t, const u32x4* k) const {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const f32x4 s = X::scores(k, q[m]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[m][t][i] = s[i] * scale;
+      for (int i = 0; i < 4; ++i) p[m][t][i] = s[i];
     }
   }
 
@@ -358,8 +369,10 @@ struct Queries {
     }
   }
 
-  // Scores to weights, with the running maxima and sums.
-  __device__ inline void soften(Weights& p) {
+  // Products to weights 2^(scale q . k - m), with the running maxima (of the scaled
+  // products; scale > 0, its sign is in q) and, where the output product does not give
+  // them, the sums.
+  __device__ inline void soften(Weights& p, float scale) {
     bool grown = false;
     float top[MT];
 #pragma unroll
@@ -369,7 +382,7 @@ struct Queries {
       for (int t = 0; t < X::kSub; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x = fmaxf(x, p[m][t][i]);
-      top[m] = rows_max(x);
+      top[m] = rows_max(x) * scale;
       grown = grown || top[m] > mx[m] + kSlack;
     }
     if (__any(grown)) {
@@ -389,14 +402,13 @@ struct Queries {
       for (int t = 0; t < X::kSub; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          p[m][t][i] = __builtin_amdgcn_exp2f(p[m][t][i] - mx[m]);
-          sum[m] += p[m][t][i];
+          p[m][t][i] = __builtin_amdgcn_exp2f(fmaf(p[m][t][i], scale, -mx[m]));
+          if constexpr (!X::kSums) sum[m][0] += p[m][t][i];
         }
     }
   }
 
-  // The result of a piece: the output if it is the only one, else its part.  Each of a
-  // query's four lanes has summed its own positions.
+  // The result of a piece: the output if it is the only one, else its part.
   __device__ inline void store(const AttendArgs& a, const SeqCall& call, int kvh, int first,
                                int split) const {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
@@ -406,11 +418,11 @@ struct Queries {
       const int64_t to = (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_heads +
                          kvh * a.group + (first + 16 * m + n) % a.group;
       if (a.splits == 1) {
-        store_query<DT, D>(a.out + to * D * X::kBytes, o[m], g, sum[m] > 0.f ? 1.f / sum[m] : 0.f);
+        store_query<DT, D>(a.out + to * D * X::kBytes, o[m], g, sum[m][0] > 0.f ? 1.f / sum[m][0] : 0.f);
       } else {
         const int64_t at = split * a.row_heads + to;
         store_partial<DT, D>(a.part_o + at * D, o[m], g);
-        if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m]);
+        if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m][0]);
       }
     }
   }
@@ -567,7 +579,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 #pragma unroll
       for (int f = 0; f < X::kFrags; ++f)
         kf[f] = share_s.k[wave][(16 * t + n) * kRow + ((4 * f + g) ^ (n & kSwizzle))];
-      Q.score(p, t, kf, a.scale_log2);
+      Q.score(p, t, kf);
     }
     wave_sync();
     if (j0 + kTile > call.c || here != (X::kSub == 2 ? ~0u : 0xffffu)) {
@@ -580,12 +592,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
         for (int i = 0; i < 4; ++i)
           if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
     }
-    Q.soften(p);
-    X::template outputs<MT>(Q.o, v, p);
+    Q.soften(p, a.scale_log2);
+    X::template outputs<MT>(Q.o, Q.sum, v, p);
     if (more) load_v();
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) Q.sum[m] = rows_sum(Q.sum[m]);
+  for (int m = 0; m < MT; ++m)
+    if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
 
   // The waves join, halves at a time.
 #pragma unroll
@@ -594,7 +607,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     if (wave >= half && wave < 2 * half) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        share_s.join.ml[wave - half][m][lane] = make_float2(Q.mx[m], Q.sum[m]);
+        share_s.join.ml[wave - half][m][lane] = make_float2(Q.mx[m], Q.sum[m][0]);
 #pragma unroll
         for (int j = 0; j < X::kOut; ++j) share_s.join.o[wave - half][m * X::kOut + j][lane] = Q.o[m][j];
       }
@@ -608,7 +621,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
         const float fa = __builtin_amdgcn_exp2f(Q.mx[m] - now);
         const float fb = __builtin_amdgcn_exp2f(y.x - now);
         Q.mx[m] = now;
-        Q.sum[m] = Q.sum[m] * fa + y.y * fb;
+        Q.sum[m][0] = Q.sum[m][0] * fa + y.y * fb;
 #pragma unroll
         for (int j = 0; j < X::kOut; ++j)
           Q.o[m][j] = Q.o[m][j] * fa + share_s.join.o[wave][m * X::kOut + j][lane] * fb;
@@ -638,6 +651,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
   const SeqCall call = seq_call(a, x.b);
   const int rows = call.q.n, first = x.mg * kWaves * MT * 16;
   if (first >= rows * a.group) return;
+  // Where the last waves have no query, two workgroups of a CU leave different SIMDs idle
+  // (an XCD's 32 CUs get one workgroup each before any gets a second).
+  const int set = (wave + (blockIdx.x >> 8 & 1) * 2) % kWaves;
+  const int mine = first + set * MT * 16;
+  const bool work = mine < rows * a.group;
   const int end = call.c < 0 ? 0 : call.c + rows;
   const int k0 = x.split * a.span;
   if (x.split > 0 && k0 >= end) return;
@@ -647,7 +665,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
     for (int u = 1 + tid; u < rows; u += kThreads)
       par_s[u] = static_cast<int16_t>(node_parent(a.rows, x.b, true, u));
   Queries<DT, D, MT> Q;
-  Q.load(a, call, x.kvh, first + wave * MT * 16);
+  Q.load(a, call, x.kvh, mine);
 
   const int64_t head_bytes = static_cast<int64_t>(x.kvh) * D * X::kBytes << a.page_log;
   const int in_page = (1 << a.page_log) - 1;
@@ -697,7 +715,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = j0 + h * kStep;
-      if (j >= k1) break;
+      if (j >= k1 || !work) break;
       typename Queries<DT, D, MT>::Weights p;
       typename X::V v;
 #pragma unroll
@@ -707,7 +725,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
 #pragma unroll
         for (int f = 0; f < X::kFrags; ++f)
           k[f] = k_s[buf][row * kRow + ((4 * f + g) ^ (n & kSwizzle))];
-        Q.score(p, t, k, a.scale_log2);
+        Q.score(p, t, k);
       }
       const unsigned char* vp = reinterpret_cast<const unsigned char*>(v_s[buf]);
 #pragma unroll
@@ -723,16 +741,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
           for (int i = 0; i < 4; ++i)
             if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
       }
-      Q.soften(p);
-      X::template outputs<MT>(Q.o, v, p);
+      Q.soften(p, a.scale_log2);
+      X::template outputs<MT>(Q.o, Q.sum, v, p);
     }
     if (more) put(buf ^ 1);
     __syncthreads();
     buf ^= 1;
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) Q.sum[m] = rows_sum(Q.sum[m]);
-  Q.store(a, call, x.kvh, first + wave * MT * 16, x.split);
+  for (int m = 0; m < MT; ++m)
+    if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
+  Q.store(a, call, x.kvh, mine, x.split);
 }
 
 // Joins the pieces of every row and head: one wave each, in the pieces' order.
@@ -853,8 +872,20 @@ AttendPlan attend_plan(const wf_page_cache& cache, const RowsArgs& rows, int32_t
   most = most < room ? most : room;
   const int64_t one =
       static_cast<int64_t>(rows.B) * cache.heads * query_groups(cache, rows, q_heads);
-  const bool wide = attend_shape(query_tiles(cache, rows, q_heads), cache.dtype).wide;
-  int64_t splits = ((wide ? kTargetWide : kTargetBlocks) + one - 1) / one;
+  // Rounds of workgroups that the card's slots hold at a time, each as long as a piece's
+  // positions, its start and end, and its part written and read again (all in positions).
+  const Shape shape = attend_shape(query_tiles(cache, rows, q_heads), cache.dtype);
+  const int64_t queries = 16 * shape.mt * (shape.wide ? kWaves : 1);
+  const int64_t part = queries * 8 / (cache.dtype == WF_BF16 ? 4 : 8);
+  int64_t splits = 1, best = INT64_MAX;
+  for (int64_t s = 1; s == 1 || (s <= kMaxSplits && most >= s * kMinSpan); ++s) {
+    const int64_t rounds = (one * s + kSlots - 1) / kSlots;
+    const int64_t cost = rounds * (most / s + kStart + (s > 1 ? part : 0));
+    if (cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
   int64_t span = (most + splits - 1) / splits;
   span = (span + kMinSpan - 1) / kMinSpan * kMinSpan;
   span = span < kMinSpan ? kMinSpan : span;
@@ -900,7 +931,8 @@ hipError_t launch_attend(const void* q, int64_t q_stride, int32_t q_heads,
   a.context = cache.context;
   a.seq = seq;
   a.max_context = max_context;
-  a.scale_log2 = fabsf(scale) * kLog2E;
+  // Above zero, so that a score of -inf stays one: 1e-30 makes all weights equal too.
+  a.scale_log2 = fmaxf(fabsf(scale) * kLog2E, 1e-30f);
   a.flip = scale < 0.f ? (cache.dtype == WF_BF16 ? 0x80008000u : 0x80000000u) : 0u;
   a.out = static_cast<unsigned char*>(out);
   a.splits = plan.splits;

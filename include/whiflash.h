@@ -711,10 +711,10 @@ size_t whiflash_attend_workspace_bytes(const wf_page_cache* cache, const wf_roun
  *   out[r, h] = sum_j p_j v_j,  p = softmax over the seen j of scale * q[r, h] . k_j
  * q: rows of q_heads * head_dim elements of the cache's dtype, q_row_stride elements
  * apart; out [rows, q_heads, head_dim] of the same dtype.  q_heads is a multiple of
- * heads.  max_context: no context is larger (it sizes the launch).
+ * heads, scale is finite.  max_context: no context is larger (it sizes the launch).
  *   Scores, maxima and sums are float32; for bfloat16 the weights p (relative to the
- * largest) are rounded to bfloat16 before they multiply v, as the matrix units take
- * them.  The order of all sums is fixed: results are reproducible bit by bit.
+ * largest) are rounded to bfloat16 before they multiply v and are summed, as the matrix
+ * units take them.  The order of all sums is fixed: results are reproducible bit by bit.
  *   Positions without a page (a table entry outside [0, pages)) are not seen.  A row
  * that sees nothing gets zeros, and so do the rows of a sequence outside [0, seqs), or
  * whose context is negative, above max_context or leaves its rows no room in max_pages
