@@ -682,8 +682,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
       const int64_t at = max(id, 0) * a.page_bytes + head_bytes +
                          static_cast<int64_t>((j + 16 * sub) & in_page) * (D * X::kBytes);
       const unsigned off = ((row & 15) * kRow + piece) * 16;
-      stage_k[i] = *reinterpret_cast<const u32x4*>(a.k + at + off);
-      stage_v[i] = *reinterpret_cast<const u32x4*>(a.v + at + off);
+      stage_k[i] = load16(reinterpret_cast<const u32x4*>(a.k + at + off));
+      stage_v[i] = load16(reinterpret_cast<const u32x4*>(a.v + at + off));
     }
     unsigned long long pages = 0;
 #pragma unroll
@@ -834,7 +834,7 @@ void launch_typed(const AttendArgs& a, Shape shape, int64_t blocks, hipStream_t 
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   if (!shape.wide && shape.mt == 1) {
     hipLaunchKernelGGL((attend_kernel<DT, D, 1>), grid, block, 0, stream, a);
-  } else if (shape.mt == 1) {
+  } else if (shape.mt == 1 && shape.wide) {
     hipLaunchKernelGGL((attend_wide_kernel<DT, D, 1>), grid, block, 0, stream, a);
   } else if constexpr (DT == WF_BF16) {
     if (shape.wide) {
