@@ -12,8 +12,8 @@ import ctypes
 
 import torch
 
-from ._binding import (_check, _device_tensor, _dtype_code, _i32, _on, _opt_out,
-                       _out, _rows_view, _workspace, lib)
+from ._binding import (_check, _device_tensor, _dtype_code, _i32, _opt_out, _out, _rows_view,
+                       _workspace, lib)
 
 ROWS_CHAIN, ROWS_TREE, ROWS_ROUTED = 0, 1, 2
 
@@ -73,53 +73,63 @@ def functions():
     return _FN
 
 
-class _Run:
-    """Where a call runs: its tensors' device made current, and its stream, so that what the
-    call allocates belongs to the stream that uses it."""
+_I32, _F32 = torch.int32, torch.float32
 
-    __slots__ = ("stream", "_was", "_on", "_index")
 
-    def __init__(self, device, stream):
-        self._index = device.index
-        self._on = None
-        self._was = None
-        if stream is not None:
-            self._on = torch.cuda.stream(stream)
-            self.stream = stream.cuda_stream
+def _enter(index: int, stream):
+    """Where a call runs: (its raw stream, a context to leave or None).  The tensors' device is
+    made current, and a stream given is too, so that what the call allocates belongs to the
+    stream that uses it."""
+    if stream is None:
+        if torch._C._cuda_getDevice() == index:
+            return torch._C._cuda_getCurrentRawStream(index), None
+        ctx = torch.cuda.device(index)
+        ctx.__enter__()
+        return torch._C._cuda_getCurrentRawStream(index), ctx
+    ctx = torch.cuda.stream(stream)
+    ctx.__enter__()
+    return stream.cuda_stream, ctx
 
-    def __enter__(self):
-        if self._on is not None:
-            self._on.__enter__()
-        else:
-            if torch.cuda.current_device() != self._index:
-                self._was = torch.cuda.device(self._index)
-                self._was.__enter__()
-            self.stream = torch.cuda.current_stream(self._index).cuda_stream
-        return self
 
-    def __exit__(self, *exc):
-        if self._on is not None:
-            self._on.__exit__(*exc)
-        elif self._was is not None:
-            self._was.__exit__(*exc)
+def _leave(ctx) -> None:
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
+
+
+def _ints(t, name: str, n: int, index: int) -> int:
+    """The address of a contiguous int32 tensor of n elements on GPU `index`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.numel() == n
+            and t.get_device() == index and t.is_contiguous()):
+        _i32(t, name, n)
+        raise ValueError(f"{name} is on {t.device}, the call runs on GPU {index}")
+    return t.data_ptr()
+
+
+def _scratch(ws, nbytes: int, device):
+    """(a tensor to hold, its address, its bytes) of a call's workspace."""
+    ws = _workspace(ws, nbytes, device)
+    return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 class RoundRows:
     """The rows of one round (wf_round_rows).  Built by chain_rows, tree_rows and routed_rows;
     holds its tensors."""
 
-    __slots__ = ("struct", "ref", "total", "B", "kind", "device", "tensors", "tokens")
+    __slots__ = ("struct", "ref", "total", "B", "kind", "device", "index", "tensors", "tokens")
 
     def __init__(self, kind, B, K, N, total, device, tokens, **tensors):
+        index = device.index
+        self.kind, self.B, self.total, self.device, self.index = kind, B, total, device, index
+        self.tokens, self.tensors = tokens, tensors
+        s = self.struct = _RowsStruct(kind, B, K, N, 0, total)
         for name, t in tensors.items():
-            if t is not None and t.device != device:
-                raise ValueError(f"{name} is on {t.device}, the round on {device}")
-        Vd = tensors["d2t"].numel() if tensors.get("d2t") is not None else 0
-        self.kind, self.B, self.total, self.device, self.tokens = kind, B, total, device, tokens
-        self.tensors = tensors
-        self.struct = _RowsStruct(kind, B, K, N, Vd, total,
-                                  **{n: t.data_ptr() for n, t in tensors.items() if t is not None})
-        self.ref = ctypes.byref(self.struct)
+            if t is not None:
+                if t.get_device() != index:
+                    raise ValueError(f"{name} is on {t.device}, the round on {device}")
+                setattr(s, name, t.data_ptr())
+                if name == "d2t":
+                    s.Vd = t.numel()
+        self.ref = ctypes.byref(s)
 
 
 def chain_rows(draft) -> RoundRows:
@@ -186,11 +196,11 @@ class LogitRules:
     ids int32, values float32), each sequence's ids ascending; allow [rows, >= ceil(V / 32)]
     int32 bit masks.  Holds its tensors."""
 
-    __slots__ = ("struct", "ref", "tensors", "V", "B", "rows", "device", "words")
+    __slots__ = ("struct", "ref", "tensors", "V", "B", "rows", "index", "words")
 
     def __init__(self, history=None, *, slot=None, penalties=None, bias=None, allow=None):
         s = self.struct = _RulesStruct()
-        self.V = self.B = self.rows = self.words = self.device = None
+        self.V = self.B = self.rows = self.words = self.index = None
         self.tensors = (history, slot, penalties, bias, allow)
         if history is not None:
             s.slots, self.V, s.history_stride = _history(history)
@@ -236,10 +246,10 @@ class LogitRules:
         self.ref = ctypes.byref(s)
 
     def _place(self, t, name):
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the other rules on {self.device}")
+        if self.index is None:
+            self.index = t.get_device()
+        elif t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, the other rules on GPU {self.index}")
 
     def _batch(self, B, name):
         if self.B is None:
@@ -248,8 +258,8 @@ class LogitRules:
             raise ValueError(f"{name} is for {B} sequences, the other rules for {self.B}")
 
     def check(self, rows: RoundRows, V: int) -> None:
-        if self.device is not None and self.device != rows.device:
-            raise ValueError(f"the rules are on {self.device}, the round on {rows.device}")
+        if self.index is not None and self.index != rows.index:
+            raise ValueError(f"the rules are on GPU {self.index}, the round on {rows.device}")
         if self.V is not None and self.V != V:
             raise ValueError(f"the history has {self.V} tokens, the logits {V}")
         if self.B is not None and self.B != rows.B:
@@ -263,8 +273,8 @@ class PageCache:
     (or without layers) float32 or bfloat16, each page contiguous; table [seqs, max_pages], held,
     context [seqs], refs [pages] int32.  Holds its tensors, which the calls update in place."""
 
-    __slots__ = ("struct", "ref", "k", "v", "table", "held", "context", "refs", "device", "dtype",
-                 "heads", "head_dim", "seqs")
+    __slots__ = ("struct", "ref", "k", "v", "table", "held", "context", "refs", "device", "index",
+                 "dtype", "heads", "head_dim", "seqs")
 
     def __init__(self, k, v, table, held, context, refs):
         _device_tensor(k, "k")
@@ -277,21 +287,20 @@ class PageCache:
         if st[-1] != 1 or st[-2] != dim or st[-3] != page * dim:
             raise ValueError("each page of k and v must be contiguous")
         layers = k.shape[0] if k.dim() == 5 else 1
-        _i32(table, "table")
+        _device_tensor(table, "table")
         if table.dim() != 2:
             raise ValueError("table must be [seqs, max_pages]")
         seqs, most = table.shape
-        _i32(held, "held", seqs)
-        _i32(context, "context", seqs)
-        _i32(refs, "refs", pages)
-        self.device = k.device
-        _on(k.device, v=v, table=table, held=held, context=context, refs=refs)
+        index = self.index = k.get_device()
+        if v.get_device() != index:
+            raise ValueError(f"v is on {v.device}, k on {k.device}")
         self.k, self.v, self.table, self.held, self.context, self.refs = k, v, table, held, context, refs
-        self.dtype, self.heads, self.head_dim, self.seqs = k.dtype, heads, dim, seqs
-        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), st[0] if k.dim() == 5 else 0,
-                                   st[-4] if pages > 1 else heads * page * dim, _dtype_code(k), layers,
-                                   pages, heads, page, dim, seqs, most, table.data_ptr(),
-                                   held.data_ptr(), context.data_ptr(), refs.data_ptr())
+        self.device, self.dtype, self.heads, self.head_dim, self.seqs = k.device, k.dtype, heads, dim, seqs
+        self.struct = _CacheStruct(
+            k.data_ptr(), v.data_ptr(), st[0] if k.dim() == 5 else 0,
+            st[-4] if pages > 1 else heads * page * dim, _dtype_code(k), layers, pages, heads, page, dim,
+            seqs, most, _ints(table, "table", seqs * most, index), _ints(held, "held", seqs, index),
+            _ints(context, "context", seqs, index), _ints(refs, "refs", pages, index))
         self.ref = ctypes.byref(self.struct)
 
     @classmethod
@@ -311,7 +320,7 @@ class PageCache:
 
 def _ruled(logits, rows: RoundRows, rules: LogitRules):
     _device_tensor(logits, "logits")
-    if logits.device != rows.device:
+    if logits.get_device() != rows.index:
         raise ValueError(f"logits is on {logits.device}, the round on {rows.device}")
     if not rows.tokens:
         raise ValueError("the rules need the round's draft tokens (draft_ids and d2t)")
@@ -326,71 +335,89 @@ def process_logits(logits, rows: RoundRows, rules: LogitRules, *, out=None, dtyp
     [B, R, V]; out: a tensor of the rows' shape (logits itself for in place), or None for a new
     one of `dtype` whose rows are a multiple of 16 bytes apart.  Returns out."""
     V, stride = _ruled(logits, rows, rules)
-    with _Run(rows.device, stream) as run:
+    raw, ctx = _enter(rows.index, stream)
+    try:
         if out is None:
-            out = torch.empty((rows.total, (V + 7) // 8 * 8), dtype=dtype, device=rows.device)[:, :V]
+            ostride = (V + 7) // 8 * 8
+            out = torch.empty((rows.total, ostride), dtype=dtype, device=rows.device)
+            if ostride != V:
+                out = out[:, :V]
         else:
             _device_tensor(out, "out")
-            if out.device != rows.device:
+            if out.get_device() != rows.index:
                 raise ValueError(f"out is on {out.device}, the round on {rows.device}")
-        oV, ostride = _rows_view(out, rows.total)
-        if oV != V:
-            raise ValueError(f"out has {oV} entries a row, the logits {V}")
+            oV, ostride = _rows_view(out, rows.total)
+            if oV != V:
+                raise ValueError(f"out has {oV} entries a row, the logits {V}")
         _check(functions().process_logits(logits.data_ptr(), _dtype_code(logits), V, stride, rows.ref,
-                                          rules.ref, out.data_ptr(), _dtype_code(out), ostride,
-                                          run.stream))
+                                          rules.ref, out.data_ptr(), _dtype_code(out), ostride, raw))
+    finally:
+        _leave(ctx)
     return out
 
 
 def verify_constrained_workspace_bytes(rows: RoundRows, V: int) -> int:
-    return int(functions().verify_constrained_workspace_bytes(rows.ref, V))
+    return functions().verify_constrained_workspace_bytes(rows.ref, V)
 
 
 def verify_constrained(logits, rows: RoundRows, rules: LogitRules, *, row_argmax=True,
                        accept_len=None, bonus=None, best_node=None, workspace=None, stream=None):
     """Greedy verification of a round under the rules.  Returns (accept_len, bonus, best_node,
-    row_argmax); tokens are -1 where the rules leave nothing."""
+    row_argmax); tokens are -1 where the rules leave nothing.  row_argmax: True to allocate, a
+    tensor to fill, or False/None to skip."""
     V, stride = _ruled(logits, rows, rules)
-    dev = rows.device
-    with _Run(dev, stream) as run:
-        accept_len = _out(accept_len, torch.int32, rows.B, dev, "accept_len")
-        bonus = _out(bonus, torch.int32, rows.B, dev, "bonus")
-        best_node = _out(best_node, torch.int32, rows.B, dev, "best_node")
-        row_argmax = _opt_out(row_argmax, rows.total, dev, "row_argmax")
-        ws = _workspace(workspace, verify_constrained_workspace_bytes(rows, V), dev)
+    dev, B = rows.device, rows.B
+    raw, ctx = _enter(rows.index, stream)
+    try:
+        if accept_len is None and bonus is None and best_node is None and row_argmax is True:
+            accept_len, bonus, best_node, row_argmax = torch.empty(
+                3 * B + rows.total, dtype=_I32, device=dev).split_with_sizes((B, B, B, rows.total))
+        else:
+            accept_len = _out(accept_len, _I32, B, dev, "accept_len")
+            bonus = _out(bonus, _I32, B, dev, "bonus")
+            best_node = _out(best_node, _I32, B, dev, "best_node")
+            row_argmax = _opt_out(row_argmax, rows.total, dev, "row_argmax")
+        ws, at, size = _scratch(workspace, verify_constrained_workspace_bytes(rows, V), dev)
         _check(functions().verify_constrained(
             logits.data_ptr(), _dtype_code(logits), V, stride, rows.ref, rules.ref,
             accept_len.data_ptr(), bonus.data_ptr(), best_node.data_ptr(),
-            None if row_argmax is None else row_argmax.data_ptr(),
-            None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel() * ws.element_size(), run.stream))
+            None if row_argmax is None else row_argmax.data_ptr(), at, size, raw))
+    finally:
+        _leave(ctx)
     return accept_len, bonus, best_node, row_argmax
 
 
 # ----------------------------------------------------------------------------- history
 
 
-def _slot(slot, B, device):
-    if slot is None:
-        return None
-    _i32(slot, "slot", B)
-    _on(device, slot=slot)
-    return slot.data_ptr()
-
-
 def history_prompt(history, tokens, offsets, *, slot=None, stream=None) -> None:
     """Marks prompt tokens: tokens[offsets[b]:offsets[b+1]] in row slot[b] (None: b)."""
     slots, V, stride = _history(history)
+    index = history.get_device()
     _i32(tokens, "tokens")
     _i32(offsets, "offsets")
     if offsets.numel() < 1:
         raise ValueError("offsets must hold B + 1 elements")
     B = offsets.numel() - 1
-    _on(history.device, tokens=tokens, offsets=offsets)
-    with _Run(history.device, stream) as run:
-        _check(functions().history_prompt(history.data_ptr(), slots, V, stride, B,
-                                          _slot(slot, B, history.device), tokens.data_ptr(),
-                                          offsets.data_ptr(), tokens.numel(), run.stream))
+    tokens_at = _ints(tokens, "tokens", tokens.numel(), index)
+    offsets_at = _ints(offsets, "offsets", B + 1, index)
+    slot_at = None if slot is None else _ints(slot, "slot", B, index)
+    raw, ctx = _enter(index, stream)
+    try:
+        _check(functions().history_prompt(history.data_ptr(), slots, V, stride, B, slot_at, tokens_at,
+                                          offsets_at, tokens.numel(), raw))
+    finally:
+        _leave(ctx)
+
+
+def _verified(rows: RoundRows, accept_len, best_node):
+    """The addresses of a verification's accept_len and best_node (None for rounds of chains)."""
+    at = _ints(accept_len, "accept_len", rows.B, rows.index)
+    if best_node is not None:
+        return at, _ints(best_node, "best_node", rows.B, rows.index)
+    if rows.kind != ROWS_CHAIN:
+        raise ValueError("rounds with trees need best_node")
+    return at, None
 
 
 def history_update(history, rows: RoundRows, accept_len, best_node, bonus, *, slot=None,
@@ -398,51 +425,43 @@ def history_update(history, rows: RoundRows, accept_len, best_node, bonus, *, sl
     """Enters a verified round's accepted draft tokens and bonus tokens into the history.
     best_node may be None for rounds of chains."""
     slots, V, stride = _history(history)
+    if history.get_device() != rows.index:
+        raise ValueError(f"history is on {history.device}, the round on {rows.device}")
     if not rows.tokens:
         raise ValueError("the history needs the round's draft tokens (draft_ids and d2t)")
-    _verified(rows, accept_len, best_node)
-    _i32(bonus, "bonus", rows.B)
-    _on(history.device, rows=next(iter(rows.tensors.values())), accept_len=accept_len, bonus=bonus)
-    with _Run(history.device, stream) as run:
-        _check(functions().history_update(
-            history.data_ptr(), slots, V, stride, rows.ref, _slot(slot, rows.B, history.device),
-            accept_len.data_ptr(), None if best_node is None else best_node.data_ptr(),
-            bonus.data_ptr(), run.stream))
-
-
-def _verified(rows, accept_len, best_node):
-    _i32(accept_len, "accept_len", rows.B)
-    _on(rows.device, accept_len=accept_len, best_node=best_node)
-    if best_node is not None:
-        _i32(best_node, "best_node", rows.B)
-    elif rows.kind != ROWS_CHAIN:
-        raise ValueError("rounds with trees need best_node")
+    al, best = _verified(rows, accept_len, best_node)
+    bonus_at = _ints(bonus, "bonus", rows.B, rows.index)
+    slot_at = None if slot is None else _ints(slot, "slot", rows.B, rows.index)
+    raw, ctx = _enter(rows.index, stream)
+    try:
+        _check(functions().history_update(history.data_ptr(), slots, V, stride, rows.ref, slot_at, al,
+                                          best, bonus_at, raw))
+    finally:
+        _leave(ctx)
 
 
 # ----------------------------------------------------------------------------- cache
 
 
 def _cache_call(cache: PageCache, rows: RoundRows, seqs):
-    if rows.device != cache.device:
+    if rows.index != cache.index:
         raise ValueError(f"the round is on {rows.device}, the cache on {cache.device}")
-    if seqs is None:
-        return None
-    _i32(seqs, "seqs", rows.B)
-    _on(cache.device, seqs=seqs)
-    return seqs.data_ptr()
+    return None if seqs is None else _ints(seqs, "seqs", rows.B, cache.index)
 
 
 def _vectors(t, name, rows, heads, cache):
     """Row stride of [rows, heads, head_dim] vectors of the cache's type, each row contiguous."""
     _device_tensor(t, name)
-    if t.device != cache.device or t.dtype != cache.dtype:
+    if t.get_device() != cache.index or t.dtype != cache.dtype:
         raise ValueError(f"{name} must be {cache.dtype} on {cache.device}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != cache.head_dim or \
-            (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != cache.head_dim or \
+            (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {cache.head_dim}]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != cache.head_dim):
+    st = t.stride()
+    if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
         raise ValueError(f"each row of {name} must be contiguous")
-    return t.stride(0) if rows > 1 else t.shape[1] * t.shape[2]
+    return st[0] if rows > 1 else shape[1] * shape[2]
 
 
 def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: int = 0, seqs=None,
@@ -452,13 +471,16 @@ def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: in
     seq = _cache_call(cache, rows, seqs)
     ks = _vectors(k_rows, "k_rows", rows.total, cache.heads, cache)
     vs = _vectors(v_rows, "v_rows", rows.total, cache.heads, cache)
-    with _Run(cache.device, stream) as run:
+    raw, ctx = _enter(cache.index, stream)
+    try:
         _check(functions().cache_append(cache.ref, layer, rows.ref, seq, k_rows.data_ptr(), ks,
-                                        v_rows.data_ptr(), vs, run.stream))
+                                        v_rows.data_ptr(), vs, raw))
+    finally:
+        _leave(ctx)
 
 
 def attend_workspace_bytes(cache: PageCache, rows: RoundRows, q_heads: int, max_context: int) -> int:
-    return int(functions().attend_workspace_bytes(cache.ref, rows.ref, q_heads, max_context))
+    return functions().attend_workspace_bytes(cache.ref, rows.ref, q_heads, max_context)
 
 
 def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, scale=None,
@@ -469,20 +491,22 @@ def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, s
     seq = _cache_call(cache, rows, seqs)
     qs = _vectors(q, "q", rows.total, None, cache)
     heads = q.shape[1]
-    s = cache.struct
     if max_context is None:
-        max_context = s.max_pages * s.page_size
+        max_context = cache.struct.max_pages * cache.struct.page_size
     if scale is None:
         scale = cache.head_dim ** -0.5
-    with _Run(cache.device, stream) as run:
+    raw, ctx = _enter(cache.index, stream)
+    try:
         if out is None:
             out = torch.empty((rows.total, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
         else:
             _out(out, cache.dtype, rows.total * heads * cache.head_dim, cache.device, "out")
-        ws = _workspace(workspace, attend_workspace_bytes(cache, rows, heads, max_context), cache.device)
+        ws, at, size = _scratch(workspace, attend_workspace_bytes(cache, rows, heads, max_context),
+                                cache.device)
         _check(functions().attend(q.data_ptr(), qs, heads, cache.ref, layer, rows.ref, seq, max_context,
-                                  scale, out.data_ptr(), None if ws is None else ws.data_ptr(),
-                                  0 if ws is None else ws.numel() * ws.element_size(), run.stream))
+                                  scale, out.data_ptr(), at, size, raw))
+    finally:
+        _leave(ctx)
     return out
 
 
@@ -492,32 +516,31 @@ def cache_compact(cache: PageCache, rows: RoundRows, accept_len, best_node=None,
     and commits accept_len positions: next_context (None: the cache's context, in place) gets
     context + accept_len.  best_node may be None for rounds of chains."""
     seq = _cache_call(cache, rows, seqs)
-    _verified(rows, accept_len, best_node)
-    if next_context is not None:
-        _i32(next_context, "next_context", cache.seqs)
-        _on(cache.device, next_context=next_context)
-    with _Run(cache.device, stream) as run:
-        _check(functions().cache_compact(cache.ref, rows.ref, seq, accept_len.data_ptr(),
-                                         None if best_node is None else best_node.data_ptr(),
-                                         None if next_context is None else next_context.data_ptr(),
-                                         run.stream))
+    al, best = _verified(rows, accept_len, best_node)
+    after = None if next_context is None else _ints(next_context, "next_context", cache.seqs, cache.index)
+    raw, ctx = _enter(cache.index, stream)
+    try:
+        _check(functions().cache_compact(cache.ref, rows.ref, seq, al, best, after, raw))
+    finally:
+        _leave(ctx)
 
 
 def cache_pages_workspace_bytes(cache: PageCache, n: int) -> int:
-    return int(functions().cache_pages_workspace_bytes(cache.ref, n))
+    return functions().cache_pages_workspace_bytes(cache.ref, n)
 
 
 def _pages_call(fn, cache, first, second, names, status, workspace, stream):
     _i32(first, names[0])
     n = first.numel()
-    _i32(second, names[1], n)
-    _on(cache.device, **{names[0]: first, names[1]: second})
-    with _Run(cache.device, stream) as run:
-        status = _out(status, torch.int32, n, cache.device, "status")
-        ws = _workspace(workspace, cache_pages_workspace_bytes(cache, n), cache.device)
-        _check(fn(cache.ref, n, first.data_ptr(), second.data_ptr(), status.data_ptr(),
-                  None if ws is None else ws.data_ptr(),
-                  0 if ws is None else ws.numel() * ws.element_size(), run.stream))
+    one = _ints(first, names[0], n, cache.index)
+    two = _ints(second, names[1], n, cache.index)
+    raw, ctx = _enter(cache.index, stream)
+    try:
+        status = _out(status, _I32, n, cache.device, "status")
+        ws, at, size = _scratch(workspace, cache_pages_workspace_bytes(cache, n), cache.device)
+        _check(fn(cache.ref, n, one, two, status.data_ptr(), at, size, raw))
+    finally:
+        _leave(ctx)
     return status
 
 
@@ -536,6 +559,10 @@ def cache_reserve(cache: PageCache, count, *, seqs, status=None, workspace=None,
 def cache_free(cache: PageCache, seqs, *, stream=None) -> None:
     """Frees the sequences' pages and empties the sequences."""
     _i32(seqs, "seqs")
-    _on(cache.device, seqs=seqs)
-    with _Run(cache.device, stream) as run:
-        _check(functions().cache_free(cache.ref, seqs.numel(), seqs.data_ptr(), run.stream))
+    n = seqs.numel()
+    at = _ints(seqs, "seqs", n, cache.index)
+    raw, ctx = _enter(cache.index, stream)
+    try:
+        _check(functions().cache_free(cache.ref, n, at, raw))
+    finally:
+        _leave(ctx)

@@ -31,6 +31,7 @@ constexpr int kMinSpan = 128;
 constexpr int kSlots = 512;        // workgroups that run at a time: two a CU
 constexpr int kStart = 256;        // the start and end of a workgroup, in positions
 constexpr int kMaxSplits = 512;
+constexpr int kMaxRounds = 8;
 constexpr int kJoinAhead = 8;      // pieces whose outputs are fetched at once
 
 struct AttendArgs {
@@ -878,9 +879,14 @@ AttendPlan attend_plan(const wf_page_cache& cache, const RowsArgs& rows, int32_t
   const int64_t queries = 16 * shape.mt * (shape.wide ? kWaves : 1);
   const int64_t part = queries * 8 / (cache.dtype == WF_BF16 ? 4 : 8);
   int64_t splits = 1, best = INT64_MAX;
-  for (int64_t s = 1; s == 1 || (s <= kMaxSplits && most >= s * kMinSpan); ++s) {
-    const int64_t rounds = (one * s + kSlots - 1) / kSlots;
-    const int64_t cost = rounds * (most / s + kStart + (s > 1 ? part : 0));
+  for (int64_t rounds = 1; rounds <= kMaxRounds; ++rounds) {
+    // The most pieces that take no more rounds.
+    int64_t s = rounds * kSlots / one;
+    const int64_t cap = most / kMinSpan < kMaxSplits ? most / kMinSpan : kMaxSplits;
+    s = s > cap ? cap : s;
+    if (s < 1) s = 1;
+    const int64_t need = (one * s + kSlots - 1) / kSlots;
+    const int64_t cost = need * (most / s + kStart + (s > 1 ? part : 0));
     if (cost < best) {
       best = cost;
       splits = s;
