@@ -84,32 +84,45 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(
 
 // ---------------------------------------------------------------- compact
 
-constexpr int kMoveBatch = 4;  // rows in flight per thread
+constexpr int kMoveBatch = 8;  // rows in flight per thread
 
-// One workgroup per (sequence, layer and k or v).  Row u_j of the path moves to row
-// j <= u_j.  Each thread owns 16-byte columns and takes the path's rows in order:
-// the destination of step j is a source of steps before j only, so no step overwrites
-// what a later one reads, and no two threads touch one column.
+// One workgroup per (sequence, layer).  Row u_j of the path moves to row j <= u_j.  Each
+// thread owns 16-byte columns (of k, then of v) and takes the path's rows in order: the
+// destination of step j is a source of steps before j only, so no step overwrites what a
+// later one reads, and no two threads touch one column.
+//
+// Bound by chains of reads: those that find the path (the parents are fetched before it is
+// known which are needed), its pages, then the rows.  COMPACT_NOTE
+// With `after` apart from the context the first layer's workgroups commit too.
 __global__ __launch_bounds__(kThreads) void cache_compact_kernel(
     CacheArgs a, RowsArgs rows, const int32_t* __restrict__ seq,
-    const int32_t* __restrict__ accept_len, const int32_t* __restrict__ best_node) {
+    const int32_t* __restrict__ accept_len, const int32_t* __restrict__ best_node,
+    int32_t* __restrict__ after) {
   __shared__ int par_s[kMaxSeqRows];
   __shared__ int64_t src_s[kMaxSeqRows], dst_s[kMaxSeqRows];
   __shared__ int len_s;
   const int b = blockIdx.x, tid = threadIdx.x;
+  for (int u = 1 + tid; u < rows.N; u += kThreads) par_s[u] = node_parent(rows, b, true, u);
   const SeqRows q = seq_rows(rows, b);
   const int s = slot_of(seq, b, a.seqs);
-  if (q.n == 0 || !q.tree || s < 0) return;
-  const int c = a.context[s];
-  const int al = accept_len[b], best = best_node[b];
-  if (c < 0 || al < 1 || al > q.n || best < 0 || best >= q.n) return;
-  for (int u = 1 + tid; u <= best; u += kThreads) par_s[u] = node_parent(rows, b, true, u);
+  if (s < 0) return;
+  const int c = a.context[s], al = accept_len[b], best = best_node[b];
+  const bool commits = after && blockIdx.y == 0 && tid == 0;
+  if (q.n == 0 || !q.tree) {
+    if (commits) after[s] = c >= 0 && q.n > 0 && al >= 0 && al <= q.n ? c + al : c;
+    return;
+  }
+  if (c < 0 || al < 1 || al > q.n || best < 0 || best >= q.n) {
+    if (commits) after[s] = c;
+    return;
+  }
   __syncthreads();
   if (tid == 0) {
     // The path from its end: step al - 1 is the best node.
     int u = best, j = al - 1;
     for (; u > 0 && j > 0; u = par_s[u]) src_s[j--] = u;
     len_s = u == 0 && j == 0 ? al : 0;
+    if (commits) after[s] = c + len_s;
   }
   __syncthreads();
   const int len = len_s;
@@ -120,11 +133,12 @@ __global__ __launch_bounds__(kThreads) void cache_compact_kernel(
     dst_s[j] = from < 0 ? -1 : position_vec(a, s, static_cast<int64_t>(c) + j);
   }
   __syncthreads();
-  u32x4* base = ((blockIdx.y & 1) ? a.v : a.k) + (blockIdx.y >> 1) * a.layer_vecs;
   const int cols = a.heads * a.row_vecs;
-  for (int col = tid; col < cols; col += kThreads) {
+  for (int t = tid; t < 2 * cols; t += kThreads) {
+    const int col = t < cols ? t : t - cols;
     const int h = col / a.row_vecs, e = col - h * a.row_vecs;
-    u32x4* p = base + (static_cast<int64_t>(h) << a.page_log) * a.row_vecs + e;
+    u32x4* p = (t < cols ? a.k : a.v) + blockIdx.y * a.layer_vecs +
+               (static_cast<int64_t>(h) << a.page_log) * a.row_vecs + e;
     for (int j0 = 1; j0 < len; j0 += kMoveBatch) {
       u32x4 d[kMoveBatch];
 #pragma unroll
@@ -137,8 +151,8 @@ __global__ __launch_bounds__(kThreads) void cache_compact_kernel(
   }
 }
 
-// The committed lengths after the moves, in a launch of its own: next_context may be
-// the context that the moves read.
+// The committed lengths in a launch of their own, after the moves: for a round of chains,
+// and where next_context is the context that the moves read.
 __global__ __launch_bounds__(kThreads) void cache_commit_kernel(
     CacheArgs a, RowsArgs rows, const int32_t* __restrict__ seq,
     const int32_t* __restrict__ accept_len, const int32_t* __restrict__ best_node,
@@ -380,15 +394,16 @@ hipError_t launch_cache_compact(const wf_page_cache& cache, const RowsArgs& rows
                                 const int32_t* best_node, int32_t* next_context,
                                 hipStream_t stream) {
   const CacheArgs a = cache_args(cache);
+  int32_t* after = next_context && next_context != cache.context ? next_context : nullptr;
   if (rows.kind != WF_ROWS_CHAIN) {
-    hipLaunchKernelGGL(cache_compact_kernel, dim3(rows.B, 2 * cache.layers), dim3(kThreads), 0,
-                       stream, a, rows, seq, accept_len, best_node);
+    hipLaunchKernelGGL(cache_compact_kernel, dim3(rows.B, cache.layers), dim3(kThreads), 0, stream,
+                       a, rows, seq, accept_len, best_node, after);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || after) return e;
   }
   hipLaunchKernelGGL(cache_commit_kernel, dim3((rows.B + kThreads - 1) / kThreads), dim3(kThreads),
                      0, stream, a, rows, seq, accept_len, best_node,
-                     next_context ? next_context : cache.context);
+                     after ? after : cache.context);
   return hipGetLastError();
 }
 
