@@ -183,9 +183,54 @@ struct Ops<WF_BF16, D> {
     }
   }
   __device__ static inline u32x4 flip_sign(u32x4 x, unsigned bits) { return x ^ bits; }
-  static constexpr unsigned kFlip = 0x80008000u;
-  // Element i of the output tiles holds dimensions (4 g + i) kOut + [0, kOut).
-  __device__ static inline int out_at(int g, int i) { return (4 * g + i) * kOut; }
+
+  // Whether the lane's values hold infinities or NaN.
+  __device__ static inline bool odd(const V& v) {
+    bool x = false;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < kVecV * 2; ++c)
+        x = x || (v.w[r][c] & 0x7f80u) == 0x7f80u || (v.w[r][c] & 0x7f800000u) == 0x7f800000u;
+    return x;
+  }
+  // Outputs that give an infinity or NaN a weight above zero become NaN; then zeros take
+  // its place in v, so that it does not reach the queries that do not see it.
+  template <int MT>
+  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4]) {
+    bf16x8 pb[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      unsigned w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        w[x] = (p[m][x >> 1][2 * x & 3] > 0.f ? 0x3f80u : 0u) |
+               (p[m][x >> 1][(2 * x & 3) + 1] > 0.f ? 0x3f800000u : 0u);
+      pb[m] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+    }
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      const unsigned half = (j & 1) ? 0xffff0000u : 0xffffu, most = 0x7f807f80u & half;
+      unsigned w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        unsigned& a = v.w[2 * x][j >> 1];
+        unsigned& b = v.w[2 * x + 1][j >> 1];
+        const bool oa = (a & most) == most, ob = (b & most) == most;
+        w[x] = (oa ? 0x3f80u : 0u) | (ob ? 0x3f800000u : 0u);
+        a = oa ? a & ~half : a;
+        b = ob ? b & ~half : b;
+      }
+      const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 t = {0.f, 0.f, 0.f, 0.f};
+        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[m], t, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[m][j][i] = t[i] > 0.f ? NAN : o[m][j][i];
+      }
+    }
+  }
 };
 
 template <int D>
@@ -239,7 +284,44 @@ struct Ops<WF_F32, D> {
                                                                    o[m][4 * h + e], 0, 0, 0);
   }
   __device__ static inline u32x4 flip_sign(u32x4 x, unsigned bits) { return x ^ bits; }
-  static constexpr unsigned kFlip = 0x80000000u;
+
+  __device__ static inline bool is_odd(float x) {
+    return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
+  }
+  __device__ static inline bool odd(const V& v) {
+    bool x = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x = x || is_odd(v.w[i][h][e]);
+    return x;
+  }
+  template <int MT>
+  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4]) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f32x4 t[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) t[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool x = is_odd(v.w[i][h][e]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            t[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(x ? 1.f : 0.f, p[m][0][i] > 0.f ? 1.f : 0.f,
+                                                        t[m], 0, 0, 0);
+          v.w[i][h][e] = x ? 0.f : v.w[i][h][e];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[m][4 * h + e][i] = t[m][i] > 0.f ? NAN : o[m][4 * h + e][i];
+      }
+  }
 };
 
 // Writes a lane's outputs of one query tile (element i of every output tile) scaled by
@@ -346,6 +428,21 @@ struct Queries {
   __device__ static inline unsigned visible(int j0, int end, unsigned pages) {
     const int have = min(max(end - j0, 0), 32);
     return pages & (have >= 32 ? ~0u : (1u << have) - 1u);
+  }
+
+  // Takes positions that no query sees out of a tile's scores and values: whatever lies
+  // there must not meet a weight of zero, it may be NaN.
+  __device__ static inline void hide(Weights& p, typename X::V& v, unsigned any) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(any >> (16 * t + 4 * g + i) & 1u)) {
+          X::zero_v(v, t, i);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) p[m][t][i] = -INFINITY;
+        }
   }
 
   // Takes out of a tile's scores what its query does not see: positions outside `any`,
@@ -558,22 +655,19 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     load_k();
     load_v();
   }
-  for (int j0 = w0; j0 < w1; j0 += kTile) {
-    typename Queries<DT, D, MT>::Weights p;
-    // Rows to operand layout through the wave's own LDS.  A row's pieces are exchanged by
-    // the row's number, so that 16 rows' pieces spread over the banks.
+  using Weights = typename Queries<DT, D, MT>::Weights;
+  constexpr unsigned kWhole = X::kSub == 2 ? ~0u : 0xffffu;
+  // Rows to operand layout through the wave's own LDS.  A row's pieces are exchanged by
+  // the row's number, so that 16 rows' pieces spread over the banks.
+  auto share_k = [&]() {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int row = (i * 64 + lane) / kRow, piece = (i * 64 + lane) % kRow;
       share_s.k[wave][row * kRow + (piece ^ (row & kSwizzle))] = k[i];
     }
     wave_sync();
-    const unsigned here = pages;
-    const bool more = j0 + kTile < w1;
-    if (more) {
-      pages = place(j0 + kTile);
-      load_k();
-    }
+  };
+  auto scores = [&](Weights& p) {
 #pragma unroll
     for (int t = 0; t < X::kSub; ++t) {
       u32x4 kf[X::kFrags];
@@ -583,19 +677,41 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
       Q.score(p, t, kf);
     }
     wave_sync();
-    if (j0 + kTile > call.c || here != (X::kSub == 2 ? ~0u : 0xffffu)) {
-      const unsigned any = Q.visible(j0, end, here);
-      Q.mask(p, j0, any, call, par_s);
-      // Whatever lies there must not meet a weight of zero: it may be NaN.
-#pragma unroll
-      for (int t = 0; t < X::kSub; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
+  };
+  // Tiles of committed positions alone, then (without fetching ahead) those with rows of
+  // the round among them.
+  int j0 = w0;
+  for (; j0 + kTile <= min(call.c, w1); j0 += kTile) {
+    Weights p;
+    share_k();
+    const unsigned here = pages;
+    const bool more = j0 + kTile < w1;
+    if (more) {
+      pages = place(j0 + kTile);
+      load_k();
     }
+    scores(p);
+    if (here != kWhole) Q.hide(p, v, here);
     Q.soften(p, a.scale_log2);
     X::template outputs<MT>(Q.o, Q.sum, v, p);
     if (more) load_v();
+  }
+  for (; j0 < w1; j0 += kTile) {
+    Weights p;
+    share_k();
+    scores(p);
+    const unsigned any = Q.visible(j0, end, pages);
+    Q.hide(p, v, any);
+    Q.mask(p, j0, any, call, par_s);
+    Q.soften(p, a.scale_log2);
+    // The round's own values do not meet every query.
+    if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p);
+    X::template outputs<MT>(Q.o, Q.sum, v, p);
+    if (j0 + kTile < w1) {
+      pages = place(j0 + kTile);
+      load_k();
+      load_v();
+    }
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -708,44 +824,67 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
     put(0);
   }
   __syncthreads();
+  using Weights = typename Queries<DT, D, MT>::Weights;
+  constexpr unsigned kWhole = X::kSub == 2 ? ~0u : 0xffffu;
   int buf = 0;
-  for (int j0 = k0; j0 < k1; j0 += kTile) {
+  // The scores and values of half h of the tile in LDS.
+  auto take = [&](Weights& p, typename X::V& v, int h) {
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t) {
+      u32x4 k[X::kFrags];
+      const int row = h * kStep + 16 * t + n;
+#pragma unroll
+      for (int f = 0; f < X::kFrags; ++f) k[f] = k_s[buf][row * kRow + ((4 * f + g) ^ (n & kSwizzle))];
+      Q.score(p, t, k);
+    }
+    const unsigned char* vp = reinterpret_cast<const unsigned char*>(v_s[buf]);
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t)
+      X::template load_v<false>(v, t, vp + (h * kStep + 16 * t) * kRow * 16, X::v_lane(n, g));
+  };
+  // Tiles of committed positions alone, then (without fetching ahead) those with rows of
+  // the round among them.
+  int j0 = k0;
+  for (; j0 + kTile <= min(call.c, k1); j0 += kTile) {
     const unsigned long long here = pages;
     const bool more = j0 + kTile < k1;
     if (more) pages = fetch(j0 + kTile);
+    if (work) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = j0 + h * kStep;
-      if (j >= k1 || !work) break;
-      typename Queries<DT, D, MT>::Weights p;
-      typename X::V v;
-#pragma unroll
-      for (int t = 0; t < X::kSub; ++t) {
-        u32x4 k[X::kFrags];
-        const int row = h * kStep + 16 * t + n;
-#pragma unroll
-        for (int f = 0; f < X::kFrags; ++f)
-          k[f] = k_s[buf][row * kRow + ((4 * f + g) ^ (n & kSwizzle))];
-        Q.score(p, t, k);
+      for (int h = 0; h < 2; ++h) {
+        Weights p;
+        typename X::V v;
+        take(p, v, h);
+        const unsigned have = static_cast<unsigned>(here >> (h * kStep)) & kWhole;
+        if (have != kWhole) Q.hide(p, v, have);
+        Q.soften(p, a.scale_log2);
+        X::template outputs<MT>(Q.o, Q.sum, v, p);
       }
-      const unsigned char* vp = reinterpret_cast<const unsigned char*>(v_s[buf]);
-#pragma unroll
-      for (int t = 0; t < X::kSub; ++t)
-        X::template load_v<false>(v, t, vp + (h * kStep + 16 * t) * kRow * 16, X::v_lane(n, g));
-      const unsigned have = static_cast<unsigned>(here >> (h * kStep));
-      if (j + kStep > call.c || (have & (X::kSub == 2 ? ~0u : 0xffffu)) != (X::kSub == 2 ? ~0u : 0xffffu)) {
-        const unsigned any = Q.visible(j, end, have);
-        Q.mask(p, j, any, call, par_s);
-#pragma unroll
-        for (int t = 0; t < X::kSub; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(any >> (16 * t + 4 * g + i) & 1u)) X::zero_v(v, t, i);
-      }
-      Q.soften(p, a.scale_log2);
-      X::template outputs<MT>(Q.o, Q.sum, v, p);
     }
     if (more) put(buf ^ 1);
+    __syncthreads();
+    buf ^= 1;
+  }
+  for (; j0 < k1; j0 += kTile) {
+#pragma unroll 1
+    for (int h = 0; work && h < 2; ++h) {
+      const int j = j0 + h * kStep;
+      if (j >= k1) break;
+      Weights p;
+      typename X::V v;
+      take(p, v, h);
+      const unsigned any = Q.visible(j, end, static_cast<unsigned>(pages >> (h * kStep)));
+      Q.hide(p, v, any);
+      Q.mask(p, j, any, call, par_s);
+      Q.soften(p, a.scale_log2);
+      // The round's own values do not meet every query.
+      if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p);
+      X::template outputs<MT>(Q.o, Q.sum, v, p);
+    }
+    if (j0 + kTile < k1) {
+      pages = fetch(j0 + kTile);
+      put(buf ^ 1);
+    }
     __syncthreads();
     buf ^= 1;
   }

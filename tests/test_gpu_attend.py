@@ -3,8 +3,10 @@
 Tolerance, per output: with u = 2^-24, A the largest sum |q . k| scale of a row's seen keys and L its
 number of keys, a float32 score is off by at most d = (D + 4) u A, its weight relative to the others
 by 2 d + 8 u (two rounded exponentials and rescalings), and a sum of L such terms by another L u; so
-the output by (2 d + (L + 16) u) sum p |v|.  In bfloat16 each weight is rounded once more before the
-product (2^-8 of it at most) and so is the output: + 2^-8 sum p |v| + 2^-8 |out|."""
+the output by (2 d + (L + 16) u) sum p |v|.  In bfloat16 each weight p is rounded to p (1 + e),
+|e| <= 2^-8, in the product and in the sum: sum p (1 + e) v / sum p (1 + e) is off by
+sum p e (v - out) / sum p (1 + e), so by 2^-8 (sum p |v| + |out|) (and a part in 2^8 of that); the
+output's own rounding adds 2^-8 |out|."""
 
 import numpy as np
 import pytest
@@ -45,7 +47,7 @@ def _check(r, o, cache, q, qx, dtype, *, scale=None, max_context=None, seq=None,
     L = int(o.context.max()) + max(q_.n for q_ in r.seqs) if r.seqs else 0
     tol = (2 * (dim + 4) * u * A + (L + 16) * u) * mag
     if dtype == "bf16":
-        tol = tol + 2.0 ** -8 * mag + 2.0 ** -8 * np.abs(want)
+        tol = tol + (2.0 ** -8 + 2.0 ** -16) * (mag + np.abs(want)) + 2.0 ** -8 * np.abs(want)
     assert np.all(np.isfinite(got))
     off = np.abs(got - want) - tol
     assert np.all(off <= 0), f"worst {off.max():.3e} over, error {np.abs(got - want).max():.3e}"
@@ -125,6 +127,35 @@ def test_bad_data_has_its_defined_result():
     seq = np.array([0, 1, 2, 3, 4, 99, -1, 7])
     _check(r, o, cache, q, qx, "bf16", seq=seq)
     _check(r, o, cache, q, qx, "bf16", seq=seq, max_context=20)   # longer contexts give zeros
+
+
+@pytest.mark.parametrize("dtype,dim", [("f32", 64), ("bf16", 128), ("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("group", [1, 8])
+def test_odd_values_reach_only_the_rows_that_see_them(dtype, dim, group):
+    # Node 2 (a leaf) and node 5 hold infinities and NaN in some dimensions of their values, node 7
+    # in its key: rows on whose path they lie get NaN there, the others are as without them.
+    parent = np.array([[-1, 0, 0, 1, 1, 3, 5, 4, 7, 8, 3]])
+    r = Round("tree", 1, 0, 11, 50, seed=2, parent=parent)
+    o, cache = make_cache(1, 1, 16, dim, [37], 11, 7, dtype=dtype)
+    q, _ = _queries(r.total, group, dim, dtype, 8)
+    clean = host(wf.attend(q, r.rows, cache).float())
+    at = {u: o.where(0, 37 + u) for u in (2, 5, 7)}
+    cache.v[0, at[2][0], 0, at[2][1], 3] = float("nan")
+    cache.v[0, at[2][0], 0, at[2][1], 8] = float("inf")
+    cache.v[0, at[5][0], 0, at[5][1], dim - 1] = float("-inf")
+    cache.k[0, at[7][0], 0, at[7][1], 1] = float("nan")
+    got = host(wf.attend(q, r.rows, cache).float())
+    for u in range(11):
+        path = r.seqs[0].path(u)
+        odd = np.zeros(dim, bool)
+        if 2 in path:
+            odd[[3, 8]] = True
+        if 5 in path:
+            odd[dim - 1] = True
+        if 7 in path:
+            odd[:] = True
+        assert np.all(~np.isfinite(got[u][:, odd])), u
+        assert np.array_equal(got[u][:, ~odd], clean[u][:, ~odd]), u
 
 
 def test_results_repeat_and_do_not_depend_on_the_batch():
