@@ -198,16 +198,6 @@ struct Ops<WF_BF16, D> {
   // its place in v, so that it does not reach the queries that do not see it.
   template <int MT>
   __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4]) {
-    bf16x8 pb[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      unsigned w[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        w[x] = (p[m][x >> 1][2 * x & 3] > 0.f ? 0x3f80u : 0u) |
-               (p[m][x >> 1][(2 * x & 3) + 1] > 0.f ? 0x3f800000u : 0u);
-      pb[m] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
-    }
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
       const unsigned half = (j & 1) ? 0xffff0000u : 0xffffu, most = 0x7f807f80u & half;
@@ -224,8 +214,13 @@ struct Ops<WF_BF16, D> {
       const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          w[x] = (p[m][x >> 1][2 * x & 3] > 0.f ? 0x3f80u : 0u) |
+                 (p[m][x >> 1][(2 * x & 3) + 1] > 0.f ? 0x3f800000u : 0u);
+        const bf16x8 pb = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
         f32x4 t = {0.f, 0.f, 0.f, 0.f};
-        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[m], t, 0, 0, 0);
+        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb, t, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][j][i] = t[i] > 0.f ? NAN : o[m][j][i];
       }
@@ -378,7 +373,7 @@ __device__ inline void wave_sync() {
 }
 
 // What a wave keeps of MT tiles of 16 queries: the queries in operand layout, and for
-// query place n of each tile its row, m, l and O.
+// query place n of each tile m, l and O.
 template <int DT, int D, int MT>
 struct Queries {
   using X = Ops<DT, D>;
@@ -386,22 +381,27 @@ struct Queries {
   f32x4 o[MT][X::kOut];
   float mx[MT];
   f32x4 sum[MT];  // element 0: l, where kSums; else this lane's part of it
-  int row[MT];  // row of the round, -1 past the last query
+  int first;       // the first query
 
-  __device__ inline void load(const AttendArgs& a, const SeqCall& call, int kvh, int first) {
-    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    const int M = call.q.n * a.group;
+  // The lane's query of tile m, or -1 past the last one.
+  __device__ inline int query(const AttendArgs& a, const SeqCall& call, int m) const {
+    const int x = first + 16 * m + static_cast<int>(threadIdx.x & 15);
+    return x < call.q.n * a.group ? x : -1;
+  }
+
+  __device__ inline void load(const AttendArgs& a, const SeqCall& call, int kvh, int from) {
+    const int g = (threadIdx.x & 63) >> 4;
+    first = from;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int x = first + 16 * m + n;
-      row[m] = x < M ? x / a.group : -1;
-      const int h = kvh * a.group + x % a.group;
-      const int64_t r = static_cast<int64_t>(call.q.row0) + max(row[m], 0);
+      const int x = query(a, call, m);
+      const int h = kvh * a.group + max(x, 0) % a.group;
+      const int64_t r = static_cast<int64_t>(call.q.row0) + max(x, 0) / a.group;
       const unsigned char* p = a.q + r * a.q_bytes + h * D * X::kBytes;
 #pragma unroll
       for (int f = 0; f < X::kFrags; ++f) {
         q[m][f] = u32x4{0u, 0u, 0u, 0u};
-        if (x < M)
+        if (x >= 0)
           q[m][f] = X::flip_sign(*reinterpret_cast<const u32x4*>(p + (4 * f + g) * 16), a.flip);
       }
       mx[m] = kLowest;
@@ -447,14 +447,16 @@ struct Queries {
 
   // Takes out of a tile's scores what its query does not see: positions outside `any`,
   // and of the round's own positions those of rows that are not on its path.
-  __device__ inline void mask(Weights& p, int j0, unsigned any, const SeqCall& call,
-                              const int16_t* par) const {
+  __device__ inline void mask(Weights& p, int j0, unsigned any, const AttendArgs& a,
+                              const SeqCall& call, const int16_t* par) const {
     const int g = (threadIdx.x & 63) >> 4;
     const int old = min(max(call.c - j0, 0), 32);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       unsigned see = old >= 32 ? ~0u : (1u << old) - 1u;
-      for (int u = row[m]; u >= 0 && call.c + u >= j0; u = u == 0 ? -1 : call.q.tree ? par[u] : u - 1) {
+      const int x0 = query(a, call, m);
+      for (int u = x0 < 0 ? -1 : x0 / a.group; u >= 0 && call.c + u >= j0;
+           u = u == 0 ? -1 : call.q.tree ? par[u] : u - 1) {
         const int x = call.c + u - j0;
         if (x < 32) see |= 1u << x;
       }
@@ -507,14 +509,14 @@ struct Queries {
   }
 
   // The result of a piece: the output if it is the only one, else its part.
-  __device__ inline void store(const AttendArgs& a, const SeqCall& call, int kvh, int first,
-                               int split) const {
-    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  __device__ inline void store(const AttendArgs& a, const SeqCall& call, int kvh, int split) const {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (row[m] < 0) continue;
-      const int64_t to = (static_cast<int64_t>(call.q.row0) + row[m]) * a.q_heads +
-                         kvh * a.group + (first + 16 * m + n) % a.group;
+      const int x = query(a, call, m);
+      if (x < 0) continue;
+      const int64_t to = (static_cast<int64_t>(call.q.row0) + x / a.group) * a.q_heads +
+                         kvh * a.group + x % a.group;
       if (a.splits == 1) {
         store_query<DT, D>(a.out + to * D * X::kBytes, o[m], g, sum[m][0] > 0.f ? 1.f / sum[m][0] : 0.f);
       } else {
@@ -660,11 +662,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   // Rows to operand layout through the wave's own LDS.  A row's pieces are exchanged by
   // the row's number, so that 16 rows' pieces spread over the banks.
   auto share_k = [&]() {
+    constexpr int kRows = 64 / kRow;  // rows of a piece of all lanes
+    const int row = lane / kRow, piece = (lane % kRow) ^ (row & kSwizzle);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int row = (i * 64 + lane) / kRow, piece = (i * 64 + lane) % kRow;
-      share_s.k[wave][row * kRow + (piece ^ (row & kSwizzle))] = k[i];
-    }
+    for (int i = 0; i < kPieces; ++i)
+      share_s.k[wave][(i * kRows + row) * kRow + (piece ^ (i * kRows & kSwizzle))] = k[i];
     wave_sync();
   };
   auto scores = [&](Weights& p) {
@@ -688,21 +690,24 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     const bool more = j0 + kTile < w1;
     if (more) {
       pages = place(j0 + kTile);
-      load_k();
+      if (MT == 1) load_k();
     }
     scores(p);
+    // (With two query tiles the registers are short until the scores are there.)
+    if (more && MT > 1) load_k();
     if (here != kWhole) Q.hide(p, v, here);
     Q.soften(p, a.scale_log2);
     X::template outputs<MT>(Q.o, Q.sum, v, p);
     if (more) load_v();
   }
+#pragma unroll 1
   for (; j0 < w1; j0 += kTile) {
     Weights p;
     share_k();
     scores(p);
     const unsigned any = Q.visible(j0, end, pages);
     Q.hide(p, v, any);
-    Q.mask(p, j0, any, call, par_s);
+    Q.mask(p, j0, any, a, call, par_s);
     Q.soften(p, a.scale_log2);
     // The round's own values do not meet every query.
     if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p);
@@ -745,7 +750,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
       }
     }
   }
-  if (wave == 0) Q.store(a, call, x.kvh, first, x.split);
+  if (wave == 0) Q.store(a, call, x.kvh, x.split);
 }
 
 // Many queries: one workgroup per (sequence, key-value head, piece, query group) whose
@@ -875,7 +880,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
       take(p, v, h);
       const unsigned any = Q.visible(j, end, static_cast<unsigned>(pages >> (h * kStep)));
       Q.hide(p, v, any);
-      Q.mask(p, j, any, call, par_s);
+      Q.mask(p, j, any, a, call, par_s);
       Q.soften(p, a.scale_log2);
       // The round's own values do not meet every query.
       if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p);
@@ -891,7 +896,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
-  Q.store(a, call, x.kvh, mine, x.split);
+  Q.store(a, call, x.kvh, x.split);
 }
 
 // Joins the pieces of every row and head: one wave each, in the pieces' order.

@@ -1,0 +1,246 @@
+"""The calls around a round used together: several rounds of a small serving loop against the
+oracle, the same calls captured in a graph and replayed, two streams at once, and the handles'
+refusals that need GPU tensors."""
+
+import numpy as np
+import pytest
+import torch
+
+import drafter_routing_verification_amd as wf
+from gpu_helpers import DEV, dev, host
+from oracle import rounds as orc
+from round_helpers import Round, bits, i32, make_cache, make_logits, make_rules, same_cache, stored
+
+pytestmark = pytest.mark.gpu
+
+HEADS, GROUP, DIM, PAGE = 2, 4, 64, 16
+
+
+def _projection(total, seed):
+    """q, k and v of a round's rows as slices of one float32 projection."""
+    x = np.random.default_rng(seed).normal(0, 1, (total, (GROUP + 2) * HEADS, DIM)).astype(np.float32)
+    t = dev(x)
+    cut = [GROUP * HEADS, (GROUP + 1) * HEADS]
+    return (t[:, :cut[0]], t[:, cut[0]:cut[1]], t[:, cut[1]:]), np.split(x, cut, 1)
+
+
+@pytest.mark.parametrize("kind,K,N", [("chain", 4, 0), ("tree", 0, 13), ("routed", 3, 9)])
+def test_a_serving_loop(kind, K, N):
+    # reserve, append, attend, verify under rules, history, compact, then a fork and a free
+    B, V, S = 4, 700, 7
+    o, cache = make_cache(1, HEADS, PAGE, DIM, [5, 16, 33, 0], 0, 3, dtype="f32", spare=40, empty=S - B)
+    seq = np.array([2, 0, 3, 1])
+    slots = B + 1
+    oh = np.zeros((slots, V), np.uint16)
+    gh = torch.zeros(slots, 704, dtype=torch.int16, device=DEV)[:, :V]
+    prompt = np.random.default_rng(1).integers(0, V, 60)
+    offsets = np.array([0, 10, 20, 45, 60])
+    slot = np.array([3, 1, 0, 4])
+    wf.history_prompt(gh, i32(prompt), i32(offsets), slot=i32(slot))
+    orc.history_prompt(oh, prompt, offsets, slot)
+    for turn in range(6):
+        print("turn", turn, flush=True)
+        r = Round(kind, B, K, N, V, seed=turn)
+        most = max(K + 1, N)
+        e = orc.cache_reserve(o, seq, np.full(B, most))
+        assert np.array_equal(host(wf.cache_reserve(cache, i32(np.full(B, most)), seqs=i32(seq))), e) and e.all()
+        (q, k, v), (qx, kx, vx) = _projection(r.total, 50 + turn)
+        wf.cache_append(cache, r.rows, k, v, seqs=i32(seq))
+        orc.cache_append(o, r.seqs, kx, vx, seq=seq)
+        out = wf.attend(q, r.rows, cache, seqs=i32(seq))
+        want = orc.attend(qx, r.seqs, o, DIM ** -0.5, 10 ** 6, seq=seq)
+        mine = r.owned()
+        # Scores of some units over at most 200 keys of unit values: see test_gpu_attend's bound
+        # (2 (D + 4) 2^-24 A + (L + 16) 2^-24) max |v| with A <= 8 * 5 * 64 / 8, max |v| <= 5.
+        assert np.abs(host(out)[mine] - want[mine]).max() < (2 * 68 * 320 + 216) * 2.0 ** -24 * 5
+        o_rules, _ = make_rules(r, 70 + turn, history=False)
+        o_rules.history, o_rules.slot = oh, slot
+        rules = wf.LogitRules(gh, slot=i32(slot), penalties=dev(o_rules.penalties),
+                              bias=(i32(o_rules.bias[0]), i32(o_rules.bias[1]), dev(o_rules.bias[2])),
+                              allow=dev(o_rules.allow.view(np.int32)))
+        raw = make_logits(r, "bf16", 90 + turn)
+        al, bonus, best, t = wf.verify_constrained(stored(raw, "bf16", 704), r.rows, rules)
+        e_al, e_bonus, e_best = (np.zeros(B, np.int64) for _ in range(3))
+        for b, s in enumerate(r.seqs):
+            x = orc.process_rows(bits(raw[s.row0:s.row0 + s.n], "bf16"), b, s, o_rules)
+            e_al[b], e_bonus[b], e_best[b] = orc.verify_seq(s, orc.constrained_tokens(x))
+        for a, e in ((al, e_al), (bonus, e_bonus), (best, e_best)):
+            assert np.array_equal(host(a), e)
+        wf.history_update(gh, r.rows, al, best, bonus, slot=i32(slot))
+        orc.history_update(oh, r.seqs, e_al, e_best, e_bonus, slot)
+        assert np.array_equal(host(gh).view(np.uint16), oh)
+        wf.cache_compact(cache, r.rows, al, best, seqs=i32(seq))
+        orc.cache_compact(o, r.seqs, e_al, e_best, o.context, seq)
+        if turn in (2, 4):   # one sequence is replaced by a fork of another
+            gone, to, new = seq[1], seq[0], next(s for s in range(S) if s not in seq)
+            assert np.array_equal(host(wf.cache_fork(cache, i32([to]), i32([new]))),
+                                  orc.cache_fork(o, np.array([to]), np.array([new])))
+            wf.cache_free(cache, i32([gone]))
+            orc.cache_free(o, np.array([gone]))
+            seq = np.array([seq[0], new, seq[2], seq[3]])
+        same_cache(o, cache)
+
+
+def test_graphs_replay_like_eager_calls():
+    """Two captured chains of calls with buffers and workspaces of their own, replayed several times
+    between eager runs of the same calls; every replay starts from the same state."""
+    made = []
+    for n, kind in enumerate(("chain", "routed")):
+        r = Round(kind, 5, 6, 17, 5003, seed=n)
+        _, rules = make_rules(r, 20 + n)
+        logits = stored(make_logits(r, "bf16", 30 + n), "bf16", 5008)
+        _, cache = make_cache(2, HEADS, PAGE, DIM, [40, 3, 16, 700, 0], 17, 40 + n, dtype="f32", spare=9, empty=2)
+        (q, k, v), _ = _projection(r.total, 60 + n)
+        history, slot = rules.tensors[0], rules.tensors[1]
+        state = [history, cache.k, cache.v, cache.table, cache.held, cache.context, cache.refs]
+        src, dst, room = i32([0, 3]), i32([5, 6]), i32([40, 2])
+        ws = [torch.empty(x, dtype=torch.uint8, device=DEV) for x in (
+            wf.verify_constrained_workspace_bytes(r.rows, 5003),
+            max(256, wf.attend_workspace_bytes(cache, r.rows, GROUP * HEADS, 700)),
+            wf.cache_pages_workspace_bytes(cache, 2))]
+
+        def fn(r=r, rules=rules, logits=logits, cache=cache, q=q, k=k, v=v, history=history, slot=slot,
+               src=src, dst=dst, room=room, ws=ws):
+            wf.cache_append(cache, r.rows, k, v, layer=1)
+            out = wf.attend(q, r.rows, cache, layer=1, max_context=700, workspace=ws[1])
+            done = wf.verify_constrained(logits, r.rows, rules, workspace=ws[0])
+            written = wf.process_logits(logits, r.rows, rules, dtype=torch.bfloat16)
+            wf.history_update(history, r.rows, done[0], done[2], done[1], slot=slot)
+            wf.cache_compact(cache, r.rows, done[0], done[2])
+            forked = wf.cache_fork(cache, src, dst, workspace=ws[2])
+            given = wf.cache_reserve(cache, room, seqs=dst, workspace=ws[2])
+            wf.cache_free(cache, src)
+            return [out, *done, written, forked, given]
+
+        made.append((fn, state, r.owned()))
+    start = [[t.clone() for t in state] for _, state, _ in made]
+
+    def reset():
+        for (_, state, _), old in zip(made, start):
+            for t, x in zip(state, old):
+                t.copy_(x)
+
+    def seen(outs):
+        # rows that no sequence owns are not written
+        shown = []
+        for (_, state, mine), o in zip(made, outs):
+            m = torch.from_numpy(mine).to(DEV)
+            shown.append([o[0][m], *o[1:4], o[4][m], o[5][m], *o[6:], *state])
+        return [[t.clone() for t in x] for x in shown]
+
+    reset()
+    want = seen([fn() for fn, _, _ in made])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for fn, _, _ in made:
+            fn()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = [fn() for fn, _, _ in made]
+    for rep in range(4):
+        print("replay", rep, flush=True)
+        reset()
+        for o in captured:
+            for t in o:
+                t.fill_(-7)
+        g.replay()
+        torch.cuda.synchronize()
+        got = seen(captured)
+        reset()
+        again = seen([fn() for fn, _, _ in made])
+        torch.cuda.synchronize()
+        for k in range(2):
+            for i, (a, b, c) in enumerate(zip(got[k], want[k], again[k])):
+                assert torch.equal(a, b), f"replay {rep}, chain {k}, output {i}"
+                assert torch.equal(c, b), f"eager after replay {rep}, chain {k}, output {i}"
+
+
+def test_two_streams_at_once():
+    work = []
+    for n in range(2):
+        r = Round("tree", 6, 0, 31, 9001, seed=n)
+        _, rules = make_rules(r, n)
+        logits = stored(make_logits(r, "f32", n), "f32", 9004)
+        _, cache = make_cache(1, HEADS, PAGE, DIM, [900] * 6, 31, n, dtype="f32")
+        (q, _, _), _ = _projection(r.total, n)
+        work.append((r, rules, logits, cache, q, torch.cuda.Stream()))
+    alone = []
+    for r, rules, logits, cache, q, _ in work:
+        alone.append([*wf.verify_constrained(logits, r.rows, rules), wf.attend(q, r.rows, cache)])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for r, rules, logits, cache, q, s in work:
+            got.append([*wf.verify_constrained(logits, r.rows, rules, stream=s),
+                        wf.attend(q, r.rows, cache, stream=s)])
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_refusals_of_gpu_tensors():
+    r = Round("tree", 3, 0, 7, 100, seed=1)
+    logits = stored(make_logits(r, "f32", 1), "f32", 104)
+    none = wf.LogitRules()
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    f = lambda *s: torch.zeros(*s, device=DEV)  # noqa: E731
+    bad = [
+        (TypeError, lambda: wf.chain_rows(torch.zeros(2, 3, device=DEV))),
+        (ValueError, lambda: wf.chain_rows(i(6))),
+        (ValueError, lambda: wf.tree_rows(i(2, 3), i(2, 3))),
+        (ValueError, lambda: wf.tree_rows(i(2, 3), i(2, 4), i(5))),
+        (ValueError, lambda: wf.routed_rows(i(3), 4, i(2), i(1, 3), i(2, 3))),
+        (TypeError, lambda: wf.chain_rows(i(3, 2).cpu())),
+        (TypeError, lambda: wf.LogitRules(f(3, 100))),
+        (ValueError, lambda: wf.LogitRules(slot=i(3))),
+        (TypeError, lambda: wf.LogitRules(penalties=f(3, 2))),
+        (ValueError, lambda: wf.LogitRules(penalties=f(3, 3), bias=(i(3), i(1), f(1)))),
+        (ValueError, lambda: wf.LogitRules(bias=(i(4), i(2), f(1)))),
+        (TypeError, lambda: wf.LogitRules(allow=f(3, 4))),
+        (ValueError, lambda: wf.verify_constrained(logits, r.rows, wf.LogitRules(allow=i(20, 4)))),
+        (ValueError, lambda: wf.verify_constrained(logits, r.rows, wf.LogitRules(allow=i(21, 3)))),
+        (ValueError, lambda: wf.verify_constrained(logits, r.rows, wf.LogitRules(penalties=f(2, 3)))),
+        (ValueError, lambda: wf.verify_constrained(logits[:20], r.rows, none)),
+        (ValueError, lambda: wf.verify_constrained(logits, wf.tree_rows(i(3, 7)), none)),
+        (wf.WhiflashError, lambda: wf.verify_constrained(f(21, 101), r.rows, none)),
+        (ValueError, lambda: wf.verify_constrained(logits, r.rows, none,
+                                                   workspace=torch.zeros(8, dtype=torch.uint8, device=DEV))),
+        (ValueError, lambda: wf.process_logits(logits, r.rows, none, out=f(21, 96))),
+        (TypeError, lambda: wf.process_logits(logits.double(), r.rows, none)),
+        (wf.WhiflashError, lambda: wf.process_logits(logits, r.rows, wf.LogitRules(
+            torch.zeros(3, 100, dtype=torch.int16, device=DEV)))),
+        (ValueError, lambda: wf.history_update(torch.zeros(3, 104, dtype=torch.int16, device=DEV), r.rows,
+                                               i(3), None, i(3))),
+    ]
+    _, cache = make_cache(1, 2, 16, 64, [3, 4, 5], 8, 1, dtype="f32")
+    k = lambda *s: torch.zeros(*s, device=DEV)  # noqa: E731
+    bad += [
+        (ValueError, lambda: wf.attend(k(20, 4, 64), r.rows, cache)),
+        (ValueError, lambda: wf.attend(k(21, 4, 32), r.rows, cache)),
+        (ValueError, lambda: wf.attend(k(21, 4, 64).bfloat16(), r.rows, cache)),
+        (wf.WhiflashError, lambda: wf.attend(k(21, 3, 64), r.rows, cache)),
+        (wf.WhiflashError, lambda: wf.attend(k(21, 4, 64), r.rows, cache, layer=1)),
+        (wf.WhiflashError, lambda: wf.attend(k(21, 4, 64), r.rows, cache, scale=float("nan"))),
+        (wf.WhiflashError, lambda: wf.attend(k(21, 4, 64), r.rows, cache, max_context=-1)),
+        (ValueError, lambda: wf.attend(k(21, 64, 4).transpose(1, 2), r.rows, cache)),
+        (ValueError, lambda: wf.attend(k(21, 4, 64), r.rows, cache, seqs=i(2))),
+        (ValueError, lambda: wf.cache_append(cache, r.rows, k(21, 2, 64), k(21, 4, 64))),
+        (ValueError, lambda: wf.cache_compact(cache, r.rows, i(3))),
+        (ValueError, lambda: wf.cache_fork(cache, i(2), i(3))),
+        (TypeError, lambda: wf.cache_free(cache, i(2).long())),
+        (wf.WhiflashError, lambda: wf.attend(k(3, 4, 96), wf.chain_rows(i(3, 0)), wf.PageCache.empty(
+            1, 4, 2, 16, 96, 3, 2, dtype=torch.float32, device=DEV))),
+        (wf.WhiflashError, lambda: wf.cache_free(wf.PageCache.empty(1, 4, 2, 24, 64, 3, 2, device=DEV), i(1))),
+        (ValueError, lambda: wf.PageCache(cache.k, cache.v[:, :2], cache.table, cache.held, cache.context,
+                                          cache.refs)),
+        (ValueError, lambda: wf.PageCache(cache.k.transpose(3, 4), cache.v.transpose(3, 4), cache.table,
+                                          cache.held, cache.context, cache.refs)),
+    ]
+    for n, (error, call) in enumerate(bad):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"call {n} was taken")
+    torch.cuda.synchronize()
