@@ -17,7 +17,11 @@ constexpr int kBiasLds = 256;                     // biases of a chunk that are 
 constexpr int kMaxGroup = 64;                     // rows per workgroup
 constexpr int kListMax = 256;                     // special elements of a wave that are listed
 constexpr int kArgmax = -1;
-constexpr int64_t kRulesBlocks = 8192;            // workgroups of a large launch
+// Workgroups of a large launch.  More make shorter groups (every group reads its history
+// words and works out its special elements anew), fewer leave an uneven end.  128 sequences
+// (half chains of 17 rows, half trees of 61) x 151,936 bf16, and 64 chains x 17 written out:
+// 4,096 397 / 158 us, 8,192 343 / 147, 12,288 328 / 149, 16,384 334 / 149, 24,576 377 / 174.
+constexpr int64_t kRulesBlocks = 12288;
 
 struct RulesArgs {
   RowsArgs rows;
@@ -133,13 +137,26 @@ __device__ inline void store_vec(unsigned char* row, int v, const float* x, int 
 // One workgroup per (sequence, group of rows, chunk of the vocabulary), the group's rows
 // one after the other: a chunk's history words stay in registers for all of them.
 //
-// HBM-bound streaming of the logits.  Nearly all tokens have neither history nor bias
-// and were not drafted in this round, so every element has one "special" bit, worked
-// out once a workgroup: elements without it take the plain path (a masked maximum, or a
-// copy), and each lane handles the special ones of its vectors in a loop of its own.
-// The path's tokens differ from row to row; only elements that some node drafted look
-// them up.  A row's maximum is reduced over the wave first, and only the lanes that hold
-// it look for its index.
+// Streaming of the logits.  Nearly all tokens have neither history nor bias and were not
+// drafted in this round, so every element has one "special" bit, worked out once a
+// workgroup: elements without it take the plain path (a masked maximum, or a copy).  The
+// argmax lists a wave's special elements, so that its lanes share them evenly: the row's
+// vectors pass through LDS, and each lane, which decoded its element once for all rows,
+// picks its logit.  Written out, each lane handles the special elements of its vectors in a
+// loop of its own.  The path's tokens differ from row to row; only elements that some node
+// drafted look them up.  The maximum is reduced over the wave, and its first place found by
+// ballots and in scalar registers.
+//
+// The next row's mask and vectors are fetched before this row is worked on, the mask first:
+// loads return in order, and the mask is needed first.
+//
+// Measured (MI355X, 151,936 bf16 entries): 64 chains x 17 rows written out 147 us, 4.8 TB/s
+// read and written together, the rate of a large copy.  The argmax of 128 sequences (4,992
+// rows, 1.65 GB) 318 us, 5.2 TB/s: bound by its instructions, some 310 vector and 220 scalar
+// ones a wave and row, and by having only 4 waves a SIMD to cover their latencies; without
+// any rule it takes 241 us, against 205 us of the plain sweep.  Fewer registers (5 waves,
+// spilling) 430 us; bit masks that keep the special elements out of an unmasked maximum
+// (137 registers, 3 waves) 416 us.
 template <int DT, int OUT>
 __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
   using E = Elem<DT>;
