@@ -11,6 +11,7 @@ constexpr size_t kWorkspaceAlign = 256;
 constexpr int64_t kMaxBlocks = int64_t{1} << 22;  // x 1024 threads: below 2^32 work items
 
 constexpr int32_t kMaxVocab = 1 << 30;
+constexpr int64_t kMaxPositions = 1 << 30;  // of a sequence: sums of two stay in an int
 
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -127,7 +128,7 @@ int32_t check_cache(const wf_page_cache* c) {
   if (c->layers < 1 || c->pages < 1 || c->heads < 1 || c->heads > 1024 || c->seqs < 1 ||
       c->max_pages < 1 || c->layers > 4096 || (c->head_dim != 64 && c->head_dim != 128) ||
       c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0 ||
-      static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - WHIFLASH_MAX_SEQ_ROWS)
+      static_cast<int64_t>(c->max_pages) * c->page_size > kMaxPositions)
     return WF_ERR_SHAPE;
   const int64_t page = static_cast<int64_t>(c->heads) * c->page_size * c->head_dim;
   if (c->page_stride < page || c->page_stride > INT64_MAX / 16 / c->pages ||
@@ -164,7 +165,7 @@ int32_t check_cache_rows(const wf_page_cache* cache, const wf_round_rows* rows, 
 
 bool attend_sizes_ok(const wf_page_cache* c, int32_t q_heads, int32_t max_context) {
   return q_heads >= 1 && q_heads <= 65535 && q_heads % c->heads == 0 && max_context >= 0 &&
-         max_context <= INT32_MAX - 2 * WHIFLASH_MAX_SEQ_ROWS;
+         max_context <= kMaxPositions;
 }
 
 }  // namespace

@@ -473,10 +473,14 @@ struct Queries {
     for (int m = 0; m < MT; ++m) {
       unsigned see = old >= 32 ? ~0u : (1u << old) - 1u;
       const int x0 = query(a, call, m);
-      for (int u = x0 < 0 ? -1 : x0 / a.group; u >= 0 && call.c + u >= j0;
-           u = u == 0 ? -1 : call.q.tree ? par[u] : u - 1) {
-        const int x = call.c + u - j0;
-        if (x < 32) see |= 1u << x;
+      const int own = x0 < 0 ? -1 : x0 / a.group, last = call.c + own - j0;
+      if (!call.q.tree) {
+        if (own >= 0 && last >= 0) see = last >= 31 ? ~0u : (2u << last) - 1u;
+      } else {
+        for (int u = own; u >= 0 && call.c + u >= j0; u = u == 0 ? -1 : par[u]) {
+          const int x = call.c + u - j0;
+          if (x < 32) see |= 1u << x;
+        }
       }
       see &= any;
 #pragma unroll
@@ -593,6 +597,19 @@ __device__ inline Unit unit_of(const AttendArgs& a) {
   return x;
 }
 
+// What `count` queries from `first` on see of a sequence: positions before `all` are seen by
+// every one of them, positions from `end` on by none.
+struct Sight {
+  int all, end;
+};
+
+__device__ inline Sight sight_of(const AttendArgs& a, const SeqCall& call, int first, int count) {
+  if (call.c < 0) return Sight{-1, 0};
+  if (call.q.tree) return Sight{call.c, call.c + call.q.n};
+  const int last = min(call.q.n * a.group, first + count) - 1;
+  return Sight{call.c + first / a.group + 1, call.c + last / a.group + 1};
+}
+
 // Up to 16 MT queries: one workgroup per (sequence, key-value head, piece, query group),
 // whose four waves share the piece's positions and join their m, l and O in LDS.  Every
 // byte is read once, by loads that take whole lines and do not stay in the caches; the
@@ -618,10 +635,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   const SeqCall call = seq_call(a, x.b);
   const int rows = call.q.n, first = x.mg * MT * 16;
   if (first >= rows * a.group) return;
-  const int end = call.c < 0 ? 0 : call.c + rows;
+  const Sight sight = sight_of(a, call, first, MT * 16);
   const int k0 = x.split * a.span;
-  if (x.split > 0 && k0 >= end) return;
-  const int k1 = min(k0 + a.span, end);
+  if (x.split > 0 && k0 >= sight.end) return;
+  const int k1 = min(k0 + a.span, sight.end);
   // The wave's positions [w0, w1), in whole tiles of the piece.
   const int share = (a.span / kTile + kWaves - 1) / kWaves * kTile;
   const int w0 = min(k0 + wave * share, k1), w1 = min(w0 + share, k1);
@@ -698,10 +715,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     }
     wave_sync();
   };
-  // Tiles of committed positions alone, then (without fetching ahead) those with rows of
-  // the round among them.
+  // Tiles that every query sees, then (without fetching ahead) those that some do not.
   int j0 = w0;
-  for (; j0 + kTile <= min(call.c, w1); j0 += kTile) {
+  for (; j0 + kTile <= min(sight.all, w1); j0 += kTile) {
     Weights p;
     share_k();
     const unsigned here = pages;
@@ -723,7 +739,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     Weights p;
     share_k();
     scores(p);
-    const unsigned any = Q.visible(j0, end, pages);
+    const unsigned any = Q.visible(j0, sight.end, pages);
     Q.hide(p, v, any);
     Q.mask(p, j0, any, a, call, par_s);
     Q.soften(p, a.scale_log2);
@@ -796,10 +812,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
   const int set = (wave + (blockIdx.x >> 8 & 1) * 2) % kWaves;
   const int mine = first + set * MT * 16;
   const bool work = mine < rows * a.group;
-  const int end = call.c < 0 ? 0 : call.c + rows;
+  const Sight sight = sight_of(a, call, first, kWaves * MT * 16);
   const int k0 = x.split * a.span;
-  if (x.split > 0 && k0 >= end) return;
-  const int k1 = min(k0 + a.span, end);
+  if (x.split > 0 && k0 >= sight.end) return;
+  const int k1 = min(k0 + a.span, sight.end);
   PageWalk walk(a, call, k0, k1);
   if (call.q.tree && k1 > call.c && call.c >= 0)
     for (int u = 1 + tid; u < rows; u += kThreads)
@@ -865,10 +881,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
     for (int t = 0; t < X::kSub; ++t)
       X::template load_v<false>(v, t, vp + (h * kStep + 16 * t) * kRow * 16, X::v_lane(n, g));
   };
-  // Tiles of committed positions alone, then (without fetching ahead) those with rows of
-  // the round among them.
+  // Tiles that every query sees, then (without fetching ahead) those that some do not.
   int j0 = k0;
-  for (; j0 + kTile <= min(call.c, k1); j0 += kTile) {
+  for (; j0 + kTile <= min(sight.all, k1); j0 += kTile) {
     const unsigned long long here = pages;
     const bool more = j0 + kTile < k1;
     if (more) pages = fetch(j0 + kTile);
@@ -896,7 +911,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
       Weights p;
       typename X::V v;
       take(p, v, h);
-      const unsigned any = Q.visible(j, end, static_cast<unsigned>(pages >> (h * kStep)));
+      const unsigned any = Q.visible(j, sight.end, static_cast<unsigned>(pages >> (h * kStep)));
       Q.hide(p, v, any);
       Q.mask(p, j, any, a, call, par_s);
       Q.soften(p, a.scale_log2);
@@ -930,7 +945,8 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
   const SeqCall call = seq_call(a, b);
   if (i >= call.q.n) return;
   const int64_t r = (static_cast<int64_t>(call.q.row0) + i) * a.q_heads + h;
-  const int end = call.c < 0 ? 0 : call.c + call.q.n;
+  // A chain's row is not in the pieces past its own position.
+  const int end = call.c < 0 ? 0 : call.c + (call.q.tree ? call.q.n : i + 1);
   const int used = end > 0 ? (end + a.span - 1) / a.span : 0;
   // Lane s holds piece s's maximum and sum, 64 pieces at a time, so that the loads of
   // the outputs depend on nothing.

@@ -664,7 +664,7 @@ int32_t whiflash_history_update(uint16_t* history, int32_t slots, int32_t V, int
  *   k[l * layer_stride + p * page_stride + (h * page_size + o) * head_dim + d]
  * (strides in elements, the page's stride and the base multiples of 16 bytes; v
  * alike).  dtype WF_F32 or WF_BF16; head_dim 64 or 128; page_size a power of two
- * from 16 to 1024.
+ * from 16 to 1024; max_pages * page_size at most 2^30.
  *   table [seqs, max_pages]: the pages of each sequence's positions (position j in
  *     page table[s][j / page_size]); -1 where it holds none;
  *   held [seqs]: how many entries of its table row hold pages;
