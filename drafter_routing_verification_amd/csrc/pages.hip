@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kAllocThreads) void pages_alloc_kernel(
         ok = c >= 0 && m >= 0 && h >= 0 && h <= a.max_pages && pages <= a.max_pages;
         need = ok && pages > h ? static_cast<int>(pages - h) : 0;
       }
-      status[i] = ok ? 1 : 0;
+      status[i] = ok ? 1 + (need > 0) : 0;  // 2: if its pages are found
     }
     int64_t total;
     const int64_t before = block_exclusive(need, sums, &total);
@@ -320,16 +320,20 @@ __global__ __launch_bounds__(kAllocThreads) void pages_alloc_kernel(
   __syncthreads();
   for (int i = tid; i < n; i += kAllocThreads) {
     if (!status[i]) continue;
-    const int need = w.rank[i + 1] - w.rank[i];
+    // (The ranks of entries behind the pool's end are all the same.)
+    const bool needs = status[i] == 2;
     const int s = seq[i];
-    if (need > 0 && w.rank[i + 1] > found) {
+    if (needs && w.rank[i + 1] > found) {
       status[i] = 0;
-    } else if (FORK) {
+      continue;
+    }
+    status[i] = 1;
+    if (FORK) {
       const int c = a.context[src[i]];
-      a.held[s] = (c >> a.page_log) + need;
+      a.held[s] = (c >> a.page_log) + (needs ? 1 : 0);
       a.context[s] = c;
     } else {
-      a.held[s] += need;
+      a.held[s] += w.rank[i + 1] - w.rank[i];
     }
   }
 }

@@ -752,8 +752,8 @@ size_t whiflash_cache_pages_workspace_bytes(const wf_page_cache* cache, int32_t 
  * Forks sequences: dst[i] becomes a copy of src[i], with the full pages of its context
  * shared (refs + 1) and a partly filled last page copied, in every layer, into a free
  * page.  status[i] is 1 if done, 0 if refused (nothing changed then): an index outside
- * [0, seqs); a src whose context is negative or past its held pages, or that is a dst
- * of the same call; a dst that holds pages or appeared before in dst; no free page left.
+ * [0, seqs); a src whose context is negative or past its held pages; a dst that holds
+ * pages, is a src of the same call or appeared before in dst; no free page left.
  * Free pages are handed out lowest first, in the order of the entries; from the first
  * entry on that finds too few, entries that need pages are refused.
  * Workspace: whiflash_cache_pages_workspace_bytes(cache, n) bytes, 256-byte aligned.

@@ -143,6 +143,34 @@ def test_reserve_hands_out_the_lowest_pages_of_a_large_pool():
     same_cache(o, cache)
 
 
+@pytest.mark.parametrize("free", [0, 1, 3])
+@pytest.mark.parametrize("entries", [6, 40, 1100])
+def test_demands_far_past_the_pool(free, entries):
+    # More pages are wanted than the pool has in all: every entry behind its end that needs
+    # one is refused, one that needs none (an empty context) is not.
+    P, S = free + 1, entries + 3
+    o = orc.Cache(np.zeros((1, P, 1, 16, 64), np.float32), np.zeros((1, P, 1, 16, 64), np.float32),
+                  np.full((S, 8), -1, np.int32), np.zeros(S, np.int32), np.zeros(S, np.int32),
+                  np.zeros(P, np.int32))
+    o.table[0, 0], o.held[0], o.context[0], o.refs[P // 2] = P // 2, 1, 5, 1
+    o.k[:] = np.random.default_rng(3).normal(0, 1, o.k.shape)
+    cache = device_cache(o, "f32")
+    src, dst = np.zeros(entries, int), np.arange(2, entries + 2)
+    src[1::2] = 1                                # holds nothing
+    e = orc.cache_fork(o, src, dst)
+    assert e[::2].sum() == min(free, (entries + 1) // 2) and e[1::2].all()
+    assert np.array_equal(host(wf.cache_fork(cache, i32(src), i32(dst))), e)
+    same_cache(o, cache)
+    gone = np.arange(2, entries + 2)
+    orc.cache_free(o, gone)
+    wf.cache_free(cache, i32(gone))
+    count = np.where(np.arange(entries) % 3 == 2, 0, 8 * 16)
+    e = orc.cache_reserve(o, dst, count)
+    assert e.sum() == (count == 0).sum()
+    assert np.array_equal(host(wf.cache_reserve(cache, i32(count), seqs=i32(dst))), e)
+    same_cache(o, cache)
+
+
 def test_random_lives_of_sequences():
     # Forks, rows, acceptances and frees in turn; the pool balances at the end.
     rng = np.random.default_rng(17)
