@@ -42,7 +42,8 @@ __global__ __launch_bounds__(kThreads) void history_prompt_kernel(
   if (s < 0) return;
   uint16_t* row = history + s * stride;
   const int lo = min(max(offsets[b], 0), count), hi = min(max(offsets[b + 1], lo), count);
-  for (int i = lo + blockIdx.y * kThreads + threadIdx.x; i < hi; i += gridDim.y * kThreads) {
+  for (int64_t i = lo + static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < hi;
+       i += gridDim.y * kThreads) {
     const int v = tokens[i];
     if (v >= 0 && v < V) change_word(row, v, [](unsigned h) { return h | 0x8000u; });
   }
