@@ -86,6 +86,8 @@ def _enter(index: int, stream):
         ctx = torch.cuda.device(index)
         ctx.__enter__()
         return torch._C._cuda_getCurrentRawStream(index), ctx
+    if stream.device_index != index:
+        raise ValueError(f"stream is of GPU {stream.device_index}, the call runs on GPU {index}")
     ctx = torch.cuda.stream(stream)
     ctx.__enter__()
     return stream.cuda_stream, ctx

@@ -143,3 +143,9 @@ def test_python_refuses_host_tensors():
                  lambda: wf.PageCache(i, i, i, i, i, i)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    from types import SimpleNamespace
+    with pytest.raises(ValueError, match="GPU 1"):
+        rd._enter(0, SimpleNamespace(device_index=1, cuda_stream=0))
