@@ -5,6 +5,11 @@
 // dependent reads (slot, drafts, word).  A word is half of an aligned 32-bit word,
 // changed by compare-and-swap, so equal tokens, and sequences that share a slot,
 // add up; sums and ORs do not depend on the order.
+//
+// The last token of an odd vocabulary has its 32 bits together with the element past the
+// row, which the last slot's storage need not hold: it is read and written as the 16 bits
+// that it has.  Every workgroup of history_prompt writes the same value there; of
+// history_update one workgroup a slot writes it, for all sequences that share the slot.
 #include "rounds.h"
 
 namespace wf {
@@ -33,6 +38,9 @@ __device__ inline void count_once(uint16_t* row, int v) {
   change_word(row, v, [](unsigned h) { return (h & kCountMask) == kCountMask ? h : h + 1u; });
 }
 
+// Whether token v has no other token of its row in its 32-bit word.
+__device__ inline bool alone(int v, int V) { return v == V - 1 && (V & 1); }
+
 __global__ __launch_bounds__(kThreads) void history_prompt_kernel(
     uint16_t* __restrict__ history, int slots, int V, int64_t stride,
     const int32_t* __restrict__ slot, const int32_t* __restrict__ tokens,
@@ -45,11 +53,31 @@ __global__ __launch_bounds__(kThreads) void history_prompt_kernel(
   for (int64_t i = lo + static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < hi;
        i += gridDim.y * kThreads) {
     const int v = tokens[i];
-    if (v >= 0 && v < V) change_word(row, v, [](unsigned h) { return h | 0x8000u; });
+    if (v < 0 || v >= V) continue;
+    if (alone(v, V)) {
+      row[v] |= 0x8000u;
+    } else {
+      change_word(row, v, [](unsigned h) { return h | 0x8000u; });
+    }
   }
 }
 
-// One wave per sequence.
+// How often a verified sequence enters token v: by one lane, along its path.
+__device__ inline int times_entered(const RowsArgs& rows, int b, int V, int v,
+                                    const int32_t* __restrict__ accept_len,
+                                    const int32_t* __restrict__ best_node,
+                                    const int32_t* __restrict__ bonus) {
+  const SeqRows q = seq_rows(rows, b);
+  int u = q.n == 0 ? -1 : q.tree ? best_node[b] : accept_len[b] - 1;
+  if (u < 0 || u >= q.n) return 0;
+  int times = bonus[b] == v;
+  for (; u > 0; u = node_parent(rows, b, q.tree, u)) times += node_token(rows, b, q.tree, u, V) == v;
+  return u == 0 ? times : 0;
+}
+
+// One wave per sequence.  The last token of an odd vocabulary, where the wave's own sequence
+// enters it, is counted by the first such sequence of its slot: that wave looks through the
+// slots for the others.  Waves that do not come upon that token do nothing of this.
 __global__ __launch_bounds__(64) void history_update_kernel(
     uint16_t* __restrict__ history, int slots, int V, int64_t stride, RowsArgs rows,
     const int32_t* __restrict__ slot, const int32_t* __restrict__ accept_len,
@@ -62,13 +90,19 @@ __global__ __launch_bounds__(64) void history_update_kernel(
   const SeqRows q = seq_rows(rows, b);
   if (s < 0 || q.n == 0) return;
   uint16_t* row = history + s * stride;
+  int last = 0;  // how often this lane came upon the last token of an odd vocabulary
+  auto enter = [&](int v) {
+    if (v < 0 || v >= V) return;
+    if (alone(v, V)) {
+      ++last;
+    } else {
+      count_once(row, v);
+    }
+  };
   if (!q.tree) {
     const int al = accept_len[b];
     if (al < 1 || al > q.n) return;
-    for (int u = 1 + lane; u < al; u += 64) {
-      const int v = node_token(rows, b, false, u, V);
-      if (v >= 0) count_once(row, v);
-    }
+    for (int u = 1 + lane; u < al; u += 64) enter(node_token(rows, b, false, u, V));
   } else {
     const int best = best_node[b];
     if (best < 0 || best >= q.n) return;
@@ -81,14 +115,23 @@ __global__ __launch_bounds__(64) void history_update_kernel(
     }
     __syncthreads();
     if (len_s < 0) return;
-    for (int i = lane; i < len_s; i += 64) {
-      const int v = node_token(rows, b, true, path_s[i], V);
-      if (v >= 0) count_once(row, v);
-    }
+    for (int i = lane; i < len_s; i += 64) enter(node_token(rows, b, true, path_s[i], V));
   }
+  if (lane == 0) enter(bonus[b]);
+  if (!__any(last > 0)) return;
+  bool earlier = false;
+  for (int o = lane; slot && o < rows.B; o += 64) {
+    if (o == b || slot[o] != s) continue;
+    const int times = times_entered(rows, o, V, V - 1, accept_len, best_node, bonus);
+    if (o > b) last += times;
+    earlier = earlier || (o < b && times > 0);
+  }
+  if (__any(earlier)) return;
+  for (int off = 32; off > 0; off >>= 1) last += __shfl_xor(last, off);
   if (lane == 0) {
-    const int v = bonus[b];
-    if (v >= 0 && v < V) count_once(row, v);
+    const unsigned h = row[V - 1], count = h & kCountMask;
+    const unsigned room = kCountMask - count;
+    row[V - 1] = static_cast<uint16_t>(h + min(static_cast<unsigned>(last), room));
   }
 }
 

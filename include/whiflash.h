@@ -565,8 +565,9 @@ typedef struct wf_round_rows {
  *   history [slots, V] uint16, rows history_stride elements apart (base and row
  *     stride multiples of 16 bytes): one word per token, bit 15 set if the token
  *     is in the prompt, the low 15 bits how often it was put out (it stays at
- *     32767).  Sequence b uses row slot[b] (slot NULL: b); a slot outside
- *     [0, slots) means no history.
+ *     32767).  A row is its V words: what lies past them is not accessed, and the
+ *     last row's storage may end there.  Sequence b uses row slot[b] (slot NULL: b);
+ *     a slot outside [0, slots) means no history.
  *   penalties [B, 3] float32: repetition, frequency, presence.
  *   bias_offsets [B + 1], bias_ids, bias_values [bias_count] (float32): sequence b
  *     adds bias_values[i] to token bias_ids[i] for i in [bias_offsets[b],
@@ -639,7 +640,7 @@ int32_t whiflash_verify_constrained(const void* logits, int32_t dtype, int32_t V
  * Marks prompt tokens in the history: for i in [offsets[b], offsets[b+1]), bit 15
  * of history[slot[b]][tokens[i]].  tokens holds `count` int32; offsets [B + 1] are
  * cut to [0, count].  Tokens outside [0, V) and slots outside [0, slots) are
- * skipped.
+ * skipped.  Calls that change one history must not overlap in time.
  */
 int32_t whiflash_history_prompt(uint16_t* history, int32_t slots, int32_t V, int64_t history_stride,
                                 int32_t B, const int32_t* slot, const int32_t* tokens,
@@ -651,7 +652,8 @@ int32_t whiflash_history_prompt(uint16_t* history, int32_t slots, int32_t V, int
  * tree, without the first row) and the bonus token each count once more.  Tokens
  * outside [0, V) are skipped; a malformed sequence, a chain's accept_len outside
  * [1, K + 1] and a tree's best_node outside [0, N) or whose path does not reach the
- * root enter nothing.  best_node may be NULL for rounds of chains.
+ * root enter nothing.  Sequences that share a slot add up.  best_node may be NULL for
+ * rounds of chains.  Calls that change one history must not overlap in time.
  */
 int32_t whiflash_history_update(uint16_t* history, int32_t slots, int32_t V, int64_t history_stride,
                                 const wf_round_rows* rows, const int32_t* slot,
