@@ -116,6 +116,25 @@ __device__ inline unsigned pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(unsigned, r);
 }
 
+// Infinities and NaN among values that not every query sees go apart from the product, where
+// they would meet the weights of zero of those queries too.  What they make of sum p v, in
+// four rounds, each the count of the seen positions whose value is of a kind: infinities
+// of either sign add theirs, NaN make NaN, and so do infinities whose weight is zero itself.
+constexpr int kOddRounds = 4;
+
+// Float32 bits x are of the round's kind if (x & mask) - low <= span.
+struct OddKind {
+  unsigned mask, low, span;
+  float effect;
+};
+
+__device__ inline OddKind odd_kind(int round) {
+  if (round == 0) return OddKind{0xffffffffu, 0x7f800000u, 0u, INFINITY};
+  if (round == 1) return OddKind{0xffffffffu, 0xff800000u, 0u, -INFINITY};
+  if (round == 2) return OddKind{0x7fffffffu, 0x7f800001u, 0x7ffffeu, NAN};
+  return OddKind{0x7fffffffu, 0x7f800000u, 0u, NAN};
+}
+
 // Operand fragment f of group g is the piece of sixteen bytes 4 f + g of a query or key.
 // What differs between the types: operand fragments, the two products and their tiles.
 // Lane l is place n = l % 16 of group g = l / 16.  kSub positions sub-tiles of 16 make
@@ -212,37 +231,61 @@ struct Ops<WF_BF16, D> {
         x = x || (v.w[r][c] & 0x7f80u) == 0x7f80u || (v.w[r][c] & 0x7f800000u) == 0x7f800000u;
     return x;
   }
-  // Outputs that give an infinity or NaN a weight above zero become NaN; then zeros take
-  // its place in v, so that it does not reach the queries that do not see it.
+  // Adds to the outputs what infinities and NaN among the values make of them (odd_kind), and
+  // puts zeros in their place.  see[m]: the positions that the lane's query of tile m sees,
+  // a bit each.
   template <int MT>
-  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4]) {
-#pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      const unsigned half = (j & 1) ? 0xffff0000u : 0xffffu, most = 0x7f807f80u & half;
-      unsigned w[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        unsigned& a = v.w[2 * x][j >> 1];
-        unsigned& b = v.w[2 * x + 1][j >> 1];
-        const bool oa = (a & most) == most, ob = (b & most) == most;
-        w[x] = (oa ? 0x3f80u : 0u) | (ob ? 0x3f800000u : 0u);
-        a = oa ? a & ~half : a;
-        b = ob ? b & ~half : b;
-      }
-      const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4],
+                                       const unsigned* see) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll 1
+    for (int round = 0; round < kOddRounds; ++round) {
+      const OddKind kind = odd_kind(round);
+      bf16x8 pb[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        unsigned w[4] = {0u, 0u, 0u, 0u}, bits = see[m] >> (4 * g);
+        asm volatile("" : "+v"(bits));  // (worked out in each round: it would take registers)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          w[x] = (p[m][x >> 1][2 * x & 3] > 0.f ? 0x3f80u : 0u) |
-                 (p[m][x >> 1][(2 * x & 3) + 1] > 0.f ? 0x3f800000u : 0u);
-        const bf16x8 pb = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
-        f32x4 t = {0.f, 0.f, 0.f, 0.f};
-        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb, t, 0, 0, 0);
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[m][j][i] = t[i] > 0.f ? NAN : o[m][j][i];
+          for (int i = 0; i < 4; ++i) {
+            const bool seen = bits >> (16 * t + i) & 1u;
+            const bool on = seen && (round < kOddRounds - 1 || !(p[m][t][i] > 0.f));
+            w[2 * t + i / 2] |= on ? 0x3f80u << (i % 2 * 16) : 0u;
+          }
+        pb[m] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+      }
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        unsigned w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          // (A half is compared where it lies: in the lower one everything is shifted.)
+          const int down = (j & 1) ? 0 : 16;
+          const unsigned mask = (kind.mask & 0xffff0000u) >> down;
+          const unsigned low = ((kind.low + 0xffffu) & 0xffff0000u) >> down, span = kind.span >> down;
+          w[x] = (v.w[2 * x][j >> 1] & mask) - low <= span ? 0x3f80u : 0u;
+          w[x] |= (v.w[2 * x + 1][j >> 1] & mask) - low <= span ? 0x3f800000u : 0u;
+        }
+        const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x4 n = {0.f, 0.f, 0.f, 0.f};
+          n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[m], n, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[m][j][i] += n[i] > 0.f ? kind.effect : 0.f;
+        }
       }
     }
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < kVecV * 2; ++c) {
+        const unsigned x = v.w[r][c];
+        v.w[r][c] = ((x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu) |
+                    ((x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u);
+      }
   }
 };
 
@@ -312,28 +355,42 @@ struct Ops<WF_F32, D> {
     return x;
   }
   template <int MT>
-  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4]) {
+  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4],
+                                       const unsigned* see) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll 1
+    for (int round = 0; round < kOddRounds; ++round) {
+      const OddKind kind = odd_kind(round);
+      unsigned bits[MT];
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f32x4 t[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) t[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool x = is_odd(v.w[i][h][e]);
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            t[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(x ? 1.f : 0.f, p[m][0][i] > 0.f ? 1.f : 0.f,
-                                                        t[m], 0, 0, 0);
-          v.w[i][h][e] = x ? 0.f : v.w[i][h][e];
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[m][4 * h + e][i] = t[m][i] > 0.f ? NAN : o[m][4 * h + e][i];
+      for (int m = 0; m < MT; ++m) {
+        bits[m] = see[m] >> (4 * g);
+        asm volatile("" : "+v"(bits[m]));
       }
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            f32x4 n = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool seen = bits[m] >> i & 1u;
+              const bool on = seen && (round < kOddRounds - 1 || !(p[m][0][i] > 0.f));
+              const bool is = (__float_as_uint(v.w[i][h][e]) & kind.mask) - kind.low <= kind.span;
+              n = __builtin_amdgcn_mfma_f32_16x16x4f32(is ? 1.f : 0.f, on ? 1.f : 0.f, n, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[m][4 * h + e][i] += n[i] > 0.f ? kind.effect : 0.f;
+          }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v.w[i][h][e] = is_odd(v.w[i][h][e]) ? 0.f : v.w[i][h][e];
   }
 };
 
@@ -464,30 +521,31 @@ struct Queries {
   }
 
   // Takes out of a tile's scores what its query does not see: positions outside `any`,
-  // and of the round's own positions those of rows that are not on its path.
-  __device__ inline void mask(Weights& p, int j0, unsigned any, const AttendArgs& a,
+  // and of the round's own positions those of rows that are not on its path.  see[m] gets the
+  // positions that the lane's query of tile m sees.
+  __device__ inline void mask(Weights& p, unsigned* see, int j0, unsigned any, const AttendArgs& a,
                               const SeqCall& call, const int16_t* par) const {
     const int g = (threadIdx.x & 63) >> 4;
     const int old = min(max(call.c - j0, 0), 32);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      unsigned see = old >= 32 ? ~0u : (1u << old) - 1u;
+      see[m] = old >= 32 ? ~0u : (1u << old) - 1u;
       const int x0 = query(a, call, m);
       const int own = x0 < 0 ? -1 : x0 / a.group, last = call.c + own - j0;
       if (!call.q.tree) {
-        if (own >= 0 && last >= 0) see = last >= 31 ? ~0u : (2u << last) - 1u;
+        if (own >= 0 && last >= 0) see[m] = last >= 31 ? ~0u : (2u << last) - 1u;
       } else {
         for (int u = own; u >= 0 && call.c + u >= j0; u = u == 0 ? -1 : par[u]) {
           const int x = call.c + u - j0;
-          if (x < 32) see |= 1u << x;
+          if (x < 32) see[m] |= 1u << x;
         }
       }
-      see &= any;
+      see[m] &= any;
 #pragma unroll
       for (int t = 0; t < X::kSub; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!(see >> (16 * t + 4 * g + i) & 1u)) p[m][t][i] = -INFINITY;
+          if (!(see[m] >> (16 * t + 4 * g + i) & 1u)) p[m][t][i] = -INFINITY;
     }
   }
 
@@ -741,10 +799,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     scores(p);
     const unsigned any = Q.visible(j0, sight.end, pages);
     Q.hide(p, v, any);
-    Q.mask(p, j0, any, a, call, par_s);
+    unsigned see[MT];
+    Q.mask(p, see, j0, any, a, call, par_s);
     Q.soften(p, a.scale_log2);
-    // The round's own values do not meet every query.
-    if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p);
+    if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p, see);
     X::template outputs<MT>(Q.o, Q.sum, v, p);
     if (j0 + kTile < w1) {
       pages = place(j0 + kTile);
@@ -913,10 +971,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendArgs a) 
       take(p, v, h);
       const unsigned any = Q.visible(j, sight.end, static_cast<unsigned>(pages >> (h * kStep)));
       Q.hide(p, v, any);
-      Q.mask(p, j, any, a, call, par_s);
+      unsigned see[MT];
+      Q.mask(p, see, j, any, a, call, par_s);
       Q.soften(p, a.scale_log2);
-      // The round's own values do not meet every query.
-      if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p);
+      if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, p, see);
       X::template outputs<MT>(Q.o, Q.sum, v, p);
     }
     if (j0 + kTile < k1) {

@@ -717,6 +717,10 @@ size_t whiflash_attend_workspace_bytes(const wf_page_cache* cache, const wf_roun
  *   Scores, maxima and sums are float32; for bfloat16 the weights p (relative to the
  * largest) are rounded to bfloat16 before they multiply v and are summed, as the matrix
  * units take them.  The order of all sums is fixed: results are reproducible bit by bit.
+ *   What a row does not see does not reach it, whatever it holds.  An infinity among the
+ * values of a seen position stays one in its dimension of out where all float32 weights on
+ * infinities are above zero and their signs agree; else that dimension is NaN, as it is with
+ * a NaN among the values.
  *   Positions without a page (a table entry outside [0, pages)) are not seen.  A row
  * that sees nothing gets zeros, and so do the rows of a sequence outside [0, seqs), or
  * whose context is negative, above max_context or leaves its rows no room in max_pages

@@ -188,3 +188,49 @@ def test_append_then_attend_past_32_bits():
     ref = torch.matmul(torch.softmax(w.masked_fill(~see, -np.inf), -1), v).transpose(0, 1)
     # normal data: scores of a few units; two bfloat16 roundings of values of order one
     assert float((out.float() - ref).abs().max()) < 2 * 2.0 ** -8 * float(v.abs().max())
+
+
+@pytest.mark.parametrize("dtype,dim", [("f32", 64), ("bf16", 128), ("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("kind,K,N,group", [("chain", 0, 0, 4), ("chain", 4, 0, 5), ("chain", 11, 0, 4),
+                                            ("chain", 16, 0, 8), ("tree", 0, 13, 3), ("tree", 0, 40, 4)])
+def test_infinite_values_do_as_the_sum_has_it(dtype, dim, kind, K, N, group):
+    # One rule wherever a seen position lies, among tiles that all rows see or those that some do:
+    # an infinity with a weight stays one, NaN, two signs and infinities whose weight is 0 give NaN.
+    for context in (6, 40, 64, 2500):
+        r = Round(kind, 1, K, N, 50, seed=2)
+        o, cache = make_cache(1, 1, 16, dim, [context], max(K + 1, N), 7, dtype=dtype)
+        q, _ = _queries(r.total, group, dim, dtype, 8)
+        q[:, :, 0] = 4.0
+        cache.k[..., 0] = 0.0
+        for first, last in ((1, context - 1), (context - 1, 1), (1, 2), (context - 2, context - 1)):
+            if first == last:
+                continue
+            clean = host(wf.attend(q, r.rows, cache).float())
+            (p0, o0), (p1, o1) = o.where(0, first), o.where(0, last)
+            kept = cache.k.clone(), cache.v.clone()
+            at, to = cache.v[0, p0, 0, o0], cache.v[0, p1, 0, o1]
+            at[3], at[8], at[9] = float("inf"), float("-inf"), float("nan")
+            at[11], to[11] = float("inf"), float("-inf")      # two signs
+            at[12], to[12] = float("inf"), float("inf")
+            # a score some thousands below the others: its weight is 0
+            cache.k[0, p1, 0, o1, 0] = -8192.0
+            to[dim - 1] = float("inf")
+            got = host(wf.attend(q, r.rows, cache).float())
+            want = {3: np.inf, 8: -np.inf, 9: np.nan, 11: np.nan, 12: np.nan, dim - 1: np.nan}
+            for d in range(dim):
+                if d in want:
+                    assert np.array_equal(got[..., d], np.full(got.shape[:2], want[d]), equal_nan=True), \
+                        (context, first, last, d, got[..., d])
+                else:
+                    assert np.all(np.isfinite(got[..., d])), (context, first, last, d)
+            cache.k.copy_(kept[0])
+            cache.k[0, p1, 0, o1, 0] = 0.0
+            got = host(wf.attend(q, r.rows, cache).float())
+            want[12], want[dim - 1] = np.inf, np.inf
+            for d in range(dim):
+                if d in want:
+                    assert np.array_equal(got[..., d], np.full(got.shape[:2], want[d]), equal_nan=True), \
+                        (context, first, last, d, got[..., d])
+                else:
+                    assert np.array_equal(got[..., d], clean[..., d]), (context, first, last, d)
+            cache.v.copy_(kept[1])
