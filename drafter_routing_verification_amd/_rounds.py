@@ -98,6 +98,13 @@ def _leave(ctx) -> None:
         ctx.__exit__(None, None, None)
 
 
+def _word(x: int, name: str) -> int:
+    """x, which the C interface takes as an int32 (ctypes would drop the bits past it)."""
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 def _ints(t, name: str, n: int, index: int) -> int:
     """The address of a contiguous int32 tensor of n elements on GPU `index`."""
     if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.numel() == n
@@ -173,7 +180,7 @@ def routed_rows(row_offsets, total_rows: int, choice, chain_draft, parent, draft
     _, N = _tree_tensors(parent, draft_ids, d2t)
     if chain_draft.dim() != 2 or chain_draft.shape[0] != B or parent.shape[0] != B:
         raise ValueError("chain_draft must be [B, K] and parent [B, N] with the batch of choice")
-    return RoundRows(ROWS_ROUTED, B, chain_draft.shape[1], N, total_rows, choice.device,
+    return RoundRows(ROWS_ROUTED, B, chain_draft.shape[1], N, _word(total_rows, "total_rows"), choice.device,
                      draft_ids is not None, chain_draft=chain_draft, parent=parent,
                      draft_ids=draft_ids, d2t=d2t, row_offsets=row_offsets, choice=choice)
 
@@ -359,7 +366,7 @@ def process_logits(logits, rows: RoundRows, rules: LogitRules, *, out=None, dtyp
 
 
 def verify_constrained_workspace_bytes(rows: RoundRows, V: int) -> int:
-    return functions().verify_constrained_workspace_bytes(rows.ref, V)
+    return functions().verify_constrained_workspace_bytes(rows.ref, _word(V, "V"))
 
 
 def verify_constrained(logits, rows: RoundRows, rules: LogitRules, *, row_argmax=True,
@@ -475,14 +482,15 @@ def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: in
     vs = _vectors(v_rows, "v_rows", rows.total, cache.heads, cache)
     raw, ctx = _enter(cache.index, stream)
     try:
-        _check(functions().cache_append(cache.ref, layer, rows.ref, seq, k_rows.data_ptr(), ks,
+        _check(functions().cache_append(cache.ref, _word(layer, "layer"), rows.ref, seq, k_rows.data_ptr(), ks,
                                         v_rows.data_ptr(), vs, raw))
     finally:
         _leave(ctx)
 
 
 def attend_workspace_bytes(cache: PageCache, rows: RoundRows, q_heads: int, max_context: int) -> int:
-    return functions().attend_workspace_bytes(cache.ref, rows.ref, q_heads, max_context)
+    return functions().attend_workspace_bytes(cache.ref, rows.ref, _word(q_heads, "q_heads"),
+                                              _word(max_context, "max_context"))
 
 
 def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, scale=None,
@@ -505,8 +513,8 @@ def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, s
             _out(out, cache.dtype, rows.total * heads * cache.head_dim, cache.device, "out")
         ws, at, size = _scratch(workspace, attend_workspace_bytes(cache, rows, heads, max_context),
                                 cache.device)
-        _check(functions().attend(q.data_ptr(), qs, heads, cache.ref, layer, rows.ref, seq, max_context,
-                                  scale, out.data_ptr(), at, size, raw))
+        _check(functions().attend(q.data_ptr(), qs, heads, cache.ref, _word(layer, "layer"), rows.ref, seq,
+                                  max_context, scale, out.data_ptr(), at, size, raw))
     finally:
         _leave(ctx)
     return out

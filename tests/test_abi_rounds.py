@@ -149,3 +149,14 @@ def test_a_stream_of_another_gpu_is_refused():
     from types import SimpleNamespace
     with pytest.raises(ValueError, match="GPU 1"):
         rd._enter(0, SimpleNamespace(device_index=1, cuda_stream=0))
+
+
+def test_sizes_past_32_bits_are_refused_by_the_binding():
+    handle = lambda ref: type("Handle", (), {"ref": ref})()  # noqa: E731
+    cache, rows = handle(_cache()), handle(_rows())
+    assert rd.attend_workspace_bytes(cache, rows, 32, 131000) > 0
+    for heads, context in ((32, 1 << 32), ((1 << 32) + 32, 131000), (32, -1 - (1 << 31))):
+        with pytest.raises(ValueError, match="32 bits"):
+            rd.attend_workspace_bytes(cache, rows, heads, context)
+    with pytest.raises(ValueError, match="32 bits"):
+        rd.verify_constrained_workspace_bytes(rows, (1 << 32) + V)

@@ -244,3 +244,20 @@ def test_refusals_of_gpu_tensors():
             call()
             pytest.fail(f"call {n} was taken")
     torch.cuda.synchronize()
+
+
+def test_numbers_past_32_bits_are_refused():
+    # 2^40 positions, layer 2^32: cut to 32 bits they would be 0, and be taken.
+    r = Round("chain", 3, 2, 0, 100, seed=1)
+    _, cache = make_cache(1, 2, 16, 64, [3, 4, 5], 8, 1, dtype="f32")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    q, k = (torch.zeros(9, h, 64, device=DEV) for h in (4, 2))
+    for call in (lambda: wf.attend(q, r.rows, cache, max_context=1 << 40),
+                 lambda: wf.attend(q, r.rows, cache, layer=1 << 32),
+                 lambda: wf.attend_workspace_bytes(cache, r.rows, 4, 1 << 32),
+                 lambda: wf.cache_append(cache, r.rows, k, k, layer=-1 << 32),
+                 lambda: wf.verify_constrained_workspace_bytes(r.rows, (1 << 32) + 8),
+                 lambda: wf.routed_rows(i(3), 1 << 32, i(2), i(2, 3), i(2, 3))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    torch.cuda.synchronize()
