@@ -16,16 +16,24 @@
 // up to two (one in float32), every wave has positions of its own and all queries; with
 // more, every wave has queries of its own and the four share the positions.
 //
-// Measured (MI355X, bf16, 32 query heads on 8, head_dim 128, pages of 16):
-//   64 sequences of 4,096-8,192 positions, one row each: 250 us, 6.5 TB/s of keys and values
-//     (a pure streaming read of the same memory: 7.3); bound by HBM and, for a quarter of
-//     it, by sequences of unequal length.
-//   2 chains of 17 rows over 131,000 positions: 170 us, 5.5 TB/s and 375 TFLOP/s (of 1,205
-//     that a large product reaches); 8 trees of 61 rows over 2,048-4,096: 60 us, 430 TFLOP/s.
-//     Neither the vector units (35%) nor the matrix units (25%) are full: two waves a SIMD
-//     do not cover the chain from scores through maxima and exponentials to the second
-//     product.  Three waves spill; 3 to 5 query tiles a wave, with its own positions, spill
-//     too (1,047 us for the long chains).
+// Measured (MI355X, 32 query heads on 8, head_dim 128, pages of 16; whole passes with their
+// append and join, inputs changing from pass to pass, and in brackets the kernel alone under
+// the profiler):
+//   64 sequences of 4,096-8,192 positions, one row each: 256 us [247-252], 6.3 TB/s of keys and
+//     values (a pure streaming read of the same memory: 7.3); bound by HBM and, for a quarter of
+//     it, by sequences of unequal length.  float32 542 us, 6.0 TB/s; head_dim 64 140 us, 5.8.
+//   2 chains of 17 rows over 131,000 positions: 188 us [189-212], 5.0 TB/s and 341 TFLOP/s (of
+//     1,205 that a large product reaches); 8 trees of 61 rows over 2,048-4,096: 77 us [69], 335
+//     TFLOP/s.  Neither the vector units (35%) nor the matrix units (25%) are full: two waves a
+//     SIMD do not cover the chain from scores through maxima and exponentials to the second
+//     product.  A third is kept out by the registers of two query tiles (spilled: slower) and by
+//     67,584 bytes of LDS, of which a CU holds two workgroups' worth.  3 to 5 query tiles a wave,
+//     with its own positions, spill too (1,047 us for the long chains).
+//   float32 there: 1,200 us (floor 415: its matrix rate) and 336 us (168).
+//   Far from their floors: fewer than eight pieces leave XCDs idle (unit_of): 2 chains of 1,001
+//     rows over 4,000 positions 763 us, 172 TFLOP/s, where 8 of 1,024 rows reach 532; and the plan
+//     knows the bound alone: one sequence of 131,000 positions among 63 of up to 1,000 1,142 us
+//     for 92 us of bytes.
 #include <math.h>
 
 #include "elem.h"
@@ -43,8 +51,9 @@ constexpr float kLowest = -3.0e38f;  // a maximum of nothing: finite, so that no
 // stay below 2^8, and most tiles need no rescaling.
 constexpr float kSlack = 8.f;
 constexpr int kMinSpan = 128;
-// The plan of pieces: workgroups that run at a time (two a CU), and the time of a
-// workgroup's start and end, in positions.  64 sequences of up to 8,192 positions: one piece
+// The plan of pieces: workgroups that run at a time (two a CU; with head_dim 64 three or four
+// would fit, which the plan does not use), and the time of a workgroup's start and end, in
+// positions.  64 sequences of up to 8,192 positions: one piece
 // 256 us, two rounds 270, four 269, sixteen 272.
 constexpr int kSlots = 512;
 constexpr int kStart = 256;
@@ -187,7 +196,13 @@ struct Ops<WF_BF16, D> {
 #pragma unroll
     for (int x = 0; x < kVecV * 2; ++x) v.w[4 * t + i][x] = 0;
   }
-  // o += V^T P^T for MT query tiles; p[m][t][i] the weights.
+  // o += V^T P^T for MT query tiles; p[m][t][i] the weights, rounded to bfloat16 as the matrix
+  // units take them (a part in 2^8 each), and summed as rounded, so that equal values come out
+  // as they are.  Against 64 bits the outputs are then off by 0.0022-0.0024 (root mean square,
+  // relative) where their own rounding alone gives 0.0017.  Weights as two bfloat16 halves give
+  // 0.0017, in the same time for one row a sequence (256 us), but 88 us against 77 for the trees
+  // and 223 against 188 for the long chains, and an infinity among the values would meet lower
+  // halves of zero: not taken.
   template <int MT>
   __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4* sum, const V& v,
                                         const float (*p)[kSub][4]) {
@@ -641,7 +656,8 @@ struct Unit {
 };
 
 // Workgroup -> (sequence, piece, key-value head, query group), such that all heads and
-// query groups of a piece go to the same XCD (every eighth workgroup does).
+// query groups of a piece go to the same XCD (every eighth workgroup does).  Eight pieces at
+// least give every XCD work.
 __device__ inline Unit unit_of(const AttendArgs& a) {
   Unit x;
   int64_t y = blockIdx.x / 8;
@@ -670,8 +686,8 @@ __device__ inline Sight sight_of(const AttendArgs& a, const SeqCall& call, int f
 
 // Up to 16 MT queries: one workgroup per (sequence, key-value head, piece, query group),
 // whose four waves share the piece's positions and join their m, l and O in LDS.  Every
-// byte is read once, by loads that take whole lines and do not stay in the caches; the
-// next tile's keys are fetched as soon as this one's are in LDS, its values after the
+// byte is read once, by loads that take whole lines and do not stay in the caches (the
+// values of bfloat16 with head_dim 64 by plain loads of 8 bytes a lane); the next tile's keys are fetched as soon as this one's are in LDS, its values after the
 // second product.
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {

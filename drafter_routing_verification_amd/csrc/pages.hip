@@ -225,9 +225,9 @@ PagesWs pages_ws(const wf_page_cache& c, int32_t n, int32_t* ws) {
 // needs a page if the context ends inside one; else entry i gives seq[i] room for
 // context + count[i] positions.  Ranks are prefix sums of the needs; the free page of
 // rank g (lowest first) goes to the entry whose range holds g, if all of that entry's
-// range was found.  One workgroup, so that ranks need no second launch: 7 to 9 us, its
-// barriers and dependent reads, for pools of some thousand pages (20,000 taken pages to look past cost
-// 5 us more, 200,000 92).
+// range was found.  One workgroup, so that ranks need no second launch: 7 to 10 us, its
+// barriers and dependent reads, for pools of some thousand pages; 16 past 20,000 taken pages and
+// 101 past 200,000, which it looks through one pass after the other.
 template <bool FORK>
 __global__ __launch_bounds__(kAllocThreads) void pages_alloc_kernel(
     CacheArgs a, int n, const int32_t* __restrict__ src, const int32_t* __restrict__ seq,

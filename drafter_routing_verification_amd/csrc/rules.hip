@@ -19,8 +19,9 @@ constexpr int kListMax = 256;                     // special elements of a wave 
 constexpr int kArgmax = -1;
 // Workgroups of a large launch.  More make shorter groups (every group reads its history
 // words and works out its special elements anew), fewer leave an uneven end.  128 sequences
-// (half chains of 17 rows, half trees of 61) x 151,936 bf16, and 64 chains x 17 written out:
-// 4,096 397 / 158 us, 8,192 343 / 147, 12,288 328 / 149, 16,384 334 / 149, 24,576 377 / 174.
+// (half chains of 17 rows, half trees of 61) x 151,936 bf16, and 64 chains x 17 written out, three
+// passes of each in turn: 8,192 369-383 / 146 us, 12,288 343-355 / 148, 16,384 343-358 / 148;
+// 4,096 and 24,576, in another session, 397 / 158 and 377 / 174.
 constexpr int64_t kRulesBlocks = 12288;
 
 struct RulesArgs {
@@ -150,13 +151,14 @@ __device__ inline void store_vec(unsigned char* row, int v, const float* x, int 
 // The next row's mask and vectors are fetched before this row is worked on, the mask first:
 // loads return in order, and the mask is needed first.
 //
-// Measured (MI355X, 151,936 bf16 entries): 64 chains x 17 rows written out 147 us, 4.8 TB/s
-// read and written together, the rate of a large copy.  The argmax of 128 sequences (4,992
-// rows, 1.65 GB) 318 us, 5.2 TB/s: bound by its instructions, some 310 vector and 220 scalar
-// ones a wave and row, and by having only 4 waves a SIMD to cover their latencies; without
-// any rule it takes 241 us, against 205 us of the plain sweep.  Fewer registers (5 waves,
-// spilling) 430 us; bit masks that keep the special elements out of an unmasked maximum
-// (137 registers, 3 waves) 416 us.
+// Measured (MI355X, 151,936 entries): 64 chains x 17 rows written out in bf16 148 us, 4.7 TB/s
+// read and written together, the rate of a large copy; in float32 269 us.  The whole
+// verification of 128 sequences (4,992 rows, 1.65 GB of bf16) 324-344 us, 5 TB/s: bound by its
+// instructions, some 310 vector and 220 scalar ones a wave and row, and by having only 4 waves
+// a SIMD to cover their latencies (105 registers, and 35,344 bytes of LDS a workgroup, of which
+// a CU holds four); without any rule it takes 243 us, against 209 us of the plain call.
+// Registers cut for five waves, which spills (and LDS still holds four): 430 us; bit masks
+// that keep the special elements out of an unmasked maximum (137 registers, 3 waves) 416 us.
 template <int DT, int OUT>
 __global__ __launch_bounds__(kThreads) void rules_kernel(RulesArgs a) {
   using E = Elem<DT>;

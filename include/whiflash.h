@@ -608,7 +608,7 @@ typedef struct wf_logit_rules {
  *   overlap.  Rows of malformed sequences, rows that no sequence owns and the
  *   entries past V are left as they were.  bfloat16 output is rounded to nearest
  *   even.  Rows that two sequences own hold either one's values (in place: unspecified
- * ones).  V is at most 2^30.  B == 0 is a no-op.  No workspace.
+ *   ones).  V is at most 2^30.  B == 0 is a no-op.  No workspace.
  */
 int32_t whiflash_process_logits(const void* logits, int32_t dtype, int32_t V, int64_t row_stride,
                                 const wf_round_rows* rows, const wf_logit_rules* rules, void* out,
@@ -716,7 +716,10 @@ size_t whiflash_attend_workspace_bytes(const wf_page_cache* cache, const wf_roun
  * heads, scale is finite.  max_context: no context is larger (it sizes the launch).
  *   Scores, maxima and sums are float32; for bfloat16 the weights p (relative to the
  * largest) are rounded to bfloat16 before they multiply v and are summed, as the matrix
- * units take them.  The order of all sums is fixed: results are reproducible bit by bit.
+ * units take them.  The order of all sums follows from the sizes of the round, the cache's
+ * geometry, q_heads and max_context: with these the same, a sequence's results are
+ * reproducible bit by bit, whatever its batch holds beside it.  Another batch size or bound
+ * may cut the positions elsewhere and change last bits.
  *   What a row does not see does not reach it, whatever it holds.  An infinity among the
  * values of a seen position stays one in its dimension of out where all float32 weights on
  * infinities are above zero and their signs agree; else that dimension is NaN, as it is with
@@ -725,7 +728,7 @@ size_t whiflash_attend_workspace_bytes(const wf_page_cache* cache, const wf_roun
  * that sees nothing gets zeros, and so do the rows of a sequence outside [0, seqs), or
  * whose context is negative, above max_context or leaves its rows no room in max_pages
  * pages.  Rows of malformed sequences and rows that no sequence owns are left as they
- * were.
+ * were; rows that two sequences own hold unspecified values.
  * Workspace: whiflash_attend_workspace_bytes(cache, rows, q_heads, max_context) bytes,
  * 256-byte aligned, contents ignored on entry; calls sharing one must not overlap.
  */
@@ -741,9 +744,10 @@ int32_t whiflash_attend(const void* q, int64_t q_row_stride, int32_t q_heads,
  * in place already.  next_context [seqs] may be the cache's context itself (NULL
  * means that).  Nothing moves and next_context[s] = context[s] for a malformed
  * sequence, a chain whose accept_len is outside [0, K + 1], and a tree whose best_node
- * is outside [0, N) or has no path of accept_len rows to the root.  Positions without
- * a page are skipped.  best_node may be NULL for rounds of chains.  A cache sequence
- * may occur once in seq.
+ * is outside [0, N) or has no path of accept_len rows to the root.  Entries of
+ * next_context for sequences that the call does not name are left as they were.
+ * Positions without a page are skipped.  best_node may be NULL for rounds of chains.
+ * A cache sequence may occur once in seq.
  */
 int32_t whiflash_cache_compact(const wf_page_cache* cache, const wf_round_rows* rows,
                                const int32_t* seq, const int32_t* accept_len,
