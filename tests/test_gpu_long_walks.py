@@ -1,6 +1,6 @@
 """Rounds whose workgroups walk far: many rows of a sequence one after the other in the rules' kernel,
 and positions past the first 1,024 of a wave, unsplit pieces and joins of more than 64 pieces in the
-attention.  The plans are worked out here from their definition, so that each case says which walk it
+attention, pools that the page bookkeeping looks through in several passes.  The plans are worked out here from their definition, so that each case says which walk it
 takes."""
 
 import numpy as np
@@ -10,7 +10,7 @@ import torch
 import drafter_routing_verification_amd as wf
 from gpu_helpers import DEV, dev, host
 from oracle import rounds as orc
-from round_helpers import Round, bits, i32, make_cache, make_logits, make_rules, to_bf16
+from round_helpers import Round, bits, device_cache, i32, make_cache, make_logits, make_rules, same_cache, to_bf16
 from test_gpu_rules import _check as check_rules
 
 pytestmark = pytest.mark.gpu
@@ -116,8 +116,7 @@ def _long_cache(context, most, dim, dtype, page):
     holes = np.arange(1100 // page, context[2] // page, 7)
     o.table[2, holes] = -1
     o.table[2, holes[1::2]] = o.k.shape[1] + 1
-    put = (lambda x: dev(to_bf16(x))) if dtype == "bf16" else dev
-    return o, wf.PageCache(put(o.k), put(o.v), i32(o.table), i32(o.held), i32(o.context), i32(o.refs))
+    return o, device_cache(o, dtype)
 
 
 # Queries of a key-value head up to 16, 32, 64 and more: every form of the kernel, in one piece whose
@@ -185,3 +184,32 @@ def test_a_sequence_does_not_see_the_rest_of_its_batch(dtype, kind, K, N):
         cache.table[b, 0] = -1
     got = wf.attend(q, r.rows, cache, max_context=3000)
     assert torch.equal(got[dev(mine)], first[dev(mine)])
+
+
+# ----------------------------------------------------------------------------- pages
+
+
+@pytest.mark.parametrize("taken", [0.0, 0.98, 0.9995])
+def test_pages_of_a_pool_of_several_passes(taken):
+    # A pass looks at 16,384 pages: the first suffices where all are free, the demands reach into the
+    # second, or through all three, where some twenty are free and the last demands find too few.
+    P, S = 40000, 700
+    rng = np.random.default_rng(int(taken * 1e4))
+    refs = (rng.random(P) < taken).astype(np.int32)
+    kv = np.zeros((1, P, 1, 16, 64), np.float32)
+    o = orc.Cache(kv, kv.copy(), np.full((S, 12), -1, np.int32), np.zeros(S, np.int32),
+                  np.zeros(S, np.int32), refs)
+    cache = device_cache(o, "f32")
+    seq = rng.permutation(S)[:300]
+    count = rng.integers(0, 40, 300)
+    e = orc.cache_reserve(o, seq, count)
+    assert o.table.max() // 16384 == {0.0: 0, 0.98: 1, 0.9995: 2}[taken]
+    assert np.array_equal(host(wf.cache_reserve(cache, i32(count), seqs=i32(seq))), e)
+    same_cache(o, cache)
+    o.context[:] = np.minimum(5, 16 * o.held)
+    cache.context.copy_(i32(o.context))
+    src = np.flatnonzero(o.held > 0)[:150]
+    dst = np.flatnonzero(o.held == 0)[:len(src)]
+    e = orc.cache_fork(o, src, dst)
+    assert np.array_equal(host(wf.cache_fork(cache, i32(src), i32(dst))), e)
+    same_cache(o, cache)
