@@ -172,7 +172,7 @@ def _cache(case, g, s, room):
     refs[order_host[:at].long()] = 1
     for name in ("k", "v"):
         x = _vectors(g, P * page, heads, dim, torch.bfloat16).float().view(P, page, heads, dim).transpose(1, 2)
-        x = x.reshape(P, heads, page // block, block, dim)
+        x = x.contiguous().view(P, heads, page // block, block, dim)
         e = _exponent(x.abs().amax((-1, -2)))
         s[name] = (x * _power(-e)[..., None, None]).to(torch.float8_e4m3fn).view(P, heads, page, dim)
         s[name + "_scale"] = (e + 127).to(torch.uint8)
