@@ -46,6 +46,16 @@ routed_rows(row_offsets, total_rows, choice, chain_draft, parent, draft_ids, d2t
     cache_compact(cache, rows, accept_len, best_node)   keeps the accepted path's rows
     cache_fork(cache, src, dst), cache_reserve(cache, count, seqs=)  -> status
     cache_free(cache, seqs)
+
+A decoding step around the round:
+    Rotary(frequency, layout=, magnitude=), Rotary.of(pairs, base, scaling=)   rotary positions
+    rotate(q, k, rows, rotary, context)   the rows' queries and keys turned by their positions -> (q, k)
+    PageCache8(k, v, k_scale, v_scale, table, held, context, refs), PageCache8.empty(..., block=)
+                 a paged cache of 8 bits, taken by cache_append, attend, cache_compact, cache_fork,
+                 cache_reserve and cache_free in the place of a PageCache
+    cache_read(cache, count, first=, pending=)   what such a cache stands for -> (k, v)
+    token_logprobs(logits, tokens, rows=, top=)   log probabilities of tokens, entropies and the most
+                 likely tokens -> (logprob, entropy, top_tokens, top_logprobs)
 """
 
 from ._binding import (  # noqa: F401
@@ -126,4 +136,14 @@ from ._rounds import (  # noqa: F401
     tree_rows,
     verify_constrained,
     verify_constrained_workspace_bytes,
+)
+
+from ._decode import (  # noqa: F401
+    PageCache8,
+    Rotary,
+    cache_read,
+    rotary_frequencies,
+    rotate,
+    token_logprobs,
+    token_logprobs_workspace_bytes,
 )

@@ -1,0 +1,412 @@
+"""ctypes binding of a decoding step's calls: rotary positions, the paged cache of 8 bits and the
+attention over it, log probabilities (argument marshalling only).
+
+Two handles: Rotary (the pairs' frequencies) and PageCache8, which cache_append, attend,
+cache_compact, cache_fork, cache_reserve and cache_free take in the place of a PageCache.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _rounds
+from ._binding import (_check, _device_tensor, _dtype_code, _i32, _out, _rows_view, lib)
+from ._rounds import (_CacheStruct, _I32, _R, _enter, _f, _i, _ints, _l, _leave, _p, _pages_call, _scratch,
+                      _sz, _verified, _word, RoundRows)
+
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+WF_E4M3 = 2
+
+
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [("frequency", _p), ("pairs", _i), ("layout", _i), ("magnitude", _f)]
+
+
+class _RotaryRowsStruct(ctypes.Structure):
+    _fields_ = [("x", _p), ("out", _p), ("stride", _l), ("out_stride", _l), ("heads", _i)]
+
+
+class _Cache8Struct(ctypes.Structure):
+    _fields_ = [("pages", _CacheStruct), ("k_scale", _p), ("v_scale", _p), ("scale_layer_stride", _l),
+                ("scale_page_stride", _l), ("block", _i)]
+
+
+_T, _V, _C8 = (ctypes.POINTER(s) for s in (_RotaryStruct, _RotaryRowsStruct, _Cache8Struct))
+
+_SIGNATURES = {
+    "whiflash_rotate": (_i, [_T, _i, _i, _R, _p, _p, _i, _V, _V, _p]),
+    "whiflash_cache8_append": (_i, [_C8, _i, _R, _p, _i, _p, _l, _p, _l, _p]),
+    "whiflash_cache8_read": (_i, [_C8, _i, _i, _p, _p, _i, _i, _i, _p, _p, _p]),
+    "whiflash_cache8_compact": (_i, [_C8, _R, _p, _p, _p, _p, _p]),
+    "whiflash_cache8_fork": (_i, [_C8, _i, _p, _p, _p, _p, _sz, _p]),
+    "whiflash_attend8_workspace_bytes": (_sz, [_C8, _R, _i, _i, _i]),
+    "whiflash_attend8": (_i, [_p, _l, _i, _i, _C8, _i, _R, _p, _i, _f, _p, _p, _sz, _p]),
+    "whiflash_token_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
+    "whiflash_token_logprobs": (_i, [_p, _i, _i, _i, _l, _i, _p, _i, _p, _i, _p, _p, _p, _p, _p, _sz, _p]),
+}
+
+_FN = None
+
+
+def functions():
+    """The library's functions of this module, with their signatures set."""
+    global _FN
+    if _FN is None:
+        handle = lib()
+        fns = {}
+        for name, (res, args) in _SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.restype = res
+            fn.argtypes = args
+            fns[name[len("whiflash_"):]] = fn
+        _FN = type("Functions", (), {k: staticmethod(v) for k, v in fns.items()})
+    return _FN
+
+
+# ----------------------------------------------------------------------------- rotary positions
+
+
+def rotary_frequencies(pairs: int, base: float = 10000.0, scaling=None):
+    """(frequencies, magnitude): the frequencies base ** (-i / pairs) as a list of floats, and the
+    factor of the turned pairs.  scaling, for contexts longer than the trained one:
+
+      None
+      ("linear", factor)         positions divided by factor
+      ("base", factor)           the base raised so that the slowest pair is slowed by factor and the
+                                 fastest not at all
+      ("wavelength", factor, low, high, trained)   pairs whose wavelength is above trained / low are
+                                 slowed by factor, those below trained / high not, between them in
+                                 proportion to trained / wavelength
+      ("turns", factor, slow, fast, trained)       pairs that turn fewer than `slow` times over the
+                                 trained context are slowed by factor, those that turn more than `fast`
+                                 times not, between them linearly in the pair's index; the magnitude is
+                                 1 + 0.1 ln factor
+    """
+    if pairs < 1 or not base > 0:
+        raise ValueError("pairs must be at least 1 and base positive")
+    plain = [base ** (-i / pairs) for i in range(pairs)]
+    if scaling is None:
+        return plain, 1.0
+    kind, factor, *more = scaling
+    if not factor > 0:
+        raise ValueError("the factor of a scaling must be positive")
+    if kind == "linear":
+        return [f / factor for f in plain], 1.0
+    if kind == "base":
+        raised = base * factor ** (pairs / (pairs - 1)) if pairs > 1 else base
+        return [raised ** (-i / pairs) for i in range(pairs)], 1.0
+    if kind == "wavelength":
+        low, high, trained = more
+        if not 0 < low < high:
+            raise ValueError("a scaling by wavelength needs 0 < low < high")
+        out = []
+        for f in plain:
+            share = min(max((trained * f / (2 * math.pi) - low) / (high - low), 0.0), 1.0)
+            out.append((1 - share) * f / factor + share * f)
+        return out, 1.0
+    if kind == "turns":
+        slow, fast, trained = more
+        if not 0 < slow < fast or not base > 1:
+            raise ValueError("a scaling by turns needs 0 < slow < fast and a base above 1")
+        # the index of the pair that turns n times over the trained context
+        at = lambda n: pairs * math.log(trained / (2 * math.pi * n)) / math.log(base)  # noqa: E731
+        lo = max(math.floor(at(fast)), 0)
+        hi = min(math.ceil(at(slow)), pairs - 1)
+        out = []
+        for i, f in enumerate(plain):
+            share = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+            out.append(share * f / factor + (1 - share) * f)
+        return out, 1 + 0.1 * math.log(factor) if factor > 1 else 1.0
+    raise ValueError(f"unknown scaling {kind!r}")
+
+
+class Rotary:
+    """Rotary positions (wf_rotary): frequency [pairs] float64 on the GPU, radians a position; layout
+    "half" (pair i: elements i and i + pairs) or "interleaved" (2 i and 2 i + 1); magnitude, the
+    factor of the turned pairs.  Holds its tensor."""
+
+    __slots__ = ("struct", "ref", "frequency", "pairs", "index")
+
+    def __init__(self, frequency, *, layout: str = "half", magnitude: float = 1.0):
+        _device_tensor(frequency, "frequency")
+        if frequency.dtype != torch.float64 or frequency.dim() != 1 or not frequency.is_contiguous():
+            raise TypeError("frequency must be a contiguous 1-D float64 tensor")
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"unknown layout {layout!r}")
+        self.frequency, self.pairs, self.index = frequency, frequency.numel(), frequency.get_device()
+        self.struct = _RotaryStruct(frequency.data_ptr(), self.pairs,
+                                    ROTARY_INTERLEAVED if layout == "interleaved" else ROTARY_HALF, magnitude)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def of(cls, pairs: int, base: float = 10000.0, *, scaling=None, layout: str = "half", device="cuda"):
+        """The positions of rotary_frequencies(pairs, base, scaling)."""
+        frequency, magnitude = rotary_frequencies(pairs, base, scaling)
+        return cls(torch.tensor(frequency, dtype=torch.float64, device=device), layout=layout, magnitude=magnitude)
+
+
+def _heads(x, name, rows, like=None):
+    """Row stride of [rows, heads, head_dim] vectors, each row contiguous."""
+    _device_tensor(x, name)
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != rows:
+        raise ValueError(f"{name} must be [{rows}, heads, head_dim]")
+    if like is not None and (shape[2] != like.shape[2] or x.dtype != like.dtype or x.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have the head size, type and device of q")
+    if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return st[0] if rows > 1 else shape[1] * shape[2]
+
+
+def _turned(x, name, rows, q, out):
+    stride = _heads(x, name, rows, q)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    out_stride = _heads(out, name + "_out", rows, q)
+    if out.shape != x.shape:
+        raise ValueError(f"{name}_out must have the shape of {name}")
+    return out, _RotaryRowsStruct(x.data_ptr(), out.data_ptr(), stride, out_stride, x.shape[1])
+
+
+def rotate(q, k, rows: RoundRows, rotary: Rotary, context, *, seqs=None, q_out=None, k_out=None, stream=None):
+    """Queries and keys [rows, heads, head_dim] of a round's rows turned by their positions: context
+    [sequences] int32 of the row's sequence plus its depth (see whiflash_rotate).  k may be None;
+    q_out, k_out: tensors of their shapes (q and k themselves for in place), or None for new ones.
+    Returns (q_out, k_out)."""
+    _i32(context, "context")
+    for t, name in ((q, "q"), (context, "context"), (rotary, "rotary")):
+        if (t.index if t is rotary else t.get_device()) != rows.index:
+            raise ValueError(f"{name} is not on the round's GPU {rows.index}")
+    seq = None if seqs is None else _ints(seqs, "seqs", rows.B, rows.index)
+    raw, ctx = _enter(rows.index, stream)
+    try:
+        q_out, one = _turned(q, "q", rows.total, q, q_out)
+        two = None
+        if k is not None:
+            k_out, two = _turned(k, "k", rows.total, q, k_out)
+        _check(functions().rotate(rotary.ref, _dtype_code(q), q.shape[2], rows.ref, seq, context.data_ptr(),
+                                  context.numel(), one, two, raw))
+    finally:
+        _leave(ctx)
+    return q_out, k_out
+
+
+# ----------------------------------------------------------------------------- cache
+
+
+class PageCache8:
+    """A paged key-value cache of 8 bits (wf_page_cache8).  k, v [layers, pages, heads, page_size,
+    head_dim] (or without layers) float8_e4m3fn, each page contiguous; k_scale, v_scale [layers, pages,
+    heads, page_size / block] uint8, the exponents of the blocks' scales plus 127, each page
+    contiguous; table [seqs, max_pages], held, context [seqs], refs [pages] int32.  Holds its
+    tensors, which the calls update in place."""
+
+    __slots__ = ("struct", "ref", "pages_ref", "k", "v", "k_scale", "v_scale", "table", "held", "context", "refs",
+                 "device", "index", "heads", "head_dim", "seqs", "block")
+
+    def __init__(self, k, v, k_scale, v_scale, table, held, context, refs):
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale), ("table", table)):
+            _device_tensor(t, name)
+        if k.dim() not in (4, 5) or v.shape != k.shape or v.stride() != k.stride() or \
+                k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype:
+            raise ValueError("k and v must be [layers,] pages, heads, page_size, head_dim tensors of float8_e4m3fn "
+                             "and of one shape and strides")
+        pages, heads, page, dim = k.shape[-4:]
+        st = k.stride()
+        if st[-1] != 1 or st[-2] != dim or st[-3] != page * dim:
+            raise ValueError("each page of k and v must be contiguous")
+        layered = k.dim() == 5
+        layers = k.shape[0] if layered else 1
+        ss = k_scale.stride()
+        if k_scale.dim() != k.dim() - 1 or k_scale.shape[:-1] != k.shape[:-2] or v_scale.shape != k_scale.shape or \
+                v_scale.stride() != ss or k_scale.dtype != torch.uint8 or v_scale.dtype != torch.uint8:
+            raise ValueError("k_scale and v_scale must be [layers,] pages, heads, blocks tensors of uint8 and of one "
+                             "shape and strides")
+        blocks = k_scale.shape[-1]
+        if blocks < 1 or page % blocks:
+            raise ValueError(f"{blocks} blocks do not divide a page of {page} positions")
+        if (blocks > 1 and ss[-1] != 1) or (heads > 1 and ss[-2] != blocks):
+            raise ValueError("each page of k_scale and v_scale must be contiguous")
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs, max_pages]")
+        seqs, most = table.shape
+        index = self.index = k.get_device()
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, k on {k.device}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.table, self.held, self.context, self.refs = table, held, context, refs
+        self.device, self.heads, self.head_dim, self.seqs, self.block = k.device, heads, dim, seqs, page // blocks
+        pages_struct = _CacheStruct(
+            k.data_ptr(), v.data_ptr(), st[0] if layered else 0, st[-4] if pages > 1 else heads * page * dim,
+            WF_E4M3, layers, pages, heads, page, dim, seqs, most, _ints(table, "table", seqs * most, index),
+            _ints(held, "held", seqs, index), _ints(context, "context", seqs, index),
+            _ints(refs, "refs", pages, index))
+        self.struct = _Cache8Struct(pages_struct, k_scale.data_ptr(), v_scale.data_ptr(), ss[0] if layered else 0,
+                                    ss[-3] if pages > 1 else heads * blocks, self.block)
+        self.ref = ctypes.byref(self.struct)
+        self.pages_ref = ctypes.byref(self.struct.pages)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, heads: int, page_size: int, head_dim: int, seqs: int, max_pages: int,
+              *, block: int = 1, device="cuda"):
+        """A cache of free pages and empty sequences, a scale for every `block` positions of a head."""
+        if block < 1 or page_size % block:
+            raise ValueError(f"blocks of {block} do not divide a page of {page_size} positions")
+        shape = (layers, pages, heads, page_size, head_dim)
+        i32 = dict(dtype=_I32, device=device)
+        zeros = lambda: torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)  # noqa: E731
+        scales = lambda: torch.full((*shape[:3], page_size // block), 27, dtype=torch.uint8, device=device)  # noqa: E731
+        return cls(zeros(), zeros(), scales(), scales(), torch.full((seqs, max_pages), -1, **i32),
+                   torch.zeros(seqs, **i32), torch.zeros(seqs, **i32), torch.zeros(pages, **i32))
+
+    # What cache_append, attend, cache_compact and cache_fork do with such a cache.
+
+    def _append(self, rows, k_rows, v_rows, layer, seqs, stream):
+        seq = _seqs(self, rows, seqs)
+        ks = _vectors8(k_rows, "k_rows", rows.total, self.heads, self)
+        vs = _vectors8(v_rows, "v_rows", rows.total, self.heads, self)
+        if k_rows.dtype != v_rows.dtype:
+            raise ValueError("k_rows and v_rows must have one type")
+        raw, ctx = _enter(self.index, stream)
+        try:
+            _check(functions().cache8_append(self.ref, _word(layer, "layer"), rows.ref, seq, _dtype_code(k_rows),
+                                             k_rows.data_ptr(), ks, v_rows.data_ptr(), vs, raw))
+        finally:
+            _leave(ctx)
+
+    def _attend(self, q, rows, layer, seqs, scale, max_context, out, workspace, stream):
+        seq = _seqs(self, rows, seqs)
+        qs = _vectors8(q, "q", rows.total, None, self)
+        heads, code = q.shape[1], _dtype_code(q)
+        if max_context is None:
+            max_context = self.struct.pages.max_pages * self.struct.pages.page_size
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        raw, ctx = _enter(self.index, stream)
+        try:
+            if out is None:
+                out = torch.empty((rows.total, heads, self.head_dim), dtype=q.dtype, device=self.device)
+            else:
+                _out(out, q.dtype, rows.total * heads * self.head_dim, self.device, "out")
+            size = self._attend_workspace_bytes(rows, heads, max_context, q.dtype, code)
+            ws, at, size = _scratch(workspace, size, self.device)
+            _check(functions().attend8(q.data_ptr(), qs, heads, code, self.ref, _word(layer, "layer"), rows.ref, seq,
+                                       max_context, scale, out.data_ptr(), at, size, raw))
+        finally:
+            _leave(ctx)
+        return out
+
+    def _attend_workspace_bytes(self, rows, q_heads, max_context, dtype, code=None):
+        if code is None:
+            code = {torch.float32: 0, torch.bfloat16: 1}[dtype]
+        return functions().attend8_workspace_bytes(self.ref, rows.ref, code, _word(q_heads, "q_heads"),
+                                                   _word(max_context, "max_context"))
+
+    def _compact(self, rows, accept_len, best_node, seqs, next_context, stream):
+        seq = _seqs(self, rows, seqs)
+        al, best = _verified(rows, accept_len, best_node)
+        after = None if next_context is None else _ints(next_context, "next_context", self.seqs, self.index)
+        raw, ctx = _enter(self.index, stream)
+        try:
+            _check(functions().cache8_compact(self.ref, rows.ref, seq, al, best, after, raw))
+        finally:
+            _leave(ctx)
+
+    def _fork(self, src, dst, status, workspace, stream):
+        return _pages_call(functions().cache8_fork, self, self.ref, src, dst, ("src", "dst"), status, workspace, stream)
+
+
+def _seqs(cache: PageCache8, rows: RoundRows, seqs):
+    if rows.index != cache.index:
+        raise ValueError(f"the round is on {rows.device}, the cache on {cache.device}")
+    return None if seqs is None else _ints(seqs, "seqs", rows.B, cache.index)
+
+
+def _vectors8(t, name, rows, heads, cache):
+    """Row stride of [rows, heads, head_dim] vectors of a cache's sequences, each row contiguous."""
+    stride = _heads(t, name, rows)
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{rows}, {heads or 'heads'}, {cache.head_dim}]")
+    return stride
+
+
+def cache_read(cache: PageCache8, count: int, *, seqs=None, first=None, pending: int = 0, layer: int = 0,
+               dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Reads back positions first[b] + i, i < count (first None: 0), of sequences seqs (None: all of the
+    cache's): (k, v) [B, count, heads, head_dim] of `dtype` (that of k_out and v_out where given),
+    zeros outside [0, context + pending) and where there is no page (see whiflash_cache8_read)."""
+    if not isinstance(cache, PageCache8):
+        raise TypeError("cache_read reads a PageCache8")
+    B = cache.seqs if seqs is None else seqs.numel()
+    seq = None if seqs is None else _ints(seqs, "seqs", B, cache.index)
+    at = None if first is None else _ints(first, "first", B, cache.index)
+    n = B * _word(count, "count") * cache.heads * cache.head_dim
+    if count < 0:
+        raise ValueError("count must not be negative")
+    raw, ctx = _enter(cache.index, stream)
+    try:
+        outs = []
+        for name, out in (("k_out", k_out), ("v_out", v_out)):
+            if out is None:
+                like = k_out if k_out is not None else v_out
+                out = torch.empty((B, count, cache.heads, cache.head_dim),
+                                  dtype=dtype if like is None else like.dtype, device=cache.device)
+            else:
+                _out(out, out.dtype, n, cache.device, name)
+            outs.append(out)
+        if outs[0].dtype != outs[1].dtype:
+            raise ValueError("k_out and v_out must have one type")
+        _check(functions().cache8_read(cache.ref, _word(layer, "layer"), B, seq, at, count,
+                                       _word(pending, "pending"), _dtype_code(outs[0]), outs[0].data_ptr(),
+                                       outs[1].data_ptr(), raw))
+    finally:
+        _leave(ctx)
+    return outs[0], outs[1]
+
+
+# ----------------------------------------------------------------------------- log probabilities
+
+
+def token_logprobs_workspace_bytes(n: int, V: int, top: int) -> int:
+    return functions().token_logprobs_workspace_bytes(_word(n, "n"), _word(V, "V"), _word(top, "top"))
+
+
+def token_logprobs(logits, tokens=None, *, rows=None, top: int = 0, entropy=True, workspace=None, stream=None):
+    """Log probabilities of tokens [n, given] int32 (or [n]) under the softmax of logits rows, the
+    entropies, and the `top` most likely tokens (see whiflash_token_logprobs).  logits [rows, V] or
+    [B, R, V]; rows [n] int32 selects rows (None: all of them in order).  Returns (logprob [n, given],
+    entropy [n] or None, top_tokens [n, top], top_logprobs [n, top])."""
+    _device_tensor(logits, "logits")
+    index, dev = logits.get_device(), logits.device
+    if logits.dim() not in (2, 3):
+        raise ValueError("logits must be [rows, V] or [B, R, V]")
+    total = logits.shape[0] * (logits.shape[1] if logits.dim() == 3 else 1)
+    V, stride = _rows_view(logits, total)
+    n = total if rows is None else rows.numel()
+    at = None if rows is None else _ints(rows, "rows", n, index)
+    given, ids = 0, None
+    if tokens is not None:
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != n:
+            raise ValueError(f"tokens must be [{n}] or [{n}, given]")
+        given = 1 if tokens.dim() == 1 else tokens.shape[1]
+        ids = _ints(tokens, "tokens", n * given, index)
+    raw, ctx = _enter(index, stream)
+    try:
+        logprob = torch.empty((n, given), dtype=torch.float32, device=dev)
+        spread = torch.empty(n, dtype=torch.float32, device=dev) if entropy else None
+        top_tokens = torch.empty((n, max(top, 0)), dtype=_I32, device=dev)
+        top_logprobs = torch.empty((n, max(top, 0)), dtype=torch.float32, device=dev)
+        ws, ws_at, size = _scratch(workspace, token_logprobs_workspace_bytes(n, V, top), dev)
+        _check(functions().token_logprobs(
+            logits.data_ptr(), _dtype_code(logits), _word(total, "rows"), V, stride, n, at, given, ids,
+            top, logprob.data_ptr(), None if spread is None else spread.data_ptr(), top_tokens.data_ptr(),
+            top_logprobs.data_ptr(), ws_at, size, raw))
+    finally:
+        _leave(ctx)
+    return logprob, spread, top_tokens, top_logprobs

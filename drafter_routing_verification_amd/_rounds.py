@@ -282,7 +282,7 @@ class PageCache:
     (or without layers) float32 or bfloat16, each page contiguous; table [seqs, max_pages], held,
     context [seqs], refs [pages] int32.  Holds its tensors, which the calls update in place."""
 
-    __slots__ = ("struct", "ref", "k", "v", "table", "held", "context", "refs", "device", "index",
+    __slots__ = ("struct", "ref", "pages_ref", "k", "v", "table", "held", "context", "refs", "device", "index",
                  "dtype", "heads", "head_dim", "seqs")
 
     def __init__(self, k, v, table, held, context, refs):
@@ -310,7 +310,7 @@ class PageCache:
             st[-4] if pages > 1 else heads * page * dim, _dtype_code(k), layers, pages, heads, page, dim,
             seqs, most, _ints(table, "table", seqs * most, index), _ints(held, "held", seqs, index),
             _ints(context, "context", seqs, index), _ints(refs, "refs", pages, index))
-        self.ref = ctypes.byref(self.struct)
+        self.ref = self.pages_ref = ctypes.byref(self.struct)
 
     @classmethod
     def empty(cls, layers: int, pages: int, heads: int, page_size: int, head_dim: int, seqs: int,
@@ -477,6 +477,8 @@ def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: in
                  stream=None) -> None:
     """Puts the rows' keys and values [rows, heads, head_dim] at positions context + i of their
     sequences in one layer.  seqs [B] int32: the cache sequences (None: 0 .. B-1)."""
+    if type(cache) is not PageCache:
+        return cache._append(rows, k_rows, v_rows, layer, seqs, stream)
     seq = _cache_call(cache, rows, seqs)
     ks = _vectors(k_rows, "k_rows", rows.total, cache.heads, cache)
     vs = _vectors(v_rows, "v_rows", rows.total, cache.heads, cache)
@@ -488,7 +490,11 @@ def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: in
         _leave(ctx)
 
 
-def attend_workspace_bytes(cache: PageCache, rows: RoundRows, q_heads: int, max_context: int) -> int:
+def attend_workspace_bytes(cache: PageCache, rows: RoundRows, q_heads: int, max_context: int,
+                           dtype=torch.bfloat16) -> int:
+    """Bytes of attend's workspace.  dtype: that of the queries, where the cache is a PageCache8."""
+    if hasattr(cache, "_attend_workspace_bytes"):
+        return cache._attend_workspace_bytes(rows, q_heads, max_context, dtype)
     return functions().attend_workspace_bytes(cache.ref, rows.ref, _word(q_heads, "q_heads"),
                                               _word(max_context, "max_context"))
 
@@ -498,6 +504,8 @@ def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, s
     """Attention of the rows' queries q [rows, q_heads, head_dim] over the cache.  scale: None for
     head_dim ** -0.5; max_context: an upper bound of the sequences' committed lengths that the host
     knows (None: what a table row can hold).  Returns out [rows, q_heads, head_dim]."""
+    if type(cache) is not PageCache:
+        return cache._attend(q, rows, layer, seqs, scale, max_context, out, workspace, stream)
     seq = _cache_call(cache, rows, seqs)
     qs = _vectors(q, "q", rows.total, None, cache)
     heads = q.shape[1]
@@ -525,6 +533,8 @@ def cache_compact(cache: PageCache, rows: RoundRows, accept_len, best_node=None,
     """Moves each accepted tree path's rows to the front of the round's positions, in every layer,
     and commits accept_len positions: next_context (None: the cache's context, in place) gets
     context + accept_len.  best_node may be None for rounds of chains."""
+    if type(cache) is not PageCache:
+        return cache._compact(rows, accept_len, best_node, seqs, next_context, stream)
     seq = _cache_call(cache, rows, seqs)
     al, best = _verified(rows, accept_len, best_node)
     after = None if next_context is None else _ints(next_context, "next_context", cache.seqs, cache.index)
@@ -536,10 +546,10 @@ def cache_compact(cache: PageCache, rows: RoundRows, accept_len, best_node=None,
 
 
 def cache_pages_workspace_bytes(cache: PageCache, n: int) -> int:
-    return functions().cache_pages_workspace_bytes(cache.ref, n)
+    return functions().cache_pages_workspace_bytes(cache.pages_ref, n)
 
 
-def _pages_call(fn, cache, first, second, names, status, workspace, stream):
+def _pages_call(fn, cache, ref, first, second, names, status, workspace, stream):
     _i32(first, names[0])
     n = first.numel()
     one = _ints(first, names[0], n, cache.index)
@@ -548,7 +558,7 @@ def _pages_call(fn, cache, first, second, names, status, workspace, stream):
     try:
         status = _out(status, _I32, n, cache.device, "status")
         ws, at, size = _scratch(workspace, cache_pages_workspace_bytes(cache, n), cache.device)
-        _check(fn(cache.ref, n, one, two, status.data_ptr(), at, size, raw))
+        _check(fn(ref, n, one, two, status.data_ptr(), at, size, raw))
     finally:
         _leave(ctx)
     return status
@@ -557,13 +567,15 @@ def _pages_call(fn, cache, first, second, names, status, workspace, stream):
 def cache_fork(cache: PageCache, src, dst, *, status=None, workspace=None, stream=None):
     """Makes sequence dst[i] a fork of src[i]: full pages shared, the last partly filled one copied.
     Returns status [n] int32, 1 where done, 0 where refused."""
-    return _pages_call(functions().cache_fork, cache, src, dst, ("src", "dst"), status, workspace, stream)
+    if type(cache) is not PageCache:
+        return cache._fork(src, dst, status, workspace, stream)
+    return _pages_call(functions().cache_fork, cache, cache.ref, src, dst, ("src", "dst"), status, workspace, stream)
 
 
 def cache_reserve(cache: PageCache, count, *, seqs, status=None, workspace=None, stream=None):
     """Gives sequence seqs[i] pages for context + count[i] positions.  Returns status [n] int32."""
-    return _pages_call(functions().cache_reserve, cache, seqs, count, ("seqs", "count"), status,
-                       workspace, stream)
+    return _pages_call(functions().cache_reserve, cache, cache.pages_ref, seqs, count, ("seqs", "count"),
+                       status, workspace, stream)
 
 
 def cache_free(cache: PageCache, seqs, *, stream=None) -> None:
@@ -573,6 +585,6 @@ def cache_free(cache: PageCache, seqs, *, stream=None) -> None:
     at = _ints(seqs, "seqs", n, cache.index)
     raw, ctx = _enter(cache.index, stream)
     try:
-        _check(functions().cache_free(cache.ref, n, at, raw))
+        _check(functions().cache_free(cache.pages_ref, n, at, raw))
     finally:
         _leave(ctx)

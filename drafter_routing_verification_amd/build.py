@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libwhiflash.so")
 SOURCES = ["api.hip", "sweep.hip", "finalize.hip", "router.hip", "entropy.hip", "catchup.hip", "round.hip", "early_exit.hip",
-           "noalloc.hip", "api_rounds.hip", "rules.hip", "history.hip", "attend.hip", "pages.hip"]
+           "noalloc.hip", "api_rounds.hip", "rules.hip", "history.hip", "attend.hip", "pages.hip",
+           "api_decode.hip", "rotary.hip", "cache8.hip", "attend8.hip", "logprobs.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,75 @@
+// The 8-bit values of a wf_page_cache8: e4m3 numbers under a power-of-two scale, stored as the
+// byte e + 127, which is the exponent field of 2^e.
+#pragma once
+
+#include "elem.h"
+
+namespace wf {
+
+constexpr int kLeastScale = 27, kMostScale = 246;  // e = -100 ... 119
+constexpr float kMostE4m3 = 448.f;
+constexpr unsigned kInfBits = 0x7f800000u;
+
+__device__ inline bool finite_bits(float x) { return (__float_as_uint(x) & kInfBits) != kInfBits; }
+
+__device__ inline float scale_of(unsigned byte) { return __uint_as_float(byte << 23); }
+
+// The least scale byte whose 448 * 2^e holds a magnitude: 448 is 1.75 * 2^8, so the exponent is
+// the magnitude's less 8, one more if its fraction is above 1.75.
+__device__ inline int scale_for(float amax) {
+  const int e = static_cast<int>((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;
+  return min(max(e, kLeastScale), kMostScale);
+}
+
+// x 2^-e within the format's range; NaN for what is not finite.
+__device__ inline float scaled_down(float x, float inv) {
+  return finite_bits(x) ? fminf(fmaxf(x * inv, -kMostE4m3), kMostE4m3) : NAN;
+}
+
+// Four values, already scaled, as e4m3 (nearest, ties to even), the first in the lowest byte.
+__device__ inline unsigned pack_e4m3(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<unsigned>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+
+// The four values of a word.
+__device__ inline void unpack_e4m3(unsigned w, float* x) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+  x[0] = lo[0];
+  x[1] = lo[1];
+  x[2] = hi[0];
+  x[3] = hi[1];
+}
+
+// Eight elements of a row, in float32.
+template <int DT>
+__device__ inline void load_eight(const unsigned char* p, float* x) {
+  using E = Elem<DT>;
+#pragma unroll
+  for (int h = 0; h < 8 / E::kPerVec; ++h) {
+    const u32x4 d = *reinterpret_cast<const u32x4*>(p + 16 * h);
+#pragma unroll
+    for (int k = 0; k < E::kPerVec; ++k) x[h * E::kPerVec + k] = E::at(d, k);
+  }
+}
+
+// Two float32 values as bfloat16, rounded to nearest even.
+__device__ inline unsigned two_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
+template <int DT>
+__device__ inline void store_eight(unsigned char* p, const float* x) {
+  u32x4* to = reinterpret_cast<u32x4*>(p);
+  if constexpr (DT == WF_BF16) {
+    to[0] = u32x4{two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]), two_bf16(x[6], x[7])};
+  } else {
+    to[0] = u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+    to[1] = u32x4{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])};
+  }
+}
+
+}  // namespace wf

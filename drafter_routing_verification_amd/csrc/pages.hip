@@ -29,7 +29,7 @@ struct CacheArgs {
 };
 
 CacheArgs cache_args(const wf_page_cache& c) {
-  const int per = c.dtype == WF_BF16 ? 8 : 4;
+  const int per = c.dtype == WF_E4M3 ? 16 : c.dtype == WF_BF16 ? 8 : 4;
   CacheArgs a{};
   a.k = static_cast<u32x4*>(c.k);
   a.v = static_cast<u32x4*>(c.v);
@@ -405,6 +405,15 @@ hipError_t launch_cache_append(const wf_page_cache& cache, int32_t layer, const 
   return hipGetLastError();
 }
 
+hipError_t launch_cache_commit(const wf_page_cache& cache, const RowsArgs& rows,
+                               const int32_t* seq, const int32_t* accept_len,
+                               const int32_t* best_node, int32_t* next_context,
+                               hipStream_t stream) {
+  hipLaunchKernelGGL(cache_commit_kernel, dim3((rows.B + kThreads - 1) / kThreads), dim3(kThreads),
+                     0, stream, cache_args(cache), rows, seq, accept_len, best_node, next_context);
+  return hipGetLastError();
+}
+
 hipError_t launch_cache_compact(const wf_page_cache& cache, const RowsArgs& rows,
                                 const int32_t* seq, const int32_t* accept_len,
                                 const int32_t* best_node, int32_t* next_context,
@@ -417,26 +426,29 @@ hipError_t launch_cache_compact(const wf_page_cache& cache, const RowsArgs& rows
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || after) return e;
   }
-  hipLaunchKernelGGL(cache_commit_kernel, dim3((rows.B + kThreads - 1) / kThreads), dim3(kThreads),
-                     0, stream, a, rows, seq, accept_len, best_node,
-                     after ? after : cache.context);
-  return hipGetLastError();
+  return launch_cache_commit(cache, rows, seq, accept_len, best_node, after ? after : cache.context,
+                             stream);
 }
 
 size_t pages_workspace_words(const wf_page_cache& cache, int32_t n) {
   return static_cast<size_t>(n) + 1 + 2 * static_cast<size_t>(cache.seqs) + cache.pages;
 }
 
+hipError_t launch_pages_fork(const wf_page_cache& cache, int32_t n, const int32_t* src,
+                             const int32_t* dst, int32_t* status, int32_t* ws,
+                             hipStream_t stream) {
+  hipLaunchKernelGGL((pages_alloc_kernel<true>), dim3(1), dim3(kAllocThreads), 0, stream,
+                     cache_args(cache), n, src, dst, nullptr, status, pages_ws(cache, n, ws));
+  return hipGetLastError();
+}
+
 hipError_t launch_cache_fork(const wf_page_cache& cache, int32_t n, const int32_t* src,
                              const int32_t* dst, int32_t* status, int32_t* ws,
                              hipStream_t stream) {
-  const CacheArgs a = cache_args(cache);
-  hipLaunchKernelGGL((pages_alloc_kernel<true>), dim3(1), dim3(kAllocThreads), 0, stream, a, n, src,
-                     dst, nullptr, status, pages_ws(cache, n, ws));
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = launch_pages_fork(cache, n, src, dst, status, ws, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(cache_fork_kernel, dim3(n, 2 * cache.layers), dim3(kThreads), 0, stream, a,
-                     src, dst, status);
+  hipLaunchKernelGGL(cache_fork_kernel, dim3(n, 2 * cache.layers), dim3(kThreads), 0, stream,
+                     cache_args(cache), src, dst, status);
   return hipGetLastError();
 }
 

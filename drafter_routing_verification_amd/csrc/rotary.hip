@@ -1,0 +1,262 @@
+// Rotary positions of a round's rows (whiflash_rotate): pair i of a head is turned by
+// position * frequency[i], the position being the context plus the row's depth in its tree.
+//
+// A workgroup takes a few rows of one sequence.  Their angles are computed once for all heads,
+// in float64: position * frequency loses nothing there up to positions of 2^30, and a part of a
+// turn in [-1/8, 1/8] needs no more than the series of sine and cosine around 0.  Then each
+// thread turns 16-byte vectors of pairs.
+#include <math.h>
+
+#include "decode.h"
+#include "e4m3.h"
+
+namespace wf {
+namespace {
+
+constexpr int kRotaryRows = 8;      // most rows of a workgroup
+constexpr int kMaxPairs = WHIFLASH_MAX_ROTARY_DIM / 2;
+
+struct RotaryArgs {
+  RowsArgs rows;
+  const int32_t* seq;
+  const int32_t* context;
+  int seqs, pairs, per_wg, groups_of_rows;
+  int items, copies;  // turned and copied units of a head: vectors, or elements
+  float magnitude;
+  const double* frequency;
+  int head_bytes, heads, q_heads;
+  const unsigned char *q, *k;
+  unsigned char *q_out, *k_out;
+  int64_t q_bytes, k_bytes, q_out_bytes, k_out_bytes;
+  bool q_in_place, k_in_place;
+};
+
+// Sine and cosine of an angle, times m.
+__device__ inline float2 cos_sin(double angle, float m) {
+  double t = angle * 0.15915494309189533577;  // turns
+  t -= rint(t);
+  const double n = rint(4.0 * t);
+  const double r = fma(n, -0.25, t) * 6.28318530717958647693;  // in [-pi/4, pi/4]
+  const double z = r * r;
+  // The Taylor series: the first terms left out are r^15 / 15! and r^14 / 14!, below 4e-13.
+  double s = 1.0 / 6227020800.0;
+  s = fma(s, z, -1.0 / 39916800.0);
+  s = fma(s, z, 1.0 / 362880.0);
+  s = fma(s, z, -1.0 / 5040.0);
+  s = fma(s, z, 1.0 / 120.0);
+  s = fma(s, z, -1.0 / 6.0);
+  s = fma(s * z, r, r);
+  double c = 1.0 / 479001600.0;
+  c = fma(c, z, -1.0 / 3628800.0);
+  c = fma(c, z, 1.0 / 40320.0);
+  c = fma(c, z, -1.0 / 720.0);
+  c = fma(c, z, 1.0 / 24.0);
+  c = fma(c, z, -0.5);
+  c = fma(c, z, 1.0);
+  const int q = static_cast<int>(n) & 3;
+  const double cq = q & 1 ? s : c, sq = q & 1 ? c : s;
+  return make_float2(static_cast<float>((q == 1 || q == 2 ? -cq : cq) * m),
+                     static_cast<float>((q >= 2 ? -sq : sq) * m));
+}
+
+template <int DT>
+__device__ inline void store_element(unsigned char* p, float x) {
+  if constexpr (DT == WF_BF16) {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(two_bf16(x, 0.f));
+  } else {
+    *reinterpret_cast<float*>(p) = x;
+  }
+}
+
+template <int DT>
+__device__ inline u32x4 pack_vector(const float* x) {
+  if constexpr (DT == WF_BF16)
+    return u32x4{two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]), two_bf16(x[6], x[7])};
+  else
+    return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+}
+
+// VEC: the pairs fill whole 16-byte vectors; else element by element.
+template <int DT, bool INTERLEAVED, bool VEC>
+__global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a) {
+  using E = Elem<DT>;
+  constexpr int kPer = VEC ? E::kPerVec : 1;
+  __shared__ float2 turn_s[kRotaryRows * kMaxPairs];
+  __shared__ int16_t up_s[kMaxSeqRows], deep_s[kMaxSeqRows];
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / a.groups_of_rows, i0 = (blockIdx.x - b * a.groups_of_rows) * a.per_wg;
+  const SeqRows q = seq_rows(a.rows, b);
+  if (i0 >= q.n) return;
+  const int s = slot_of(a.seq, b, a.seqs);
+  if (s < 0) return;
+  const int c = a.context[s];
+  if (c < 0) return;
+  const int rows = min(a.per_wg, q.n - i0);
+  if (q.tree) {
+    // Depths by doubling: up is the node as many edges above as deep counts, until no path goes on.
+    for (int u = tid; u < q.n; u += kThreads) {
+      const int p = u == 0 ? -1 : node_parent(a.rows, b, true, u);
+      up_s[u] = static_cast<int16_t>(p);
+      deep_s[u] = p >= 0 ? 1 : 0;
+    }
+    __syncthreads();
+    bool more = true;
+    while (__syncthreads_or(more)) {
+      int p[kRowsPerThread], d[kRowsPerThread];
+      more = false;
+#pragma unroll
+      for (int k = 0; k < kRowsPerThread; ++k) {
+        const int u = tid + k * kThreads;
+        p[k] = -1;
+        d[k] = 0;
+        if (u < q.n && up_s[u] >= 0) {
+          const int o = up_s[u];
+          p[k] = up_s[o];
+          d[k] = deep_s[o];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kRowsPerThread; ++k) {
+        const int u = tid + k * kThreads;
+        if (u < q.n && up_s[u] >= 0) {
+          up_s[u] = static_cast<int16_t>(p[k]);
+          deep_s[u] = static_cast<int16_t>(deep_s[u] + d[k]);
+          more = more || p[k] >= 0;
+        }
+      }
+    }
+  }
+  for (int t = tid; t < rows * a.pairs; t += kThreads) {
+    const int r = t / a.pairs, i = t - r * a.pairs;
+    const int depth = q.tree ? deep_s[i0 + r] : i0 + r;
+    turn_s[t] = cos_sin(static_cast<double>(static_cast<int64_t>(c) + depth) * a.frequency[i], a.magnitude);
+  }
+  __syncthreads();
+  // Threads in groups of `width`, each group a head of a row at a time.
+  const int each = a.items + a.copies;
+  const int width = min(each, kThreads), step = kThreads / width;
+  const int mine = tid / width;
+  if (mine >= step) return;
+  int r = 0, h = mine;
+  while (h >= a.heads && r < rows) {
+    h -= a.heads;
+    ++r;
+  }
+  while (r < rows) {
+    const bool key = h >= a.q_heads;
+    const int64_t row = static_cast<int64_t>(q.row0) + i0 + r;
+    const int64_t in_head = static_cast<int64_t>(key ? h - a.q_heads : h) * a.head_bytes;
+    const unsigned char* x = (key ? a.k + row * a.k_bytes : a.q + row * a.q_bytes) + in_head;
+    unsigned char* y = (key ? a.k_out + row * a.k_out_bytes : a.q_out + row * a.q_out_bytes) + in_head;
+    const float2* turn = turn_s + r * a.pairs;
+    for (int j = tid - mine * width; j < each; j += width) {
+      if (j >= a.items) {  // past the turned part
+        if (key ? a.k_in_place : a.q_in_place) break;
+        const int at = 2 * a.pairs * E::kBytes + (j - a.items) * kPer * E::kBytes;
+        if constexpr (VEC) {
+          *reinterpret_cast<u32x4*>(y + at) = *reinterpret_cast<const u32x4*>(x + at);
+        } else {
+          store_element<DT>(y + at, E::scalar(x + at, 0));
+        }
+        continue;
+      }
+      if constexpr (!VEC) {
+        const int one = (INTERLEAVED ? 2 * j : j) * E::kBytes;
+        const int two = one + (INTERLEAVED ? 1 : a.pairs) * E::kBytes;
+        const float u = E::scalar(x + one, 0), v = E::scalar(x + two, 0);
+        const float2 w = turn[j];
+        store_element<DT>(y + one, u * w.x - v * w.y);
+        store_element<DT>(y + two, v * w.x + u * w.y);
+      } else if constexpr (INTERLEAVED) {
+        const u32x4 d = *reinterpret_cast<const u32x4*>(x + j * 16);
+        float o[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 w = turn[j * (kPer / 2) + e / 2];
+          const float u = E::at(d, e), v = E::at(d, e + 1);
+          o[e] = u * w.x - v * w.y;
+          o[e + 1] = v * w.x + u * w.y;
+        }
+        *reinterpret_cast<u32x4*>(y + j * 16) = pack_vector<DT>(o);
+      } else {
+        const int far = a.pairs * E::kBytes;
+        const u32x4 d = *reinterpret_cast<const u32x4*>(x + j * 16);
+        const u32x4 f = *reinterpret_cast<const u32x4*>(x + far + j * 16);
+        float o[kPer], p[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const float2 w = turn[j * kPer + e];
+          const float u = E::at(d, e), v = E::at(f, e);
+          o[e] = u * w.x - v * w.y;
+          p[e] = v * w.x + u * w.y;
+        }
+        *reinterpret_cast<u32x4*>(y + j * 16) = pack_vector<DT>(o);
+        *reinterpret_cast<u32x4*>(y + far + j * 16) = pack_vector<DT>(p);
+      }
+    }
+    h += step;
+    while (h >= a.heads && r < rows) {
+      h -= a.heads;
+      ++r;
+    }
+  }
+}
+
+template <int DT>
+void launch_typed(const RotaryArgs& a, bool interleaved, bool vec, unsigned blocks, hipStream_t stream) {
+  const dim3 grid(blocks), block(kThreads);
+  if (interleaved && vec) hipLaunchKernelGGL((rotate_kernel<DT, true, true>), grid, block, 0, stream, a);
+  if (interleaved && !vec) hipLaunchKernelGGL((rotate_kernel<DT, true, false>), grid, block, 0, stream, a);
+  if (!interleaved && vec) hipLaunchKernelGGL((rotate_kernel<DT, false, true>), grid, block, 0, stream, a);
+  if (!interleaved && !vec) hipLaunchKernelGGL((rotate_kernel<DT, false, false>), grid, block, 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_rotate(const wf_rotary& rotary, int dtype, int32_t head_dim, const RowsArgs& rows,
+                         const int32_t* seq, const int32_t* context, int32_t seqs,
+                         const wf_rotary_rows& q, const wf_rotary_rows* k, hipStream_t stream) {
+  const int bytes = dtype == WF_BF16 ? 2 : 4, per = 16 / bytes;
+  const bool interleaved = rotary.layout == WF_ROTARY_INTERLEAVED;
+  const bool vec = (interleaved ? 2 * rotary.pairs : rotary.pairs) % per == 0;
+  RotaryArgs a{};
+  a.rows = rows;
+  a.seq = seq;
+  a.context = context;
+  a.seqs = seqs;
+  a.pairs = rotary.pairs;
+  a.frequency = rotary.frequency;
+  a.magnitude = rotary.magnitude;
+  a.items = vec ? (interleaved ? 2 * rotary.pairs : rotary.pairs) / per : rotary.pairs;
+  a.copies = (head_dim - 2 * rotary.pairs) / (vec ? per : 1);
+  a.head_bytes = head_dim * bytes;
+  a.q_heads = q.heads;
+  a.heads = q.heads + (k ? k->heads : 0);
+  a.q = static_cast<const unsigned char*>(q.x);
+  a.q_out = static_cast<unsigned char*>(q.out);
+  a.q_bytes = q.stride * bytes;
+  a.q_out_bytes = q.out_stride * bytes;
+  a.q_in_place = q.x == q.out;
+  if (k) {
+    a.k = static_cast<const unsigned char*>(k->x);
+    a.k_out = static_cast<unsigned char*>(k->out);
+    a.k_bytes = k->stride * bytes;
+    a.k_out_bytes = k->out_stride * bytes;
+    a.k_in_place = k->x == k->out;
+  }
+  // As many rows a workgroup as leave every CU several workgroups.
+  a.per_wg = kRotaryRows;
+  while (a.per_wg > 1 && static_cast<int64_t>(rows.B) * ((rows.rmax + a.per_wg - 1) / a.per_wg) < 2048)
+    a.per_wg /= 2;
+  a.groups_of_rows = (rows.rmax + a.per_wg - 1) / a.per_wg;
+  const unsigned blocks = static_cast<unsigned>(rows.B) * a.groups_of_rows;
+  if (dtype == WF_BF16) {
+    launch_typed<WF_BF16>(a, interleaved, vec, blocks, stream);
+  } else {
+    launch_typed<WF_F32>(a, interleaved, vec, blocks, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace wf

@@ -55,6 +55,13 @@ hipError_t launch_cache_compact(const wf_page_cache& cache, const RowsArgs& rows
                                 const int32_t* seq, const int32_t* accept_len,
                                 const int32_t* best_node, int32_t* next_context,
                                 hipStream_t stream);
+// The committed lengths alone, and a fork's pages alone (the copies come after them).
+hipError_t launch_cache_commit(const wf_page_cache& cache, const RowsArgs& rows,
+                               const int32_t* seq, const int32_t* accept_len,
+                               const int32_t* best_node, int32_t* next_context,
+                               hipStream_t stream);
+hipError_t launch_pages_fork(const wf_page_cache& cache, int32_t n, const int32_t* src,
+                             const int32_t* dst, int32_t* status, int32_t* ws, hipStream_t stream);
 // int32 words of scratch of the page bookkeeping for n entries.
 size_t pages_workspace_words(const wf_page_cache& cache, int32_t n);
 hipError_t launch_cache_fork(const wf_page_cache& cache, int32_t n, const int32_t* src,

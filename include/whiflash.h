@@ -46,8 +46,9 @@
 extern "C" {
 #endif
 
-/* Element type of logits, hidden states and router weights. */
-typedef enum { WF_F32 = 0, WF_BF16 = 1 } wf_dtype;
+/* Element type of logits, hidden states and router weights; WF_E4M3 (8 bits: a sign, four
+ * exponent and three fraction bits, no infinities) is that of a wf_page_cache8 alone. */
+typedef enum { WF_F32 = 0, WF_BF16 = 1, WF_E4M3 = 2 } wf_dtype;
 
 typedef enum {
   WF_OK = 0,
@@ -790,6 +791,159 @@ int32_t whiflash_cache_reserve(const wf_page_cache* cache, int32_t n, const int3
  */
 int32_t whiflash_cache_free(const wf_page_cache* cache, int32_t n, const int32_t* seq,
                             hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A decoding step around the round: rotary positions, the paged cache held in 8
+ * bits and the attention over it, log probabilities.
+ * ------------------------------------------------------------------------- */
+
+enum { WF_ROTARY_HALF = 0, WF_ROTARY_INTERLEAVED = 1 };
+
+/* Largest head that whiflash_rotate takes. */
+#define WHIFLASH_MAX_ROTARY_DIM 512
+
+/*
+ * Rotary positions: pair i of a head, elements (i, i + pairs) in the half layout and
+ * (2 i, 2 i + 1) in the interleaved one, is turned by position * frequency[i] radians and
+ * multiplied by magnitude; the head's elements from 2 * pairs on are not turned.
+ *   frequency [pairs] float64 (device), 1 <= pairs <= head_dim / 2; magnitude is finite.
+ */
+typedef struct wf_rotary {
+  const double* frequency;
+  int32_t pairs, layout;
+  float magnitude;
+} wf_rotary;
+
+/* Rows of heads * head_dim elements, `stride` elements apart, and where they are written.  out
+ * may be x itself with the same stride; otherwise they must not overlap. */
+typedef struct wf_rotary_rows {
+  const void* x;
+  void* out;
+  int64_t stride, out_stride;
+  int32_t heads;
+} wf_rotary_rows;
+
+/*
+ * Turns the queries and keys of a round's rows by their positions: row i of sequence b is at
+ * context[s] + the edges of its path (a chain's row i: i), s = seq[b] (seq NULL: b).  The
+ * elements that are not turned are copied.
+ *   q, k: of element type dtype (bases and strides multiples of 16 bytes); k may be NULL.
+ *   head_dim * element size is a multiple of 16 bytes, head_dim at most WHIFLASH_MAX_ROTARY_DIM.
+ *   context [seqs] int32, e.g. a cache's.
+ * The angle is taken in float64 and reduced to a part of a turn before its sine and cosine, so
+ * far positions lose nothing; x' = x c - y s and y' = y c + x s (c and s with the magnitude in
+ * them) are float32 and rounded once.
+ *   Rows of malformed sequences, of sequences outside [0, seqs) or with a negative context, and
+ * rows that no sequence owns are left as they were.  B == 0 is a no-op.  No workspace.
+ */
+int32_t whiflash_rotate(const wf_rotary* rotary, int32_t dtype, int32_t head_dim,
+                        const wf_round_rows* rows, const int32_t* seq, const int32_t* context,
+                        int32_t seqs, const wf_rotary_rows* q, const wf_rotary_rows* k,
+                        hipStream_t stream);
+
+/*
+ * A paged key-value cache of 8 bits: `pages` is laid out as a wf_page_cache of dtype WF_E4M3
+ * (strides in elements, that is bytes), and every `block` positions of a head (block a power of
+ * two, at most page_size) share a scale 2^e, stored as the byte e + 127:
+ *   k_scale[l * scale_layer_stride + p * scale_page_stride + h * (page_size / block) + o / block]
+ * for position o of head h in page p of layer l (v_scale alike; strides in bytes).  A byte c
+ * stands for e4m3(c) * 2^e.
+ *   What the calls write: e is the least of -100 ... 119 with 448 * 2^e no smaller than the
+ * magnitude of any finite value among the block's committed and newly written positions, and
+ * each value is rounded to the nearest e4m3 (ties to even) of value / 2^e, at most 448 (only
+ * values past 448 * 2^119 are cut).  NaN and infinities become NaN.  Committed values of a block
+ * that gets another exponent are shifted: nothing changes unless they fall below 2^-6 * 2^e,
+ * where the spacing stops to shrink and they are rounded again.  With block 1 nothing is
+ * ever shifted.
+ *   Its whiflash_cache_reserve, _free and _pages_workspace_bytes are those of &cache->pages.
+ */
+typedef struct wf_page_cache8 {
+  wf_page_cache pages;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t scale_layer_stride, scale_page_stride;
+  int32_t block;
+} wf_page_cache8;
+
+/*
+ * whiflash_cache_append into an 8-bit cache: the same rows, positions and skipped rows, the
+ * vectors of element type dtype.  Bytes behind the new rows of a block are left as they were (the
+ * block's scale is not theirs then).  A cache sequence may occur once in seq.
+ */
+int32_t whiflash_cache8_append(const wf_page_cache8* cache, int32_t layer,
+                               const wf_round_rows* rows, const int32_t* seq, int32_t dtype,
+                               const void* k_rows, int64_t k_row_stride, const void* v_rows,
+                               int64_t v_row_stride, hipStream_t stream);
+
+/*
+ * Reads positions back: k_out, v_out [B, count, heads, head_dim] of element type dtype (16-byte
+ * aligned, either may be NULL) get what positions first[b] + i, i < count, of sequence seq[b]
+ * stand for (first NULL: 0; seq NULL: b).  Positions outside [0, context + pending), without a
+ * page, or of a sequence outside [0, seqs) or with a negative context give zeros.  pending >= 0
+ * counts positions of a round that are written and not yet committed.  Both types hold every
+ * value of the cache exactly.
+ */
+int32_t whiflash_cache8_read(const wf_page_cache8* cache, int32_t layer, int32_t B,
+                             const int32_t* seq, const int32_t* first, int32_t count,
+                             int32_t pending, int32_t dtype, void* k_out, void* v_out,
+                             hipStream_t stream);
+
+/* whiflash_cache_compact of an 8-bit cache: moved values keep what they stand for, but for the
+ * shifts of the blocks they come into. */
+int32_t whiflash_cache8_compact(const wf_page_cache8* cache, const wf_round_rows* rows,
+                                const int32_t* seq, const int32_t* accept_len,
+                                const int32_t* best_node, int32_t* next_context,
+                                hipStream_t stream);
+
+/* whiflash_cache_fork of an 8-bit cache. */
+int32_t whiflash_cache8_fork(const wf_page_cache8* cache, int32_t n, const int32_t* src,
+                             const int32_t* dst, int32_t* status, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of whiflash_attend8 (host only; 0 on bad sizes, and where none is needed). */
+size_t whiflash_attend8_workspace_bytes(const wf_page_cache8* cache, const wf_round_rows* rows,
+                                        int32_t dtype, int32_t q_heads, int32_t max_context);
+
+/*
+ * whiflash_attend over an 8-bit cache: the attention over the values that it stands for, with
+ * queries and outputs of element type dtype.  What whiflash_attend says of sights, sums,
+ * reproducibility, positions without a page, refused sequences and the workspace holds here;
+ * a NaN among the values of a seen position makes its dimension of out NaN, a NaN in its key
+ * every one.
+ */
+int32_t whiflash_attend8(const void* q, int64_t q_row_stride, int32_t q_heads, int32_t dtype,
+                         const wf_page_cache8* cache, int32_t layer, const wf_round_rows* rows,
+                         const int32_t* seq, int32_t max_context, float scale, void* out,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Most alternatives of whiflash_token_logprobs. */
+#define WHIFLASH_MAX_TOP 64
+
+/* Workspace bytes of whiflash_token_logprobs (host only; 0 on bad sizes). */
+size_t whiflash_token_logprobs_workspace_bytes(int32_t n, int32_t V, int32_t top);
+
+/*
+ * Log probabilities under the softmax of logits rows:
+ *   logprob[i, j] = log softmax(row i)[tokens[i, j]]        (tokens [n, given] int32)
+ *   entropy[i]    = -sum p log p, in nats                   (may be NULL)
+ *   top_tokens, top_logprobs [n, top]: the `top` most likely tokens, the most likely first and
+ *     the lowest index first among equal logits.
+ *   logits: total_rows rows of V entries, row_stride apart.  Row i is rows[i] (int32, rows NULL:
+ *   i, and then n is at most total_rows).  0 <= given <= 65536, 0 <= top <= WHIFLASH_MAX_TOP;
+ *   V is at most 2^30.
+ * Sums are float32 relative to the row's maximum, in an order that n and V fix.  Entries of
+ * -inf have probability 0: log probability -inf, no part of the entropy, and no alternatives: places
+ * without one hold token -1 and -inf.  A token outside [0, V) has log probability NaN.  A row
+ * outside [0, total_rows), one of only -inf and one that holds NaN or +inf has NaN for logprob,
+ * entropy and top_logprobs; its top_tokens are -1.  n == 0 is a no-op.
+ * Workspace: whiflash_token_logprobs_workspace_bytes(n, V, top), 256-byte aligned, contents
+ * ignored on entry; calls sharing one must not overlap in time.
+ */
+int32_t whiflash_token_logprobs(const void* logits, int32_t dtype, int32_t total_rows, int32_t V,
+                                int64_t row_stride, int32_t n, const int32_t* rows, int32_t given,
+                                const int32_t* tokens, int32_t top, float* logprob, float* entropy,
+                                int32_t* top_tokens, float* top_logprobs, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
