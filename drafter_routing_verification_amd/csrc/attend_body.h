@@ -1,0 +1,722 @@
+// What the attention over a paged cache of float32 or bfloat16 (attend.hip) and that over one of 8
+// bits (attend8.hip) share: the products and their layouts, a wave's queries with their running
+// softmax, the walk over a sequence's pages, and the join of pieces.
+//
+// A wave walks its share of the positions in tiles of 16 or 32, keeping each query's running
+// maximum m, sum l and output O in registers:
+//   S^T = K Q^T           (MFMA; a lane holds one query's scores of four positions)
+//   p = 2^(s - m), l += p (the softmax in base 2, one pass)
+//   O^T += V^T P^T        (MFMA)
+// The transposed products keep everything in registers.  A lane's scores all belong to
+// query lane % 16, so m, l and the rescaling of O are one value a lane, and the scores'
+// layout is the second product's operand layout if V's positions take the same order.
+#pragma once
+
+#include <math.h>
+
+#include "elem.h"
+#include "rounds.h"
+
+namespace wf {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLowest = -3.0e38f;  // a maximum of nothing: finite, so that no inf - inf arises
+// O is rescaled only when a maximum grows by more than this (base 2): the weights then
+// stay below 2^8, and most tiles need no rescaling.
+constexpr float kSlack = 8.f;
+constexpr int kJoinAhead = 8;      // pieces whose outputs are fetched at once
+
+struct AttendArgs {
+  RowsArgs rows;
+  const unsigned char* q;
+  int64_t q_bytes;
+  int q_heads, group;
+  const unsigned char* k;  // the layer
+  const unsigned char* v;
+  int64_t page_bytes;
+  int pages, heads, page_log, seqs, max_pages;
+  const int32_t* table;
+  const int32_t* context;
+  const int32_t* seq;
+  int max_context;
+  float scale_log2;  // |scale| log2(e)
+  unsigned flip;     // the sign bits to flip in q (scale < 0)
+  unsigned char* out;
+  int splits, span, mgroups;
+  float* part_o;     // [splits][rows x q_heads][D]
+  float2* part_ml;   // [splits][rows x q_heads]
+  int64_t row_heads;
+};
+
+// One sequence's part of a launch: its rows, cache sequence and committed length
+// (-1: its rows get zeros).
+struct SeqCall {
+  SeqRows q;
+  int s, c;
+};
+
+__device__ inline SeqCall seq_call(const AttendArgs& a, int b) {
+  SeqCall x;
+  x.q = seq_rows(a.rows, b);
+  x.s = slot_of(a.seq, b, a.seqs);
+  x.c = x.s < 0 ? -1 : a.context[x.s];
+  if (x.c > a.max_context ||
+      static_cast<int64_t>(x.c) + x.q.n > static_cast<int64_t>(a.max_pages) << a.page_log)
+    x.c = -1;
+  if (x.c < 0) x.c = -1;
+  return x;
+}
+
+// Max over the four 16-lane rows of a wave, for each of their 16 places.
+__device__ inline float rows_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ inline float rows_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Two float32 values as bfloat16, rounded to nearest even.
+__device__ inline unsigned pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 r = __builtin_convertvector((f32x2{lo, hi}), bf16x2);
+  return __builtin_bit_cast(unsigned, r);
+}
+
+// Infinities and NaN among values that not every query sees go apart from the product, where
+// they would meet the weights of zero of those queries too.  What they make of sum p v, in
+// four rounds, each the count of the seen positions whose value is of a kind: infinities
+// of either sign add theirs, NaN make NaN, and so do infinities whose weight is zero itself.
+constexpr int kOddRounds = 4;
+
+// Float32 bits x are of the round's kind if (x & mask) - low <= span.
+struct OddKind {
+  unsigned mask, low, span;
+  float effect;
+};
+
+__device__ inline OddKind odd_kind(int round) {
+  if (round == 0) return OddKind{0xffffffffu, 0x7f800000u, 0u, INFINITY};
+  if (round == 1) return OddKind{0xffffffffu, 0xff800000u, 0u, -INFINITY};
+  if (round == 2) return OddKind{0x7fffffffu, 0x7f800001u, 0x7ffffeu, NAN};
+  return OddKind{0x7fffffffu, 0x7f800000u, 0u, NAN};
+}
+
+// Operand fragment f of group g is the piece of sixteen bytes 4 f + g of a query or key.
+// What differs between the types: operand fragments, the two products and their tiles.
+// Lane l is place n = l % 16 of group g = l / 16.  kSub positions sub-tiles of 16 make
+// a tile; a lane's scores of sub-tile t are positions 16 t + 4 g + i, i < 4.  The
+// output tile j, element i is dimension dim(g, i, j) of query n.
+template <int DT, int D>
+struct Ops;
+
+template <int DT, int D>
+__device__ inline void store_query(unsigned char* out, const f32x4* o, int g, float f);
+template <int DT, int D>
+__device__ inline void store_partial(float* out, const f32x4* o, int g);
+
+template <int D>
+struct Ops<WF_BF16, D> {
+  static constexpr int kD = D;
+  static constexpr int kSub = 2;
+  static constexpr bool kSums = true;    // outputs() adds up the weights too
+  static constexpr int kFrags = D / 32;  // 16-byte operand vectors of a query or key
+  static constexpr int kOut = D / 16;    // output tiles
+  static constexpr int kBytes = 2;
+  static constexpr int kVecV = D / 64;   // 8-byte pieces of a lane's share of a row of V
+  struct V {
+    unsigned w[2 * 4][kVecV * 2];        // [position][dimension pairs]
+  };
+
+  __device__ static inline f32x4 scores(const u32x4* k, const u32x4* q) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[f]),
+                                                  __builtin_bit_cast(bf16x8, q[f]), s, 0, 0, 0);
+    return s;
+  }
+  // Rows 4 g + i of sub-tile t, dimensions [n D / 16, (n + 1) D / 16).
+  template <bool STREAM>
+  __device__ static inline void load_v(V& v, int t, const unsigned char* p, unsigned lane_off) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (D == 128) {
+        const u32x4 x = STREAM ? load16(reinterpret_cast<const u32x4*>(p + lane_off + i * D * 2))
+                               : *reinterpret_cast<const u32x4*>(p + lane_off + i * D * 2);
+        v.w[4 * t + i][0] = x.x;
+        v.w[4 * t + i][1] = x.y;
+        v.w[4 * t + i][2] = x.z;
+        v.w[4 * t + i][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + lane_off + i * D * 2);
+        v.w[4 * t + i][0] = x.x;
+        v.w[4 * t + i][1] = x.y;
+      }
+    }
+  }
+  __device__ static inline unsigned v_lane(int n, int g) { return (4 * g * D + n * (D / 16)) * 2; }
+  __device__ static inline void zero_v(V& v, int t, int i) {
+#pragma unroll
+    for (int x = 0; x < kVecV * 2; ++x) v.w[4 * t + i][x] = 0;
+  }
+  // o += V^T P^T for MT query tiles; p[m][t][i] the weights, rounded to bfloat16 as the matrix
+  // units take them (a part in 2^8 each), and summed as rounded, so that equal values come out
+  // as they are.  Against 64 bits the outputs are then off by 0.0022-0.0024 (root mean square,
+  // relative) where their own rounding alone gives 0.0017.  Weights as two bfloat16 halves give
+  // 0.0017, in the same time for one row a sequence (256 us), but 88 us against 77 for the trees
+  // and 223 against 188 for the long chains, and an infinity among the values would meet lower
+  // halves of zero: not taken.
+  template <int MT>
+  __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4* sum, const V& v,
+                                        const float (*p)[kSub][4]) {
+    bf16x8 pb[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const u32x4 x = {pack_bf16(p[m][0][0], p[m][0][1]), pack_bf16(p[m][0][2], p[m][0][3]),
+                       pack_bf16(p[m][1][0], p[m][1][1]), pack_bf16(p[m][1][2], p[m][1][3])};
+      pb[m] = __builtin_bit_cast(bf16x8, x);
+    }
+    // The sums of the rounded weights: a product with ones, in place of 8 additions.
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pb[m], sum[m], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      // Element j of each position's dimensions, two positions a word.
+      u32x4 a;
+      unsigned w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        w[x] = __builtin_amdgcn_perm(v.w[2 * x + 1][j >> 1], v.w[2 * x][j >> 1],
+                                     (j & 1) ? 0x07060302u : 0x05040100u);
+      a = u32x4{w[0], w[1], w[2], w[3]};
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        o[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), pb[m],
+                                                          o[m][j], 0, 0, 0);
+    }
+  }
+  static constexpr int kQ = kFrags;
+  // Operand fragment f of a query, for group g.
+  __device__ static inline u32x4 q_fragment(const unsigned char* p, int f, int g, unsigned flip) {
+    return *reinterpret_cast<const u32x4*>(p + (4 * f + g) * 16) ^ flip;
+  }
+  __device__ static inline void store_out(unsigned char* out, const f32x4* o, int g, float f) {
+    store_query<WF_BF16, D>(out, o, g, f);
+  }
+  __device__ static inline void store_part(float* out, const f32x4* o, int g) {
+    store_partial<WF_BF16, D>(out, o, g);
+  }
+
+  // Whether the lane's values hold infinities or NaN.
+  __device__ static inline bool odd(const V& v) {
+    bool x = false;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < kVecV * 2; ++c)
+        x = x || (v.w[r][c] & 0x7f80u) == 0x7f80u || (v.w[r][c] & 0x7f800000u) == 0x7f800000u;
+    return x;
+  }
+  // Adds to the outputs what infinities and NaN among the values make of them (odd_kind), and
+  // puts zeros in their place.  see[m]: the positions that the lane's query of tile m sees,
+  // a bit each.
+  template <int MT>
+  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4],
+                                       const unsigned* see) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll 1
+    for (int round = 0; round < kOddRounds; ++round) {
+      const OddKind kind = odd_kind(round);
+      bf16x8 pb[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        unsigned w[4] = {0u, 0u, 0u, 0u}, bits = see[m] >> (4 * g);
+        asm volatile("" : "+v"(bits));  // (worked out in each round: it would take registers)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool seen = bits >> (16 * t + i) & 1u;
+            const bool on = seen && (round < kOddRounds - 1 || !(p[m][t][i] > 0.f));
+            w[2 * t + i / 2] |= on ? 0x3f80u << (i % 2 * 16) : 0u;
+          }
+        pb[m] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+      }
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        unsigned w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          // (A half is compared where it lies: in the lower one everything is shifted.)
+          const int down = (j & 1) ? 0 : 16;
+          const unsigned mask = (kind.mask & 0xffff0000u) >> down;
+          const unsigned low = ((kind.low + 0xffffu) & 0xffff0000u) >> down, span = kind.span >> down;
+          w[x] = (v.w[2 * x][j >> 1] & mask) - low <= span ? 0x3f80u : 0u;
+          w[x] |= (v.w[2 * x + 1][j >> 1] & mask) - low <= span ? 0x3f800000u : 0u;
+        }
+        const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x4 n = {0.f, 0.f, 0.f, 0.f};
+          n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[m], n, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[m][j][i] += n[i] > 0.f ? kind.effect : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < kVecV * 2; ++c) {
+        const unsigned x = v.w[r][c];
+        v.w[r][c] = ((x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu) |
+                    ((x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u);
+      }
+  }
+};
+
+template <int D>
+struct Ops<WF_F32, D> {
+  static constexpr int kD = D;
+  static constexpr int kSub = 1;
+  static constexpr bool kSums = false;
+  static constexpr int kFrags = D / 16;
+  static constexpr int kOut = D / 16;
+  static constexpr int kBytes = 4;
+  struct V {
+    f32x4 w[4][D / 64];
+  };
+  __device__ static inline f32x4 scores(const u32x4* k, const u32x4* q) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+      const f32x4 kf = __builtin_bit_cast(f32x4, k[f]), qf = __builtin_bit_cast(f32x4, q[f]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[e], qf[e], s, 0, 0, 0);
+    }
+    return s;
+  }
+  // Rows 4 g + i, dimensions 64 h + 4 n + [0, 4).
+  template <bool STREAM>
+  __device__ static inline void load_v(V& v, int, const unsigned char* p, unsigned lane_off) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        v.w[i][h] = __builtin_bit_cast(
+            f32x4, STREAM ? load16(reinterpret_cast<const u32x4*>(p + lane_off + i * D * 4 + h * 256))
+                          : *reinterpret_cast<const u32x4*>(p + lane_off + i * D * 4 + h * 256));
+  }
+  __device__ static inline unsigned v_lane(int n, int g) { return (4 * g * D + n * 4) * 4; }
+  __device__ static inline void zero_v(V& v, int, int i) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) v.w[i][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  template <int MT>
+  __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4*, const V& v,
+                                        const float (*p)[kSub][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            o[m][4 * h + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.w[i][h][e], p[m][0][i],
+                                                                   o[m][4 * h + e], 0, 0, 0);
+  }
+  static constexpr int kQ = kFrags;
+  // Operand fragment f of a query, for group g.
+  __device__ static inline u32x4 q_fragment(const unsigned char* p, int f, int g, unsigned flip) {
+    return *reinterpret_cast<const u32x4*>(p + (4 * f + g) * 16) ^ flip;
+  }
+  __device__ static inline void store_out(unsigned char* out, const f32x4* o, int g, float f) {
+    store_query<WF_F32, D>(out, o, g, f);
+  }
+  __device__ static inline void store_part(float* out, const f32x4* o, int g) {
+    store_partial<WF_F32, D>(out, o, g);
+  }
+
+  __device__ static inline bool is_odd(float x) {
+    return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
+  }
+  __device__ static inline bool odd(const V& v) {
+    bool x = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x = x || is_odd(v.w[i][h][e]);
+    return x;
+  }
+  template <int MT>
+  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const float (*p)[kSub][4],
+                                       const unsigned* see) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll 1
+    for (int round = 0; round < kOddRounds; ++round) {
+      const OddKind kind = odd_kind(round);
+      unsigned bits[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        bits[m] = see[m] >> (4 * g);
+        asm volatile("" : "+v"(bits[m]));
+      }
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            f32x4 n = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool seen = bits[m] >> i & 1u;
+              const bool on = seen && (round < kOddRounds - 1 || !(p[m][0][i] > 0.f));
+              const bool is = (__float_as_uint(v.w[i][h][e]) & kind.mask) - kind.low <= kind.span;
+              n = __builtin_amdgcn_mfma_f32_16x16x4f32(is ? 1.f : 0.f, on ? 1.f : 0.f, n, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[m][4 * h + e][i] += n[i] > 0.f ? kind.effect : 0.f;
+          }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v.w[i][h][e] = is_odd(v.w[i][h][e]) ? 0.f : v.w[i][h][e];
+  }
+};
+
+// Writes a lane's outputs of one query tile (element i of every output tile) scaled by
+// `f`: to out in the call's type, or float32.
+template <int DT, int D>
+__device__ inline void store_query(unsigned char* out, const f32x4* o, int g, float f) {
+  constexpr int kOut = Ops<DT, D>::kOut;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == WF_BF16) {
+      unsigned w[kOut / 2];
+#pragma unroll
+      for (int j = 0; j < kOut / 2; ++j) w[j] = pack_bf16(o[2 * j][i] * f, o[2 * j + 1][i] * f);
+      unsigned char* p = out + (4 * g + i) * kOut * 2;
+      if constexpr (kOut == 8) {
+        *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        *reinterpret_cast<f32x4*>(out + (64 * h + (4 * g + i) * 4) * 4) =
+            f32x4{o[4 * h][i] * f, o[4 * h + 1][i] * f, o[4 * h + 2][i] * f, o[4 * h + 3][i] * f};
+    }
+  }
+}
+
+// ... the partial output, float32 in the order of the dimensions.
+template <int DT, int D>
+__device__ inline void store_partial(float* out, const f32x4* o, int g) {
+  constexpr int kOut = Ops<DT, D>::kOut;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == WF_BF16) {
+#pragma unroll
+      for (int j = 0; j < kOut; j += 4)
+        *reinterpret_cast<f32x4*>(out + (4 * g + i) * kOut + j) =
+            f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        *reinterpret_cast<f32x4*>(out + 64 * h + (4 * g + i) * 4) =
+            f32x4{o[4 * h][i], o[4 * h + 1][i], o[4 * h + 2][i], o[4 * h + 3][i]};
+    }
+  }
+}
+
+// Orders a wave's LDS accesses: what a lane wrote before, every lane reads after.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// What a wave keeps of MT tiles of 16 queries: the queries in operand layout, and for
+// query place n of each tile m, l and O.
+template <class X, int MT>
+struct Queries {
+  u32x4 q[MT][X::kQ];
+  f32x4 o[MT][X::kOut];
+  float mx[MT];
+  f32x4 sum[MT];  // element 0: l, where kSums; else this lane's part of it
+  int first;       // the first query
+
+  // The lane's query of tile m, or -1 past the last one.
+  __device__ inline int query(const AttendArgs& a, const SeqCall& call, int m) const {
+    const int x = first + 16 * m + static_cast<int>(threadIdx.x & 15);
+    return x < call.q.n * a.group ? x : -1;
+  }
+
+  __device__ inline void load(const AttendArgs& a, const SeqCall& call, int kvh, int from) {
+    const int g = (threadIdx.x & 63) >> 4;
+    first = from;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int x = query(a, call, m);
+      const int h = kvh * a.group + max(x, 0) % a.group;
+      const int64_t r = static_cast<int64_t>(call.q.row0) + max(x, 0) / a.group;
+      const unsigned char* p = a.q + r * a.q_bytes + h * X::kD * X::kBytes;
+#pragma unroll
+      for (int f = 0; f < X::kQ; ++f) {
+        q[m][f] = u32x4{0u, 0u, 0u, 0u};
+        if (x >= 0) q[m][f] = X::q_fragment(p, f, g, a.flip);
+      }
+      mx[m] = kLowest;
+      sum[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < X::kOut; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+
+  using Weights = float[MT][X::kSub][4];
+
+  // The products q . k of sub-tile t.
+  __device__ inline void score(Weights& p, int t, const u32x4* k) const {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const f32x4 s = X::scores(k, q[m]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[m][t][i] = s[i];
+    }
+  }
+
+  // Of the 32 positions from j0 on, those that can be seen at all: before `end` and with
+  // a page (`pages`: a bit each).
+  __device__ static inline unsigned visible(int j0, int end, unsigned pages) {
+    const int have = min(max(end - j0, 0), 32);
+    return pages & (have >= 32 ? ~0u : (1u << have) - 1u);
+  }
+
+  // Takes positions that no query sees out of a tile's scores and values: whatever lies
+  // there must not meet a weight of zero, it may be NaN.
+  __device__ static inline void hide(Weights& p, typename X::V& v, unsigned any) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(any >> (16 * t + 4 * g + i) & 1u)) {
+          X::zero_v(v, t, i);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) p[m][t][i] = -INFINITY;
+        }
+  }
+
+  // Takes out of a tile's scores what its query does not see: positions outside `any`,
+  // and of the round's own positions those of rows that are not on its path.  see[m] gets the
+  // positions that the lane's query of tile m sees.
+  __device__ inline void mask(Weights& p, unsigned* see, int j0, unsigned any, const AttendArgs& a,
+                              const SeqCall& call, const int16_t* par) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    const int old = min(max(call.c - j0, 0), 32);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      see[m] = old >= 32 ? ~0u : (1u << old) - 1u;
+      const int x0 = query(a, call, m);
+      const int own = x0 < 0 ? -1 : x0 / a.group, last = call.c + own - j0;
+      if (!call.q.tree) {
+        if (own >= 0 && last >= 0) see[m] = last >= 31 ? ~0u : (2u << last) - 1u;
+      } else {
+        for (int u = own; u >= 0 && call.c + u >= j0; u = u == 0 ? -1 : par[u]) {
+          const int x = call.c + u - j0;
+          if (x < 32) see[m] |= 1u << x;
+        }
+      }
+      see[m] &= any;
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(see[m] >> (16 * t + 4 * g + i) & 1u)) p[m][t][i] = -INFINITY;
+    }
+  }
+
+  // Products to weights 2^(scale q . k - m), with the running maxima (of the scaled
+  // products; scale > 0, its sign is in q) and, where the output product does not give
+  // them, the sums.
+  __device__ inline void soften(Weights& p, float scale) {
+    bool grown = false;
+    float top[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float x = p[m][0][0];
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = fmaxf(x, p[m][t][i]);
+      top[m] = rows_max(x) * scale;
+      grown = grown || top[m] > mx[m] + kSlack;
+    }
+    if (__any(grown)) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float now = fmaxf(mx[m], top[m]);
+        const float f = __builtin_amdgcn_exp2f(mx[m] - now);
+        mx[m] = now;
+        sum[m] *= f;
+#pragma unroll
+        for (int j = 0; j < X::kOut; ++j) o[m][j] *= f;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[m][t][i] = __builtin_amdgcn_exp2f(fmaf(p[m][t][i], scale, -mx[m]));
+          if constexpr (!X::kSums) sum[m][0] += p[m][t][i];
+        }
+    }
+  }
+
+  // The result of a piece: the output if it is the only one, else its part.
+  __device__ inline void store(const AttendArgs& a, const SeqCall& call, int kvh, int split) const {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int x = query(a, call, m);
+      if (x < 0) continue;
+      const int64_t to = (static_cast<int64_t>(call.q.row0) + x / a.group) * a.q_heads +
+                         kvh * a.group + x % a.group;
+      if (a.splits == 1) {
+        X::store_out(a.out + to * X::kD * X::kBytes, o[m], g, sum[m][0] > 0.f ? 1.f / sum[m][0] : 0.f);
+      } else {
+        const int64_t at = split * a.row_heads + to;
+        X::store_part(a.part_o + at * X::kD, o[m], g);
+        if (g == 0) a.part_ml[at] = make_float2(mx[m], sum[m][0]);
+      }
+    }
+  }
+};
+
+// The pages of one sequence as a wave walks it: the ids of 64 sub-tiles at a time, one a
+// lane (-1: none).
+struct PageWalk {
+  const int32_t* table;
+  int log, pages, stop, base, ids;
+
+  __device__ inline void fetch(int from) {
+    const int j = from + 16 * static_cast<int>(threadIdx.x & 63);
+    base = from;
+    ids = j < stop ? table[j >> log] : -1;
+    if (ids >= pages) ids = -1;
+  }
+  __device__ inline PageWalk(const AttendArgs& a, const SeqCall& call, int from, int to)
+      : table(a.table + static_cast<int64_t>(max(call.s, 0)) * a.max_pages), log(a.page_log),
+        pages(a.pages), stop(to), base(from), ids(-1) {
+    if (from < to) fetch(from);
+  }
+  // The tile from j0 on (j0 grows by no more than 1,024 between calls).
+  __device__ inline void reach(int j0, int tile) {
+    if (j0 + tile - base > 64 * 16) fetch(j0);
+  }
+  // The page of sub-tile j, uniform, or -1.
+  __device__ inline int at(int j) const {
+    return __builtin_amdgcn_readlane(ids, ((j - base) >> 4) & 63);
+  }
+};
+
+// What `count` queries from `first` on see of a sequence: positions before `all` are seen by
+// every one of them, positions from `end` on by none.
+struct Sight {
+  int all, end;
+};
+
+__device__ inline Sight sight_of(const AttendArgs& a, const SeqCall& call, int first, int count) {
+  if (call.c < 0) return Sight{-1, 0};
+  if (call.q.tree) return Sight{call.c, call.c + call.q.n};
+  const int last = min(call.q.n * a.group, first + count) - 1;
+  return Sight{call.c + first / a.group + 1, call.c + last / a.group + 1};
+}
+
+// Joins the pieces of every row and head: one wave each, in the pieces' order.
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
+  constexpr int kPer = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int h = static_cast<int>(x % a.q_heads);
+  const int64_t bi = x / a.q_heads;
+  const int b = static_cast<int>(bi / a.rows.rmax), i = static_cast<int>(bi % a.rows.rmax);
+  if (b >= a.rows.B) return;
+  const SeqCall call = seq_call(a, b);
+  if (i >= call.q.n) return;
+  const int64_t r = (static_cast<int64_t>(call.q.row0) + i) * a.q_heads + h;
+  // A chain's row is not in the pieces past its own position.
+  const int end = call.c < 0 ? 0 : call.c + (call.q.tree ? call.q.n : i + 1);
+  const int used = end > 0 ? (end + a.span - 1) / a.span : 0;
+  // Lane s holds piece s's maximum and sum, 64 pieces at a time, so that the loads of
+  // the outputs depend on nothing.
+  float m = kLowest, l = 0.f, o[kPer] = {};
+  for (int s0 = 0; s0 < used; s0 += 64) {
+    const int many = min(used - s0, 64);
+    float2 y = make_float2(kLowest, 0.f);
+    if (lane < many) y = a.part_ml[(s0 + lane) * a.row_heads + r];
+    float top = y.x;
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const float now = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - now);
+    const float w = __builtin_amdgcn_exp2f(y.x - now);
+    float sum = y.y * w;
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    m = now;
+    l = l * f + sum;
+#pragma unroll
+    for (int t = 0; t < kPer; ++t) o[t] *= f;
+    for (int s = 0; s < many; s += kJoinAhead) {
+      float p[kJoinAhead][kPer];
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float* from = a.part_o + ((s0 + min(s + e, many - 1)) * a.row_heads + r) * D + lane * kPer;
+#pragma unroll
+        for (int t = 0; t < kPer; ++t) p[e][t] = from[t];
+      }
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), (s + e) & 63));
+#pragma unroll
+        for (int t = 0; t < kPer; ++t) o[t] += s + e < many ? p[e][t] * ws : 0.f;
+      }
+    }
+  }
+  const float f = l > 0.f ? 1.f / l : 0.f;
+  if constexpr (DT == WF_F32) {
+#pragma unroll
+    for (int t = 0; t < kPer; ++t)
+      reinterpret_cast<float*>(a.out)[r * D + lane * kPer + t] = o[t] * f;
+  } else if constexpr (kPer == 2) {
+    reinterpret_cast<unsigned*>(a.out)[r * (D / 2) + lane] = pack_bf16(o[0] * f, o[1] * f);
+  } else {
+    reinterpret_cast<uint16_t*>(a.out)[r * D + lane] = static_cast<uint16_t>(pack_bf16(o[0] * f, 0.f));
+  }
+}
+
+}  // namespace
+}  // namespace wf
