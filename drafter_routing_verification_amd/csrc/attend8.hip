@@ -44,6 +44,11 @@ __device__ inline unsigned uppers(float lo, float hi) {
   return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
 
+// All bits, or none: bit i of x.
+__device__ inline unsigned all_of(unsigned x, int i) {
+  return static_cast<unsigned>(static_cast<int>(x << (31 - i)) >> 31);
+}
+
 template <int DT, int D>
 struct Ops8 {
   static constexpr int kD = D;
@@ -54,10 +59,6 @@ struct Ops8 {
   static constexpr int kQ = kParts * kFrags;
   static constexpr int kOut = D / 16;
   static constexpr int kBytes = DT == WF_BF16 ? 2 : 4;
-  static constexpr int kWords = D / 32;     // bfloat16 pairs of a lane's share of a row of V
-  struct V {
-    unsigned w[8][kWords];                  // [position][dimension pairs]
-  };
   // A lane's share of a tile as it lies in memory.
   struct Raw {
     u32x4 k[2][D / 64];
@@ -100,30 +101,31 @@ struct Ops8 {
       k[f] = u32x4{widen<false>(lo, scale), widen<true>(lo, scale), widen<false>(hi, scale), widen<true>(hi, scale)};
     }
   }
-  // The values, under the scales of the positions (bytes of scale[t]: those of 4 g + i).
-  __device__ static inline void values(V& v, const Raw& raw, const unsigned* scale) {
+  // The scale of position r (4 t + i) out of the bytes of sub-tile t's.
+  __device__ static inline float value_scale(const unsigned* bytes, int r) {
+    const unsigned w = bytes[r / 4];
+    const int up = 23 - 8 * (r % 4);
+    return __uint_as_float((up >= 0 ? w << (up >= 0 ? up : 0) : w >> 1) & 0x7f800000u);
+  }
+  // Takes the values of positions without their bit out: 0 under a scale of 1.  any: a lane's
+  // positions 4 g + i of sub-tile t at bit 16 t + i.
+  __device__ static inline void hide(Raw& raw, unsigned* bytes, unsigned any) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const float s = __uint_as_float((r % 4 < 3 ? scale[r / 4] << (23 - 8 * (r % 4) < 0 ? 0 : 23 - 8 * (r % 4))
-                                                 : scale[r / 4] >> 1) & 0x7f800000u);
+      const unsigned in = all_of(any, 16 * (r / 4) + r % 4);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        v.w[r][2 * c] = widen<false>(raw.v[r][c], s);
-        v.w[r][2 * c + 1] = widen<true>(raw.v[r][c], s);
-      }
+      for (int c = 0; c < D / 64; ++c) raw.v[r][c] &= in;
+      const unsigned place = 0xffu << (8 * (r % 4));
+      bytes[r / 4] = (bytes[r / 4] & (in | ~place)) | (127u << (8 * (r % 4)) & ~in);
     }
-  }
-  __device__ static inline void zero_v(V& v, int t, int i) {
-#pragma unroll
-    for (int x = 0; x < kWords; ++x) v.w[4 * t + i][x] = 0;
   }
 
   // o += V^T P^T for MT query tiles.  bfloat16: the weights rounded as the matrix units take them
   // (a part in 2^8 each), and summed as rounded, so that equal values come out as they are.
   // float32: in three parts, exactly.
   template <int MT>
-  __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4* sum, const V& v,
-                                        const float (*p)[kSub][4]) {
+  __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4* sum, const Raw& raw,
+                                        const unsigned* bytes, const float (*p)[kSub][4]) {
     bf16x8 pb[MT][kParts];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -148,37 +150,55 @@ struct Ops8 {
       for (int m = 0; m < MT; ++m)
         sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pb[m][0], sum[m], 0, 0, 0);
     }
+    float scale[8];
 #pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      // Element j of each position's dimensions, two positions a word.
-      unsigned w[4];
+    for (int r = 0; r < 8; ++r) scale[r] = value_scale(bytes, r);
+    // The values are widened two dimensions at a time, so that few of them need registers.
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        w[x] = __builtin_amdgcn_perm(v.w[2 * x + 1][j >> 1], v.w[2 * x][j >> 1],
-                                     (j & 1) ? 0x07060302u : 0x05040100u);
-      const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+    for (int c = 0; c < kOut / 2; ++c) {
+      unsigned v[8];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int r = 0; r < 8; ++r)
+        v[r] = c % 2 ? widen<true>(raw.v[r][c / 2], scale[r]) : widen<false>(raw.v[r][c / 2], scale[r]);
 #pragma unroll
-        for (int part = kParts - 1; part >= 0; --part)
-          o[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[m][part], o[m][j], 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        // Dimension 2 c + h of each position, two positions a word.
+        unsigned w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          w[x] = __builtin_amdgcn_perm(v[2 * x + 1], v[2 * x], h ? 0x07060302u : 0x05040100u);
+        const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int part = kParts - 1; part >= 0; --part)
+            o[m][2 * c + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[m][part], o[m][2 * c + h], 0, 0, 0);
+      }
     }
   }
 
-  __device__ static inline bool odd(const V& v) {
-    bool x = false;
+  // Whether the lane's values hold NaN (0x7f but for the sign).
+  __device__ static inline bool odd(const Raw& raw) {
+    unsigned x = 0;
 #pragma unroll
     for (int r = 0; r < 8; ++r)
 #pragma unroll
-      for (int c = 0; c < kWords; ++c)
-        x = x || (v.w[r][c] & 0x7f80u) == 0x7f80u || (v.w[r][c] & 0x7f800000u) == 0x7f800000u;
-    return x;
+      for (int c = 0; c < D / 64; ++c) x |= (raw.v[r][c] & 0x7f7f7f7fu) + 0x01010101u;
+    return (x & 0x80808080u) != 0;
   }
-  // NaN among the values that not every query sees go apart from the product, where they would
-  // meet the weights of zero of those queries too: they make NaN of the outputs that see them,
-  // and zeros take their place.
+  // Zeros in the place of NaN.
+  __device__ static inline void clean(Raw& raw) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const unsigned is = ((raw.v[r][c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        raw.v[r][c] &= ~(is | (is - (is >> 7)));  // (0x80 and 0x7f of every such byte)
+      }
+  }
+  // Makes NaN of the outputs that see one among the values.
   template <int MT>
-  __device__ static inline void poison(f32x4 (*o)[kOut], V& v, const unsigned* see) {
+  __device__ static inline void poison(f32x4 (*o)[kOut], const Raw& raw, const unsigned* see) {
     const int g = (threadIdx.x & 63) >> 4;
     bf16x8 pb[MT];
 #pragma unroll
@@ -191,13 +211,11 @@ struct Ops8 {
     }
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
-      unsigned w[4];
+      const unsigned mask = 0x7fu << (8 * (j % 4));
+      unsigned w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const unsigned mask = (j & 1) ? 0x7f800000u : 0x7f80u;
-        w[x] = (v.w[2 * x][j >> 1] & mask) == mask ? 0x3f80u : 0u;
-        w[x] |= (v.w[2 * x + 1][j >> 1] & mask) == mask ? 0x3f800000u : 0u;
-      }
+      for (int r = 0; r < 8; ++r)
+        w[r / 2] |= (raw.v[r][j / 4] & mask) == mask ? 0x3f80u << (r % 2 * 16) : 0u;
       const bf16x8 a = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -206,15 +224,8 @@ struct Ops8 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][j][i] += n[i] > 0.f ? NAN : 0.f;
       }
+      __builtin_amdgcn_sched_barrier(0);  // (one at a time: their results would all need registers)
     }
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-#pragma unroll
-      for (int c = 0; c < kWords; ++c) {
-        const unsigned x = v.w[r][c];
-        v.w[r][c] = ((x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu) |
-                    ((x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u);
-      }
   }
 
   // Element i of every output tile of one query (dimensions (4 g + i) D / 16 and on), times f.
@@ -234,6 +245,68 @@ struct Ops8 {
     store_partial<WF_BF16, D>(out, o, g);
   }
 };
+
+// Products to weights 2^(scale q . k - m).  The reference m of a query is a maximum of its row that
+// is raised only when a product exceeds it by more than kSlack8: bfloat16 and float32 hold weights
+// up to 2^16 and their sums as well as those up to 1, and so most tiles need no maximum over the
+// lanes and no rescaling.
+constexpr float kSlack8 = 16.f;
+
+template <class X, int MT>
+__device__ inline void soften8(Queries<X, MT>& Q, typename Queries<X, MT>::Weights& p, float scale) {
+  bool grown = false;
+  float top[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float x = p[m][0][0];
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x = fmaxf(x, p[m][t][i]);
+    top[m] = x * scale;
+    grown = grown || top[m] > Q.mx[m] + kSlack8;
+  }
+  if (__any(grown)) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float now = fmaxf(Q.mx[m], rows_max(top[m]));
+      const float f = __builtin_amdgcn_exp2f(Q.mx[m] - now);
+      Q.mx[m] = now;
+      Q.sum[m] *= f;
+#pragma unroll
+      for (int j = 0; j < X::kOut; ++j) Q.o[m][j] *= f;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < X::kSub; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[m][t][i] = __builtin_amdgcn_exp2f(fmaf(p[m][t][i], scale, -Q.mx[m]));
+        if constexpr (!X::kSums) Q.sum[m][0] += p[m][t][i];
+      }
+}
+
+// Of the 32 positions from j0 on, of which `any` can be seen at all, those that the lane's query of
+// tile m sees.
+template <class X, int MT>
+__device__ inline unsigned seen_of(const Queries<X, MT>& Q, int m, int j0, unsigned any,
+                                   const AttendArgs& a, const SeqCall& call, const int16_t* par) {
+  const int old = min(max(call.c - j0, 0), 32);
+  unsigned bits = old >= 32 ? ~0u : (1u << old) - 1u;
+  const int x0 = Q.query(a, call, m);
+  const int own = x0 < 0 ? -1 : x0 / a.group, last = call.c + own - j0;
+  if (!call.q.tree) {
+    if (own >= 0 && last >= 0) bits = last >= 31 ? ~0u : (2u << last) - 1u;
+  } else {
+    for (int u = own; u >= 0 && call.c + u >= j0; u = u == 0 ? -1 : par[u]) {
+      const int x = call.c + u - j0;
+      if (x < 32) bits |= 1u << x;
+    }
+  }
+  return bits & any;
+}
 
 struct Unit {
   int split, b, kvh, mg;
@@ -256,36 +329,54 @@ __device__ inline Unit unit_of(const AttendArgs& a) {
   return x;
 }
 
-template <int DT, int D, int MT, int PER_SIMD>
-__global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args a) {
+// GS query groups a workgroup: its waves take a group each and 4 / GS shares of the piece.  The waves
+// of a share read the same keys and values, from memory once and else from the CU's cache.
+template <int DT, int D, int MT, int GS>
+__global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
   using X = Ops8<DT, D>;
+  constexpr int kShares = kWaves / GS;
   __shared__ int16_t par_s[kMaxSeqRows];
   __shared__ struct {
-    f32x4 o[kWaves / 2][MT * X::kOut][64];
-    float2 ml[kWaves / 2][MT][64];
+    f32x4 o[kShares > 1 ? kWaves / 2 : 1][MT * X::kOut][64];
+    float2 ml[kShares > 1 ? kWaves / 2 : 1][MT][64];
   } join_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = lane & 15, g = lane >> 4;
   const Unit x = unit_of(a);
   if (!x.ok) return;
   const SeqCall call = seq_call(a, x.b);
-  const int rows = call.q.n, first = x.mg * MT * 16;
-  if (first >= rows * a.group) return;
-  const Sight sight = sight_of(a, call, first, MT * 16);
+  const int rows = call.q.n;
+  const int all_first = x.mg * GS * MT * 16;
+  if (all_first >= rows * a.group) return;
   const int k0 = x.split * a.span;
-  if (x.split > 0 && k0 >= sight.end) return;
-  const int k1 = min(k0 + a.span, sight.end);
+  const Sight all = sight_of(a, call, all_first, GS * MT * 16);
+  if (x.split > 0 && k0 >= all.end) return;
+  const int first = all_first + wave % GS * MT * 16;
+  const bool work = first < rows * a.group;
+  const Sight sight = sight_of(a, call, work ? first : all_first, MT * 16);
+  const int k1 = work ? min(k0 + a.span, sight.end) : k0;
   // The wave's positions [w0, w1), in whole tiles of the piece.
-  const int share = (a.span / kTile + kWaves - 1) / kWaves * kTile;
-  const int w0 = min(k0 + wave * share, k1), w1 = min(w0 + share, k1);
+  const int share = (a.span / kTile + kShares - 1) / kShares * kTile;
+  const int w0 = min(k0 + wave / GS * share, k1), w1 = min(w0 + share, k1);
   PageWalk walk(a, call, w0, w1);
-  if (call.q.tree && k1 > call.c && call.c >= 0) {
+  if (call.q.tree && k0 + a.span > call.c && call.c >= 0) {
     for (int u = 1 + tid; u < rows; u += kThreads)
       par_s[u] = static_cast<int16_t>(node_parent(a.rows, x.b, true, u));
     __syncthreads();
   }
+  // Three tiles of queries do not fit the registers beside their outputs: they stay in LDS.
+  constexpr bool kInLds = MT * X::kQ > 8;
+  __shared__ u32x4 q_s[kInLds ? GS : 1][kInLds ? MT * X::kQ : 1][64];
   Queries<X, MT> Q;
   Q.load(a, call, x.kvh, first);
+  if constexpr (kInLds) {
+    if (wave < GS)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int f = 0; f < X::kQ; ++f) q_s[wave][m * X::kQ + f][lane] = Q.q[m][f];
+    __syncthreads();
+  }
 
   const int64_t head_bytes = static_cast<int64_t>(x.kvh) * D << a.page_log;
   const int64_t head_scale = static_cast<int64_t>(x.kvh) << (a.page_log - a.block_log);
@@ -293,7 +384,7 @@ __global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args
   const unsigned k_lane = n * D + 16 * g, v_lane = 4 * g * D + n * (D / 16);
   const unsigned char* scales = lane < 32 ? a.k_scale : a.v_scale;
   typename X::Raw raw;
-  int id[2];
+  int id[2] = {-1, -1};
   // Places the tile from j on; its bits that have a page.
   auto place = [&](int j) {
     walk.reach(j, kTile);
@@ -305,6 +396,11 @@ __global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args
     }
     return pages;
   };
+  // Loads that stay in the caches only where another wave wants them too.
+  auto fetch = [&](auto* p) {
+    if constexpr (GS > 1) return *p;
+    return __builtin_nontemporal_load(p);
+  };
   auto load_k = [&](int j) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -312,9 +408,10 @@ __global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args
                                static_cast<int64_t>((j + 16 * t) & in_page) * D;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
-        raw.k[t][i] = load16(reinterpret_cast<const u32x4*>(p + k_lane + 64 * i));
+        raw.k[t][i] = fetch(reinterpret_cast<const u32x4*>(p + k_lane + 64 * i));
     }
-    const int mine = lane & 16 ? id[1] : id[0];
+    // (A choice between the elements of an array would put it into memory.)
+    const int mine = id[0] ^ ((id[0] ^ id[1]) & static_cast<int>(all_of(lane, 4)));
     raw.scale = scales[max(mine, 0) * a.scale_page + head_scale + (((j + (lane & 31)) & in_page) >> a.block_log)];
   };
   auto load_v = [&](int j) {
@@ -326,25 +423,13 @@ __global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args
       for (int i = 0; i < 4; ++i) {
         if constexpr (D == 128) {
           typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-          const u32x2 y = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + v_lane + i * D));
+          const u32x2 y = fetch(reinterpret_cast<const u32x2*>(p + v_lane + i * D));
           raw.v[4 * t + i][0] = y.x;
           raw.v[4 * t + i][1] = y.y;
         } else {
-          raw.v[4 * t + i][0] = __builtin_nontemporal_load(reinterpret_cast<const unsigned*>(p + v_lane + i * D));
+          raw.v[4 * t + i][0] = fetch(reinterpret_cast<const unsigned*>(p + v_lane + i * D));
         }
       }
-    }
-  };
-  // Scales to the lanes that use them: keys' of position n, values' of positions 4 g + i (a byte each).
-  auto spread = [&](float* ks, unsigned* vs) {
-    const unsigned byte = raw.scale;
-    unsigned four = byte << (8 * (lane & 3));
-    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor1>(static_cast<int>(four)));
-    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor2>(static_cast<int>(four)));
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      ks[t] = __uint_as_float(static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (16 * t + n), static_cast<int>(byte << 23))));
-      vs[t] = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (32 + 16 * t + 4 * g), static_cast<int>(four)));
     }
   };
   unsigned pages = 0;
@@ -354,66 +439,122 @@ __global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args
     load_v(w0);
   }
   using Weights = typename Queries<X, MT>::Weights;
-  // The products of the tile at hand with the queries; its values; the loads of the next tile.
-  auto take = [&](Weights& p, typename X::V& v, int next) {
+  // The products of the tile's keys with the queries, the scales of its values (a byte for each of
+  // the positions 4 g + i), and the loads of the next tile's keys; the bits that have a page.
+  auto scores = [&](Weights& p, unsigned* vs, int next) {
+    const unsigned byte = raw.scale;
+    unsigned four = byte << (8 * (lane & 3));
+    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor1>(static_cast<int>(four)));
+    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor2>(static_cast<int>(four)));
     float ks[2];
-    unsigned vs[2];
-    spread(ks, vs);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      u32x4 k[X::kFrags];
-      X::keys(k, raw, t, ks[t]);
-      Q.score(p, t, k);
+      ks[t] = __uint_as_float(static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (16 * t + n), static_cast<int>(byte << 23))));
+      vs[t] = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (32 + 16 * t + 4 * g), static_cast<int>(four)));
     }
-    X::values(v, raw, vs);
+    if constexpr (kInLds) {
+      u32x4 k[2][X::kFrags];
+      X::keys(k[0], raw, 0, ks[0]);
+      X::keys(k[1], raw, 1, ks[1]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 sum[2] = {};
+#pragma unroll
+        for (int f = X::kQ - 1; f >= 0; --f) {
+          const u32x4 q = q_s[wave % GS][m * X::kQ + f][lane];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[t][f % X::kFrags]),
+                                                             __builtin_bit_cast(bf16x8, q), sum[t], 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[m][t][i] = sum[t][i];
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        u32x4 k[X::kFrags];
+        X::keys(k, raw, t, ks[t]);
+        Q.score(p, t, k);
+      }
+    }
     const unsigned here = pages;
     if (next < w1) {
       pages = place(next);
       load_k(next);
-      load_v(next);
     }
     return here;
   };
-  // Tiles that every query sees, then those that some do not.
-  int j0 = w0;
-  for (; j0 + kTile <= min(sight.all, w1); j0 += kTile) {
-    Weights p;
-    typename X::V v;
-    const unsigned here = take(p, v, j0 + kTile);
-    if (here != ~0u) Q.hide(p, v, here);
-    Q.soften(p, a.scale_log2);
-    X::template outputs<MT>(Q.o, Q.sum, v, p);
-  }
+  int odd_from = -1;  // the first tile with NaN that were taken out
 #pragma unroll 1
-  for (; j0 < w1; j0 += kTile) {
+  for (int j0 = w0; j0 < w1; j0 += kTile) {
     Weights p;
-    typename X::V v;
-    const unsigned any = Q.visible(j0, sight.end, take(p, v, j0 + kTile));
-    Q.hide(p, v, any);
-    unsigned see[MT];
-    Q.mask(p, see, j0, any, a, call, par_s);
-    Q.soften(p, a.scale_log2);
-    if (__any(X::odd(v))) X::template poison<MT>(Q.o, v, see);
-    X::template outputs<MT>(Q.o, Q.sum, v, p);
+    unsigned vs[2];
+    const unsigned here = scores(p, vs, j0 + kTile);
+    if (here != ~0u || j0 + kTile > min(sight.all, w1)) {
+      // Some query does not see all of the tile.
+      const unsigned any = Q.visible(j0, sight.end, here);
+      X::hide(raw, vs, any >> (4 * g));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const unsigned see = seen_of(Q, m, j0, any, a, call, par_s) >> (4 * g);
+        __builtin_amdgcn_sched_barrier(0);
+        // (By masks of bits: comparisons would take two scalar registers for each product.)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const unsigned in = all_of(see, 16 * (r / 4) + r % 4);
+          float& x = p[m][r / 4][r % 4];
+          x = __uint_as_float((__float_as_uint(x) & in) | (0xff800000u & ~in));
+        }
+      }
+      // NaN among values that not every query sees would meet weights of zero: they go apart.
+      if (__any(X::odd(raw))) {
+        if (odd_from < 0) odd_from = j0;
+        X::clean(raw);
+      }
+    }
+    soften8<X, MT>(Q, p, a.scale_log2);
+    X::template outputs<MT>(Q.o, Q.sum, raw, vs, p);
+    if (j0 + kTile < w1) load_v(j0 + kTile);
+  }
+  if (odd_from >= 0) {
+    // Once more over the tiles that some query does not see, for their NaN.
+    walk.fetch(odd_from);
+#pragma unroll 1
+    for (int j0 = odd_from; j0 < w1; j0 += kTile) {
+      const unsigned here = place(j0);
+      if (here == ~0u && j0 + kTile <= min(sight.all, w1)) continue;
+      const unsigned any = Q.visible(j0, sight.end, here);
+      unsigned see[MT], none[2] = {0u, 0u};
+      load_v(j0);
+      X::hide(raw, none, any >> (4 * g));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) see[m] = seen_of(Q, m, j0, any, a, call, par_s);
+      X::template poison<MT>(Q.o, raw, see);
+    }
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
 
-  // The waves join, halves at a time.
+  // The shares of a group join, halves at a time.
+  const int mine = wave / GS;
 #pragma unroll
-  for (int half = kWaves / 2; half > 0; half /= 2) {
+  for (int half = kShares / 2; half > 0; half /= 2) {
     __syncthreads();
-    if (wave >= half && wave < 2 * half) {
+    if (mine >= half && mine < 2 * half) {
+      const int to = wave - half * GS;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        join_s.ml[wave - half][m][lane] = make_float2(Q.mx[m], Q.sum[m][0]);
+        join_s.ml[to][m][lane] = make_float2(Q.mx[m], Q.sum[m][0]);
 #pragma unroll
-        for (int j = 0; j < X::kOut; ++j) join_s.o[wave - half][m * X::kOut + j][lane] = Q.o[m][j];
+        for (int j = 0; j < X::kOut; ++j) join_s.o[to][m * X::kOut + j][lane] = Q.o[m][j];
       }
     }
     __syncthreads();
-    if (wave < half) {
+    if (mine < half) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const float2 y = join_s.ml[wave][m][lane];
@@ -428,31 +569,35 @@ __global__ __launch_bounds__(kThreads, PER_SIMD) void attend8_kernel(Attend8Args
       }
     }
   }
-  if (wave == 0) Q.store(a, call, x.kvh, x.split);
+  if (mine == 0 && work) Q.store(a, call, x.kvh, x.split);
 }
 
-// Query tiles of a workgroup, and workgroups of a CU.
+// Query tiles of a wave, and query groups of a workgroup.
 struct Shape {
-  int mt, per_cu;
+  int mt, gs;
 };
 
 Shape shape_of(int tiles, int dtype) {
-  if (dtype == WF_F32) return tiles <= 1 ? Shape{1, 2} : Shape{2, 1};
-  if (tiles <= 1) return Shape{1, 2};
-  if (tiles <= 2) return Shape{2, 2};
-  return Shape{3, 1};
+  const int mt = dtype == WF_F32 ? 1 : tiles <= 1 ? 1 : tiles <= 2 ? 2 : 3;
+  const int groups = (tiles + mt - 1) / mt;
+  return Shape{mt, groups > 2 ? 4 : groups > 1 ? 2 : 1};
+}
+
+template <int DT, int D, int MT>
+void launch_groups(const Attend8Args& a, int gs, int64_t blocks, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+  if (gs == 1) go(attend8_kernel<DT, D, MT, 1>);
+  if (gs == 2) go(attend8_kernel<DT, D, MT, 2>);
+  if (gs == 4) go(attend8_kernel<DT, D, MT, 4>);
 }
 
 template <int DT, int D>
 void launch_typed(const Attend8Args& a, Shape s, int64_t blocks, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-  if constexpr (DT == WF_F32) {
-    s.mt == 1 ? go(attend8_kernel<DT, D, 1, 2>) : go(attend8_kernel<DT, D, 2, 1>);
-  } else {
-    if (s.mt == 1) go(attend8_kernel<DT, D, 1, 2>);
-    if (s.mt == 2) go(attend8_kernel<DT, D, 2, 2>);
-    if (s.mt == 3) go(attend8_kernel<DT, D, 3, 1>);
+  if (s.mt == 1) launch_groups<DT, D, 1>(a, s.gs, blocks, stream);
+  if constexpr (DT == WF_BF16) {
+    if (s.mt == 2) launch_groups<DT, D, 2>(a, s.gs, blocks, stream);
+    if (s.mt == 3) launch_groups<DT, D, 3>(a, s.gs, blocks, stream);
   }
 }
 
@@ -463,7 +608,7 @@ void launch_join(const AttendArgs& a, hipStream_t stream) {
                      dim3(kThreads), 0, stream, a);
 }
 
-// How a call is cut: `splits` pieces of `span` positions a sequence, `groups` query groups a head.
+// How a call is cut: `splits` pieces of `span` positions a sequence, `groups` workgroups a piece and head.
 struct Plan8 {
   Shape shape;
   int groups, splits, span;
@@ -475,12 +620,13 @@ Plan8 plan_of(const wf_page_cache8& cache, const RowsArgs& rows, int dtype, int3
   Plan8 p;
   const int tiles = static_cast<int>((static_cast<int64_t>(rows.rmax) * (q_heads / c.heads) + 15) / 16);
   p.shape = shape_of(tiles, dtype);
-  p.groups = (tiles + p.shape.mt - 1) / p.shape.mt;
+  const int each = p.shape.mt * p.shape.gs;
+  p.groups = (tiles + each - 1) / each;
   int64_t most = static_cast<int64_t>(max_context) + rows.rmax;
   const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_size;
   most = most < room ? most : room;
   const int64_t one = static_cast<int64_t>(rows.B) * c.heads * p.groups;
-  const int64_t slots = 256 * p.shape.per_cu;
+  const int64_t slots = 512;
   int64_t best = INT64_MAX, splits = 1;
   for (int64_t rounds = 1; rounds <= 8; ++rounds) {
     int64_t s = rounds * slots / one;
@@ -488,7 +634,7 @@ Plan8 plan_of(const wf_page_cache8& cache, const RowsArgs& rows, int dtype, int3
     s = s > cap ? cap : s;
     s = s < 1 ? 1 : s;
     const int64_t need = (one * s + slots - 1) / slots;
-    const int64_t cost = need * (most / s + 256 + (s > 1 ? 32 * p.shape.mt : 0));
+    const int64_t cost = need * (most / s + 256 + (s > 1 ? 32 * each : 0));
     if (cost < best) {
       best = cost;
       splits = s;

@@ -516,7 +516,8 @@ struct Queries {
 
   // Takes positions that no query sees out of a tile's scores and values: whatever lies
   // there must not meet a weight of zero, it may be NaN.
-  __device__ static inline void hide(Weights& p, typename X::V& v, unsigned any) {
+  template <class V>
+  __device__ static inline void hide(Weights& p, V& v, unsigned any) {
     const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int t = 0; t < X::kSub; ++t)
