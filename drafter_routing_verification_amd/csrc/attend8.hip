@@ -59,11 +59,11 @@ struct Ops8 {
   static constexpr int kQ = kParts * kFrags;
   static constexpr int kOut = D / 16;
   static constexpr int kBytes = DT == WF_BF16 ? 2 : 4;
-  // A lane's share of a tile as it lies in memory.
+  // A lane's share of 32 positions as they lie in memory: of sub-tile t, bytes [64 i + 16 g, + 16)
+  // of key n, and D / 16 dimensions from n D / 16 on of the values 4 g + i.
   struct Raw {
     u32x4 k[2][D / 64];
     unsigned v[8][D / 64];
-    unsigned scale;                         // lanes 0 - 31: the keys' byte of a position, then the values'
   };
 
   // Fragment f: dimensions 64 (f / 2) + 16 g + 8 (f % 2) and the seven behind it.
@@ -101,22 +101,15 @@ struct Ops8 {
       k[f] = u32x4{widen<false>(lo, scale), widen<true>(lo, scale), widen<false>(hi, scale), widen<true>(hi, scale)};
     }
   }
-  // The scale of position r (4 t + i) out of the bytes of sub-tile t's.
-  __device__ static inline float value_scale(const unsigned* bytes, int r) {
-    const unsigned w = bytes[r / 4];
-    const int up = 23 - 8 * (r % 4);
-    return __uint_as_float((up >= 0 ? w << (up >= 0 ? up : 0) : w >> 1) & 0x7f800000u);
-  }
   // Takes the values of positions without their bit out: 0 under a scale of 1.  any: a lane's
   // positions 4 g + i of sub-tile t at bit 16 t + i.
-  __device__ static inline void hide(Raw& raw, unsigned* bytes, unsigned any) {
+  __device__ static inline void hide(Raw& raw, float* scale, unsigned any) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const unsigned in = all_of(any, 16 * (r / 4) + r % 4);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) raw.v[r][c] &= in;
-      const unsigned place = 0xffu << (8 * (r % 4));
-      bytes[r / 4] = (bytes[r / 4] & (in | ~place)) | (127u << (8 * (r % 4)) & ~in);
+      scale[r] = __uint_as_float((__float_as_uint(scale[r]) & in) | (0x3f800000u & ~in));
     }
   }
 
@@ -125,7 +118,7 @@ struct Ops8 {
   // float32: in three parts, exactly.
   template <int MT>
   __device__ static inline void outputs(f32x4 (*o)[kOut], f32x4* sum, const Raw& raw,
-                                        const unsigned* bytes, const float (*p)[kSub][4]) {
+                                        const float* scale, const float (*p)[kSub][4]) {
     bf16x8 pb[MT][kParts];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -150,9 +143,6 @@ struct Ops8 {
       for (int m = 0; m < MT; ++m)
         sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pb[m][0], sum[m], 0, 0, 0);
     }
-    float scale[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) scale[r] = value_scale(bytes, r);
     // The values are widened two dimensions at a time, so that few of them need registers.
 #pragma unroll
     for (int c = 0; c < kOut / 2; ++c) {
@@ -264,7 +254,7 @@ __device__ inline void soften8(Queries<X, MT>& Q, typename Queries<X, MT>::Weigh
 #pragma unroll
       for (int i = 0; i < 4; ++i) x = fmaxf(x, p[m][t][i]);
     top[m] = x * scale;
-    grown = grown || top[m] > Q.mx[m] + kSlack8;
+    grown = grown | (top[m] > Q.mx[m] + kSlack8);
   }
   if (__any(grown)) {
 #pragma unroll
@@ -329,44 +319,300 @@ __device__ inline Unit unit_of(const AttendArgs& a) {
   return x;
 }
 
-// GS query groups a workgroup: its waves take a group each and 4 / GS shares of the piece.  The waves
-// of a share read the same keys and values, from memory once and else from the CU's cache.
-template <int DT, int D, int MT, int GS>
+// What a wave needs to know of its call besides its queries.
+struct Walk8 {
+  int64_t head_bytes, head_scale;
+  int in_page, block_log;
+
+  __device__ inline Walk8(const Attend8Args& a, int kvh, int d)
+      : head_bytes(static_cast<int64_t>(kvh) * d << a.page_log),
+        head_scale(static_cast<int64_t>(kvh) << (a.page_log - a.block_log)),
+        in_page((1 << a.page_log) - 1), block_log(a.block_log) {}
+  // Offsets of position j of page id (-1: page 0, whose values are not used).
+  __device__ inline int64_t at(const Attend8Args& a, int id, int j, int d) const {
+    return max(id, 0) * a.page_bytes + head_bytes + static_cast<int64_t>(j & in_page) * d;
+  }
+  __device__ inline int64_t scale_at(const Attend8Args& a, int id, int j) const {
+    return max(id, 0) * a.scale_page + head_scale + ((j & in_page) >> block_log);
+  }
+};
+
+// The weights and outputs of 32 positions from their products with the queries.  here: those with a
+// page.  Returns whether NaN among the values were taken out.
+template <class X, int MT>
+__device__ inline bool use_tile(Queries<X, MT>& Q, typename Queries<X, MT>::Weights& p,
+                                typename X::Raw& raw, float* scale, int j0, unsigned here,
+                                const Sight& sight, const Attend8Args& a, const SeqCall& call,
+                                const int16_t* par) {
+  const int g = (threadIdx.x & 63) >> 4;
+  bool odd = false;
+  if (here != ~0u || j0 + kTile > sight.all) {
+    // Some query does not see all of the tile.
+    const unsigned any = Q.visible(j0, sight.end, here);
+    X::hide(raw, scale, any >> (4 * g));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const unsigned see = seen_of(Q, m, j0, any, a, call, par) >> (4 * g);
+      __builtin_amdgcn_sched_barrier(0);
+      // (By masks of bits: comparisons would take two scalar registers for each product.)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const unsigned in = all_of(see, 16 * (r / 4) + r % 4);
+        float& x = p[m][r / 4][r % 4];
+        x = __uint_as_float((__float_as_uint(x) & in) | (0xff800000u & ~in));
+      }
+    }
+    // NaN among values that not every query sees would meet weights of zero: they go apart.
+    odd = __any(X::odd(raw));
+    if (odd) X::clean(raw);
+  }
+  soften8<X, MT>(Q, p, a.scale_log2);
+  // The wave that feeds the matrix units goes first, so that the SIMD's other one is left with the
+  // vector work: 8 trees of 61 76 -> 70 us, long chains 144 -> 140.
+  __builtin_amdgcn_s_setprio(1);
+  X::template outputs<MT>(Q.o, Q.sum, raw, scale, p);
+  __builtin_amdgcn_s_setprio(0);
+  return odd;
+}
+
+// The values of 32 positions from memory.
+template <class X, bool STREAM>
+__device__ inline void load_values(typename X::Raw& raw, const Attend8Args& a, const Walk8& w,
+                                   const int* id, int j, unsigned v_lane) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const unsigned char* p = a.v + w.at(a, id[t], j + 16 * t, X::kD) + v_lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (X::kD == 128) {
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2* from = reinterpret_cast<const u32x2*>(p + i * X::kD);
+        const u32x2 y = STREAM ? __builtin_nontemporal_load(from) : *from;
+        raw.v[4 * t + i][0] = y.x;
+        raw.v[4 * t + i][1] = y.y;
+      } else {
+        const unsigned* from = reinterpret_cast<const unsigned*>(p + i * X::kD);
+        raw.v[4 * t + i][0] = STREAM ? __builtin_nontemporal_load(from) : *from;
+      }
+    }
+  }
+}
+
+// Once more over the positions [from, to) that some query does not see, for the NaN among their values.
+template <class X, int MT>
+__device__ inline void poison_from(Queries<X, MT>& Q, typename X::Raw& raw, PageWalk& walk, int from,
+                                   int to, const Sight& sight, const Attend8Args& a, const Walk8& w,
+                                   const SeqCall& call, const int16_t* par, unsigned v_lane) {
+  const int g = (threadIdx.x & 63) >> 4;
+  walk.fetch(from);
+#pragma unroll 1
+  for (int j0 = from; j0 < to; j0 += kTile) {
+    walk.reach(j0, kTile);
+    const int id[2] = {walk.at(j0), walk.at(j0 + 16)};
+    const unsigned any = Q.visible(j0, sight.end, (id[0] >= 0 ? 0xffffu : 0u) | (id[1] >= 0 ? 0xffff0000u : 0u));
+    unsigned see[MT];
+    float none[8];
+    load_values<X, false>(raw, a, w, id, j0, v_lane);
+    X::hide(raw, none, any >> (4 * g));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) see[m] = seen_of(Q, m, j0, any, a, call, par);
+    X::template poison<MT>(Q.o, raw, see);
+  }
+}
+
+// What the shares of a query group leave for each other at the end, of one query tile.
+template <class X, int SLOTS>
+struct Joins {
+  f32x4 o[SLOTS][X::kOut][64];
+  float2 ml[SLOTS][64];
+};
+
+// Joins the waves that hold the same queries (wave = share * GS + group), halves at a time, into
+// those of share 0.
+template <int GS, class X, int MT, int SLOTS>
+__device__ inline void join_shares(Queries<X, MT>& Q, Joins<X, SLOTS>& join_s) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, mine = wave / GS;
+#pragma unroll
+  for (int half = kWaves / GS / 2; half > 0; half /= 2)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      __syncthreads();
+      if (mine >= half && mine < 2 * half) {
+        const int to = wave - half * GS;
+        join_s.ml[to][lane] = make_float2(Q.mx[m], Q.sum[m][0]);
+#pragma unroll
+        for (int j = 0; j < X::kOut; ++j) join_s.o[to][j][lane] = Q.o[m][j];
+      }
+      __syncthreads();
+      if (mine < half) {
+        const float2 y = join_s.ml[wave][lane];
+        const float now = fmaxf(Q.mx[m], y.x);
+        const float fa = __builtin_amdgcn_exp2f(Q.mx[m] - now);
+        const float fb = __builtin_amdgcn_exp2f(y.x - now);
+        Q.mx[m] = now;
+        Q.sum[m][0] = Q.sum[m][0] * fa + y.y * fb;
+#pragma unroll
+        for (int j = 0; j < X::kOut; ++j) Q.o[m][j] = Q.o[m][j] * fa + join_s.o[wave][j][lane] * fb;
+      }
+    }
+}
+
+// Up to 16 MT queries a key-value head: each of the four waves takes a share of the piece, with all
+// queries.  Keys and values come straight from memory, the next tile's while this one is used.
+template <int DT, int D, int MT>
 __global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
   using X = Ops8<DT, D>;
-  constexpr int kShares = kWaves / GS;
   __shared__ int16_t par_s[kMaxSeqRows];
-  __shared__ struct {
-    f32x4 o[kShares > 1 ? kWaves / 2 : 1][MT * X::kOut][64];
-    float2 ml[kShares > 1 ? kWaves / 2 : 1][MT][64];
-  } join_s;
+  __shared__ Joins<X, kWaves / 2> join_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = lane & 15, g = lane >> 4;
   const Unit x = unit_of(a);
   if (!x.ok) return;
   const SeqCall call = seq_call(a, x.b);
-  const int rows = call.q.n;
-  const int all_first = x.mg * GS * MT * 16;
-  if (all_first >= rows * a.group) return;
+  const int rows = call.q.n, first = x.mg * MT * 16;
+  if (first >= rows * a.group) return;
+  const Sight sight = sight_of(a, call, first, MT * 16);
   const int k0 = x.split * a.span;
-  const Sight all = sight_of(a, call, all_first, GS * MT * 16);
-  if (x.split > 0 && k0 >= all.end) return;
-  const int first = all_first + wave % GS * MT * 16;
-  const bool work = first < rows * a.group;
-  const Sight sight = sight_of(a, call, work ? first : all_first, MT * 16);
-  const int k1 = work ? min(k0 + a.span, sight.end) : k0;
+  if (x.split > 0 && k0 >= sight.end) return;
+  const int k1 = min(k0 + a.span, sight.end);
   // The wave's positions [w0, w1), in whole tiles of the piece.
-  const int share = (a.span / kTile + kShares - 1) / kShares * kTile;
-  const int w0 = min(k0 + wave / GS * share, k1), w1 = min(w0 + share, k1);
+  const int share = (a.span / kTile + kWaves - 1) / kWaves * kTile;
+  const int w0 = min(k0 + wave * share, k1), w1 = min(w0 + share, k1);
   PageWalk walk(a, call, w0, w1);
-  if (call.q.tree && k0 + a.span > call.c && call.c >= 0) {
+  if (call.q.tree && k1 > call.c && call.c >= 0) {
     for (int u = 1 + tid; u < rows; u += kThreads)
       par_s[u] = static_cast<int16_t>(node_parent(a.rows, x.b, true, u));
     __syncthreads();
   }
+  Queries<X, MT> Q;
+  Q.load(a, call, x.kvh, first);
+
+  const Walk8 w(a, x.kvh, D);
+  const unsigned k_lane = n * D + 16 * g, v_lane = 4 * g * D + n * (D / 16);
+  const unsigned char* scales = lane < 32 ? a.k_scale : a.v_scale;
+  typename X::Raw raw;
+  unsigned byte = 0;  // lanes 0 - 31: the scale of a key, lanes 32 - 63: that of a value
+  int id[2] = {-1, -1};
+  // Places the tile from j on; its bits that have a page.
+  auto place = [&](int j) {
+    walk.reach(j, kTile);
+    id[0] = walk.at(j);
+    id[1] = walk.at(j + 16);
+    return (id[0] >= 0 ? 0xffffu : 0u) | (id[1] >= 0 ? 0xffff0000u : 0u);
+  };
+  auto load_keys = [&](int j) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const unsigned char* p = a.k + w.at(a, id[t], j + 16 * t, D) + k_lane;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) raw.k[t][i] = load16(reinterpret_cast<const u32x4*>(p + 64 * i));
+    }
+    // (A choice between the elements of an array would put it into memory.)
+    const int mine = id[0] ^ ((id[0] ^ id[1]) & static_cast<int>(all_of(lane, 4)));
+    byte = scales[w.scale_at(a, mine, j + (lane & 31))];
+  };
+  unsigned pages = 0;
+  if (w0 < w1) {
+    pages = place(w0);
+    load_keys(w0);
+    load_values<X, true>(raw, a, w, id, w0, v_lane);
+  }
+  int odd_from = -1;  // the first tile with NaN that were taken out
+#pragma unroll 1
+  for (int j0 = w0; j0 < w1; j0 += kTile) {
+    typename Queries<X, MT>::Weights p;
+    // Scales to the lanes that use them: those of key n, and of values 4 g + i (a byte each).
+    unsigned four = byte << (8 * (lane & 3));
+    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor1>(static_cast<int>(four)));
+    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor2>(static_cast<int>(four)));
+    float ks[2], vs[8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      ks[t] = __uint_as_float(static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (16 * t + n), static_cast<int>(byte << 23))));
+      const unsigned b = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (32 + 16 * t + 4 * g), static_cast<int>(four)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vs[4 * t + i] = scale_of(b >> (8 * i) & 0xffu);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      u32x4 k[X::kFrags];
+      X::keys(k, raw, t, ks[t]);
+      Q.score(p, t, k);
+    }
+    const unsigned here = pages;
+    const int next = j0 + kTile;
+    if (next < w1) {
+      pages = place(next);
+      load_keys(next);
+    }
+    if (use_tile<X, MT>(Q, p, raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
+    if (next < w1) load_values<X, true>(raw, a, w, id, next, v_lane);
+  }
+  if (odd_from >= 0) poison_from<X, MT>(Q, raw, walk, odd_from, w1, sight, a, w, call, par_s, v_lane);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
+  join_shares<1>(Q, join_s);
+  if (wave == 0) Q.store(a, call, x.kvh, x.split);
+}
+
+// A tile of 64 positions as it lies in memory, in LDS.  The pieces of 16 bytes of key n are exchanged
+// so that sixteen keys' pieces spread over the banks, values 4 g + i lie at row 4 i + g, so that a
+// wave reads them one after the other.  scale: a word each for 16 keys, 16 values.
+constexpr int kWide = 64;
+constexpr int kRing = 3;
+template <int D>
+struct Stage {
+  u32x4 k[kWide * D / 16], v[kWide * D / 16];
+  unsigned scale[kWide / 16][64];
+};
+
+// Loads straight into LDS: 16 bytes a lane from base + offset, or one byte a lane, zero-extended to a
+// word, from p; lane after lane from `to` on.  They have no registers to wait for: who reads the
+// LDS waits for the count of loads in flight himself.
+__device__ inline unsigned lds_address(const void* p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+__device__ inline void to_lds16(const void* to, const unsigned char* base, unsigned offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds_address(to)), "v"(offset), "s"(base) : "m0", "memory");
+}
+__device__ inline void to_lds1(const void* to, const unsigned char* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, off"
+               :: "s"(lds_address(to)), "v"(p) : "m0", "memory");
+}
+
+// More queries: GS groups of 16 MT share every tile, which all four waves fetch together, straight into
+// LDS and two tiles ahead; the waves take a group and one of 4 / GS shares of the tile each.
+template <int DT, int D, int MT, int GS>
+__global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a) {
+  using X = Ops8<DT, D>;
+  constexpr int kShares = kWaves / GS, kSteps = kWide / kTile / kShares;
+  constexpr int kRow = D / 16;              // 16-byte pieces of a row
+  constexpr int kLoads = D / 64;            // loads of 1 KB of a sub-tile's keys, or values
   // Three tiles of queries do not fit the registers beside their outputs: they stay in LDS.
-  constexpr bool kInLds = MT * X::kQ > 8;
+  constexpr bool kInLds = MT * X::kQ > 8 && X::kParts == 1;
+  __shared__ int16_t par_s[kMaxSeqRows];
   __shared__ u32x4 q_s[kInLds ? GS : 1][kInLds ? MT * X::kQ : 1][64];
+  __shared__ Stage<D> ring_s[kRing];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const Unit x = unit_of(a);
+  if (!x.ok) return;
+  const SeqCall call = seq_call(a, x.b);
+  const int rows = call.q.n, all_first = x.mg * GS * MT * 16;
+  if (all_first >= rows * a.group) return;
+  const Sight all = sight_of(a, call, all_first, GS * MT * 16);
+  const int k0 = x.split * a.span;
+  if (x.split > 0 && k0 >= all.end) return;
+  const int k1 = min(k0 + a.span, all.end);
+  const int first = all_first + wave % GS * MT * 16;
+  const bool work = first < rows * a.group;
+  const Sight sight = sight_of(a, call, work ? first : all_first, MT * 16);
+  PageWalk walk(a, call, k0, k1);
+  if (call.q.tree && k1 > call.c && call.c >= 0)
+    for (int u = 1 + tid; u < rows; u += kThreads)
+      par_s[u] = static_cast<int16_t>(node_parent(a.rows, x.b, true, u));
   Queries<X, MT> Q;
   Q.load(a, call, x.kvh, first);
   if constexpr (kInLds) {
@@ -375,201 +621,142 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int f = 0; f < X::kQ; ++f) q_s[wave][m * X::kQ + f][lane] = Q.q[m][f];
-    __syncthreads();
   }
+  __syncthreads();
 
-  const int64_t head_bytes = static_cast<int64_t>(x.kvh) * D << a.page_log;
-  const int64_t head_scale = static_cast<int64_t>(x.kvh) << (a.page_log - a.block_log);
-  const int in_page = (1 << a.page_log) - 1;
-  const unsigned k_lane = n * D + 16 * g, v_lane = 4 * g * D + n * (D / 16);
-  const unsigned char* scales = lane < 32 ? a.k_scale : a.v_scale;
-  typename X::Raw raw;
-  int id[2] = {-1, -1};
-  // Places the tile from j on; its bits that have a page.
-  auto place = [&](int j) {
-    walk.reach(j, kTile);
+  const Walk8 w(a, x.kvh, D);
+  // Where a lane's pieces of the wave's sub-tile come from: row and piece.
+  unsigned k_from[kLoads], v_from[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int q = i * (64 / kRow) + lane / kRow, slot = lane % kRow;  // row and slot in LDS
+    const int turn = D == 128 ? q & 7 : q >> 2 & 3;
+    k_from[i] = q * D + (slot ^ turn) * 16;
+    v_from[i] = (4 * (q & 3) + (q >> 2)) * D + slot * 16;
+  }
+  const int k_turn = D == 128 ? n & 7 : n >> 2 & 3;
+  const unsigned char* scales = lane & 16 ? a.v_scale : a.k_scale;
+  // Starts the loads of the tile from j on into the ring's place `to`, whatever the tile holds (the
+  // number of loads in flight is counted on); a bit for each sub-tile with a page.
+  auto issue = [&](int to, int j) __attribute__((always_inline)) {
+    walk.reach(j, kWide);
     unsigned pages = 0;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      id[t] = walk.at(j + 16 * t);
-      pages |= id[t] >= 0 ? 0xffffu << (16 * t) : 0u;
+    for (int t = 0; t < kWide / 16; ++t) pages |= walk.at(j + 16 * t) >= 0 ? 1u << t : 0u;
+    const int mine = j + 16 * wave, id = walk.at(mine);
+    const int64_t at = w.at(a, id, mine, D);
+    Stage<D>& st = ring_s[to];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      to_lds16(st.k + wave * 16 * kRow + i * 64, a.k + at, k_from[i]);
+      to_lds16(st.v + wave * 16 * kRow + i * 64, a.v + at, v_from[i]);
     }
+    to_lds1(st.scale[wave], scales + w.scale_at(a, id, mine + n));
     return pages;
   };
-  // Loads that stay in the caches only where another wave wants them too.
-  auto fetch = [&](auto* p) {
-    if constexpr (GS > 1) return *p;
-    return __builtin_nontemporal_load(p);
-  };
-  auto load_k = [&](int j) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const unsigned char* p = a.k + max(id[t], 0) * a.page_bytes + head_bytes +
-                               static_cast<int64_t>((j + 16 * t) & in_page) * D;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-        raw.k[t][i] = fetch(reinterpret_cast<const u32x4*>(p + k_lane + 64 * i));
-    }
-    // (A choice between the elements of an array would put it into memory.)
-    const int mine = id[0] ^ ((id[0] ^ id[1]) & static_cast<int>(all_of(lane, 4)));
-    raw.scale = scales[max(mine, 0) * a.scale_page + head_scale + (((j + (lane & 31)) & in_page) >> a.block_log)];
-  };
-  auto load_v = [&](int j) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const unsigned char* p = a.v + max(id[t], 0) * a.page_bytes + head_bytes +
-                               static_cast<int64_t>((j + 16 * t) & in_page) * D;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128) {
-          typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-          const u32x2 y = fetch(reinterpret_cast<const u32x2*>(p + v_lane + i * D));
-          raw.v[4 * t + i][0] = y.x;
-          raw.v[4 * t + i][1] = y.y;
-        } else {
-          raw.v[4 * t + i][0] = fetch(reinterpret_cast<const unsigned*>(p + v_lane + i * D));
-        }
-      }
-    }
-  };
-  unsigned pages = 0;
-  if (w0 < w1) {
-    pages = place(w0);
-    load_k(w0);
-    load_v(w0);
-  }
-  using Weights = typename Queries<X, MT>::Weights;
-  // The products of the tile's keys with the queries, the scales of its values (a byte for each of
-  // the positions 4 g + i), and the loads of the next tile's keys; the bits that have a page.
-  auto scores = [&](Weights& p, unsigned* vs, int next) {
-    const unsigned byte = raw.scale;
-    unsigned four = byte << (8 * (lane & 3));
-    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor1>(static_cast<int>(four)));
-    four |= static_cast<unsigned>(dpp_mov<kDppQuadXor2>(static_cast<int>(four)));
-    float ks[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      ks[t] = __uint_as_float(static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (16 * t + n), static_cast<int>(byte << 23))));
-      vs[t] = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (32 + 16 * t + 4 * g), static_cast<int>(four)));
-    }
-    if constexpr (kInLds) {
+  constexpr int kInFlight = 2 * kLoads + 1;
+  int odd_from = -1;
+  auto take = [&](const Stage<D>& st, int j, unsigned pages) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int step = 0; step < kSteps; ++step) {
+      const int sub = (wave / GS * kSteps + step) * 2, j0 = j + 16 * sub;
+      if (!work || j0 >= min(k1, sight.end)) break;
+      typename Queries<X, MT>::Weights p;
+      typename X::Raw raw;
+      float vs[8];
       u32x4 k[2][X::kFrags];
-      X::keys(k[0], raw, 0, ks[0]);
-      X::keys(k[1], raw, 1, ks[1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int row = 16 * (sub + t);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) raw.k[t][i] = st.k[(row + n) * kRow + ((4 * i + g) ^ k_turn)];
+        X::keys(k[t], raw, t, scale_of(st.scale[sub + t][n]));
+      }
+      __builtin_amdgcn_s_setprio(1);
+      // (A tile's queries are fetched while the one before multiplies.)
+      u32x4 q[2][kInLds ? X::kQ : 1];
+      if constexpr (kInLds)
+#pragma unroll
+        for (int f = 0; f < X::kQ; ++f) q[0][f] = q_s[wave % GS][f][lane];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        if constexpr (kInLds)
+          if (m + 1 < MT)
+#pragma unroll
+            for (int f = 0; f < X::kQ; ++f) q[(m + 1) % 2][f] = q_s[wave % GS][(m + 1) * X::kQ + f][lane];
         f32x4 sum[2] = {};
 #pragma unroll
         for (int f = X::kQ - 1; f >= 0; --f) {
-          const u32x4 q = q_s[wave % GS][m * X::kQ + f][lane];
+          u32x4 x;
+          if constexpr (kInLds) {
+            x = q[m % 2][f];
+          } else {
+            x = Q.q[m][f];
+          }
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[t][f % X::kFrags]),
-                                                             __builtin_bit_cast(bf16x8, q), sum[t], 0, 0, 0);
+                                                             __builtin_bit_cast(bf16x8, x), sum[t], 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) p[m][t][i] = sum[t][i];
+        if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
+      __builtin_amdgcn_s_setprio(0);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        u32x4 k[X::kFrags];
-        X::keys(k, raw, t, ks[t]);
-        Q.score(p, t, k);
-      }
-    }
-    const unsigned here = pages;
-    if (next < w1) {
-      pages = place(next);
-      load_k(next);
-    }
-    return here;
-  };
-  int odd_from = -1;  // the first tile with NaN that were taken out
-#pragma unroll 1
-  for (int j0 = w0; j0 < w1; j0 += kTile) {
-    Weights p;
-    unsigned vs[2];
-    const unsigned here = scores(p, vs, j0 + kTile);
-    if (here != ~0u || j0 + kTile > min(sight.all, w1)) {
-      // Some query does not see all of the tile.
-      const unsigned any = Q.visible(j0, sight.end, here);
-      X::hide(raw, vs, any >> (4 * g));
+        const u32x4 b = *reinterpret_cast<const u32x4*>(&st.scale[sub + t][16 + 4 * g]);
+        const unsigned char* v = reinterpret_cast<const unsigned char*>(st.v + 16 * (sub + t) * kRow) + g * D + n * (D / 16);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const unsigned see = seen_of(Q, m, j0, any, a, call, par_s) >> (4 * g);
-        __builtin_amdgcn_sched_barrier(0);
-        // (By masks of bits: comparisons would take two scalar registers for each product.)
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const unsigned in = all_of(see, 16 * (r / 4) + r % 4);
-          float& x = p[m][r / 4][r % 4];
-          x = __uint_as_float((__float_as_uint(x) & in) | (0xff800000u & ~in));
+        for (int i = 0; i < 4; ++i) {
+          vs[4 * t + i] = scale_of(b[i]);
+          if constexpr (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2*>(v + 4 * i * D);
+            raw.v[4 * t + i][0] = y.x;
+            raw.v[4 * t + i][1] = y.y;
+          } else {
+            raw.v[4 * t + i][0] = *reinterpret_cast<const unsigned*>(v + 4 * i * D);
+          }
         }
       }
-      // NaN among values that not every query sees would meet weights of zero: they go apart.
-      if (__any(X::odd(raw))) {
-        if (odd_from < 0) odd_from = j0;
-        X::clean(raw);
-      }
+      const unsigned here = (pages >> sub & 1u ? 0xffffu : 0u) | (pages >> sub & 2u ? 0xffff0000u : 0u);
+      if (use_tile<X, MT>(Q, p, raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
     }
-    soften8<X, MT>(Q, p, a.scale_log2);
-    X::template outputs<MT>(Q.o, Q.sum, raw, vs, p);
-    if (j0 + kTile < w1) load_v(j0 + kTile);
-  }
-  if (odd_from >= 0) {
-    // Once more over the tiles that some query does not see, for their NaN.
-    walk.fetch(odd_from);
+  };
+  // The tile at hand has arrived when no more than the next one's loads are in flight, for every
+  // wave; and every wave is done with the one before it, whose place the tile after the next takes.
+  if (k0 < k1) {
+    unsigned here = issue(0, k0), next = issue(1, k0 + kWide);
+    int now = 0;
 #pragma unroll 1
-    for (int j0 = odd_from; j0 < w1; j0 += kTile) {
-      const unsigned here = place(j0);
-      if (here == ~0u && j0 + kTile <= min(sight.all, w1)) continue;
-      const unsigned any = Q.visible(j0, sight.end, here);
-      unsigned see[MT], none[2] = {0u, 0u};
-      load_v(j0);
-      X::hide(raw, none, any >> (4 * g));
-#pragma unroll
-      for (int m = 0; m < MT; ++m) see[m] = seen_of(Q, m, j0, any, a, call, par_s);
-      X::template poison<MT>(Q.o, raw, see);
+    for (int j = k0; j < k1; j += kWide) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0070 | kInFlight);  // vmcnt(kInFlight) lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const unsigned after = issue(now == 0 ? kRing - 1 : now - 1, j + 2 * kWide);
+      take(ring_s[now], j, here);
+      here = next;
+      next = after;
+      now = now == kRing - 1 ? 0 : now + 1;
     }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  if (odd_from >= 0) {
+    typename X::Raw raw;
+    const int last = min(k1, sight.end);
+    poison_from<X, MT>(Q, raw, walk, odd_from, last, sight, a, w, call, par_s, 4 * g * D + n * (D / 16));
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
-
-  // The shares of a group join, halves at a time.
-  const int mine = wave / GS;
-#pragma unroll
-  for (int half = kShares / 2; half > 0; half /= 2) {
-    __syncthreads();
-    if (mine >= half && mine < 2 * half) {
-      const int to = wave - half * GS;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        join_s.ml[to][m][lane] = make_float2(Q.mx[m], Q.sum[m][0]);
-#pragma unroll
-        for (int j = 0; j < X::kOut; ++j) join_s.o[to][m * X::kOut + j][lane] = Q.o[m][j];
-      }
-    }
-    __syncthreads();
-    if (mine < half) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float2 y = join_s.ml[wave][m][lane];
-        const float now = fmaxf(Q.mx[m], y.x);
-        const float fa = __builtin_amdgcn_exp2f(Q.mx[m] - now);
-        const float fb = __builtin_amdgcn_exp2f(y.x - now);
-        Q.mx[m] = now;
-        Q.sum[m][0] = Q.sum[m][0] * fa + y.y * fb;
-#pragma unroll
-        for (int j = 0; j < X::kOut; ++j)
-          Q.o[m][j] = Q.o[m][j] * fa + join_s.o[wave][m * X::kOut + j][lane] * fb;
-      }
-    }
+  if constexpr (kShares > 1) {
+    static_assert(sizeof(Joins<X, GS>) <= sizeof(Stage<D>), "the tiles' place holds a join");
+    join_shares<GS>(Q, *reinterpret_cast<Joins<X, GS>*>(ring_s));
   }
-  if (mine == 0 && work) Q.store(a, call, x.kvh, x.split);
+  if (wave < GS && work) Q.store(a, call, x.kvh, x.split);
 }
 
 // Query tiles of a wave, and query groups of a workgroup.
@@ -578,26 +765,27 @@ struct Shape {
 };
 
 Shape shape_of(int tiles, int dtype) {
-  const int mt = dtype == WF_F32 ? 1 : tiles <= 1 ? 1 : tiles <= 2 ? 2 : 3;
-  const int groups = (tiles + mt - 1) / mt;
-  return Shape{mt, groups > 2 ? 4 : groups > 1 ? 2 : 1};
-}
-
-template <int DT, int D, int MT>
-void launch_groups(const Attend8Args& a, int gs, int64_t blocks, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-  if (gs == 1) go(attend8_kernel<DT, D, MT, 1>);
-  if (gs == 2) go(attend8_kernel<DT, D, MT, 2>);
-  if (gs == 4) go(attend8_kernel<DT, D, MT, 4>);
+  if (dtype == WF_F32) return tiles <= 1 ? Shape{1, 1} : tiles <= 2 ? Shape{1, 2} : Shape{1, 4};
+  if (tiles <= 2) return Shape{tiles <= 1 ? 1 : 2, 1};
+  if (tiles <= 4) return Shape{2, 2};
+  if (tiles <= 6) return Shape{3, 2};
+  return Shape{2, 4};
 }
 
 template <int DT, int D>
 void launch_typed(const Attend8Args& a, Shape s, int64_t blocks, hipStream_t stream) {
-  if (s.mt == 1) launch_groups<DT, D, 1>(a, s.gs, blocks, stream);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
   if constexpr (DT == WF_BF16) {
-    if (s.mt == 2) launch_groups<DT, D, 2>(a, s.gs, blocks, stream);
-    if (s.mt == 3) launch_groups<DT, D, 3>(a, s.gs, blocks, stream);
+    if (s.mt == 1) go(attend8_kernel<DT, D, 1>);
+    if (s.mt == 2 && s.gs == 1) go(attend8_kernel<DT, D, 2>);
+    if (s.mt == 2 && s.gs == 2) go(attend8_wide_kernel<DT, D, 2, 2>);
+    if (s.mt == 2 && s.gs == 4) go(attend8_wide_kernel<DT, D, 2, 4>);
+    if (s.mt == 3) go(attend8_wide_kernel<DT, D, 3, 2>);
+  } else {
+    if (s.gs == 1) go(attend8_kernel<DT, D, 1>);
+    if (s.gs == 2) go(attend8_wide_kernel<DT, D, 1, 2>);
+    if (s.gs == 4) go(attend8_wide_kernel<DT, D, 1, 4>);
   }
 }
 
