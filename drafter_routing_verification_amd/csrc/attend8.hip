@@ -573,6 +573,8 @@ struct Stage {
 __device__ inline unsigned lds_address(const void* p) {
   return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
 }
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // (m0 is a reserved register: nothing else uses it)
 __device__ inline void to_lds16(const void* to, const unsigned char* base, unsigned offset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(lds_address(to)), "v"(offset), "s"(base) : "m0", "memory");
@@ -581,6 +583,7 @@ __device__ inline void to_lds1(const void* to, const unsigned char* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, off"
                :: "s"(lds_address(to)), "v"(p) : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // More queries: GS groups of 16 MT share every tile, which all four waves fetch together, straight into
 // LDS and two tiles ahead; the waves take a group and one of 4 / GS shares of the tile each.

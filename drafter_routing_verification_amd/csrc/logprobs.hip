@@ -1,55 +1,82 @@
 // Log probabilities of given tokens, entropy and most likely tokens of logits rows
 // (whiflash_token_logprobs), in one pass over the logits.
 //
-// Every thread keeps, for the vectors it takes, S = sum of e^(x - r), U = sum of (x - r) e^(x - r)
-// and the true maximum; r is a maximum it has seen, raised only when a vector's exceeds it by
-// more than kSlack, so that hardly any vector rescales.  Sums over another reference follow from
-//   S' = f S,  U' = f (U + (r - r') S),  f = e^(r - r'),
-// and with the row's maximum M: log p(x) = (x - M) - ln S, H = ln S - U / S.
+// In base 2, with a reference m and t = (x - m) log2 e, a lane sums S = sum of 2^t and U = sum of
+// t 2^t over the elements it takes.  With the largest logit M and both sums moved to it,
+//   log p(x) = (x - M) - ln T,  H = ln T - ln 2 U / T,  T = S.
+// The reference is a wave's: the largest logit seen when one passed it by more than kSlack last.
 //
-// The most likely tokens: a wave keeps the 64 best it has seen as a sorted list, one a lane.  What
-// exceeds the list's place `top` is put aside in LDS, 64 at a time are sorted and merged.  The
-// first vectors set the bar: the top-th largest of the lanes' maxima is held by as many elements.
-// A wave's vectors come in the order of their indices, so that a later element equal to the bar
-// never displaces an earlier one.
+// A row with one likely token: T = 1 + the rest, and the rest, which the entropy consists of, would
+// lose its digits in the lane that also holds the 1.  If T < kSharp, that lane's elements are read
+// once more and summed without the largest, which is counted apart:
+//   T = c + S, ln T = ln c + ln(1 + S / c).
+//
+// t is one operation, x log2 e - r, with r = m log2 e rounded; the rounding of r (t of m itself, at
+// most 0.09 as long as |m| <= 2^20) is taken out of S and U when they are moved.  Beyond that t comes
+// from the difference.
+//
+// The most likely tokens are found behind the sums: a lane leaves the largest element of each of up
+// to kSlots groups of its vectors in LDS.  The `top`-th largest of the lanes' largest elements is
+// reached by at least `top` elements; the groups that reach it are read once more, and the elements in
+// them that reach it are sorted.  Where more than kFew groups of a wave do (many equal logits, few
+// logits), the wave reads its part of the row once more instead, 64 of the elements that reach the bar
+// at a time being sorted and merged into the best so far, which raise the bar.
 #include <limits.h>
 #include <math.h>
 
 #include "decode.h"
+#include "dpp.h"
 #include "elem.h"
 
 namespace wf {
 namespace {
 
 constexpr float kLog2E = 1.44269504088896340736f;
-constexpr float kFloor = -3.402823466e38f;  // a reference below every finite logit
-constexpr float kSlack = 8.f;
-constexpr float kFar = -1000.f;  // e^kFar is 0: what stands for -inf where it meets that 0
-constexpr int kAhead = 4;        // vectors in flight per thread
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kFar = -1000.f;        // 2^kFar is 0: what stands for -inf where it meets that 0
+constexpr float kPlain = 1048576.f;    // references up to this take t in one operation
+constexpr float kSlack = 0.7f;         // what a logit may pass the reference by
+constexpr float kSharp = 1.5f;
+constexpr int kAhead = 2;              // vectors of a batch
+constexpr int kSlots = 16;             // groups of a lane
+constexpr int kFew = 64;               // groups of a wave that are read one by one
 constexpr int kList = 64;
 
 struct LogprobsArgs {
   const unsigned char* logits;
   int64_t row_bytes;
   int total_rows, V, n, given, top, chunks, vecs, nvec;
+  int group;       // 2^group batches of a lane are a group
   const int32_t* rows;
   const int32_t* tokens;
   float* logprob;
   float* entropy;
   int32_t* top_tokens;
   float* top_logprobs;
-  float4* stats;   // [n][chunks] maximum, S, U
+  float4* stats;   // [n][chunks] m, c, S, U
   float2* lists;   // [n][chunks][top] value, index bits
 };
 
-// Sums relative to a reference m.
+// Sums of a part of a row relative to m, c of its elements equal to m apart; m = -inf: nothing seen.
 struct Sums {
-  float m, s, u;
+  float m, c, s, u;
+
   __device__ inline void move(float to) {
-    const float f = __builtin_amdgcn_exp2f((m - to) * kLog2E);
-    u = f > 0.f ? f * (u + (m - to) * s) : 0.f;
-    s = f > 0.f ? f * s : (s != s ? s : 0.f);
+    if (!(to > m)) return;
+    const float d = (m - to) * kLog2E, f = __builtin_amdgcn_exp2f(d), all = s + c;
+    // (f is 0 from -inf, and from so far below that nothing is left; NaN stays.)
+    u = f > 0.f ? f * fmaf(d, all, u) : 0.f;
+    s = f > 0.f ? f * all : all != all ? all : 0.f;
+    c = 0.f;
     m = to;
+  }
+  __device__ inline void join(Sums o) {
+    const float to = fmaxf(m, o.m);
+    move(to);
+    o.move(to);
+    c += o.c;
+    s += o.s;
+    u += o.u;
   }
 };
 
@@ -93,51 +120,103 @@ __device__ inline void merge_wave(Entry& e, const Entry& other) {
   for (int j = 32; j > 0; j >>= 1) exchange(e, j, (lane & j) == 0);
 }
 
-// The most likely entries that a wave has seen.
+// The number behind x.
+__device__ inline float next_up(float x) {
+  const int b = __float_as_int(x);
+  if (x == 0.f) return __int_as_float(1);
+  return __int_as_float(b > 0 ? b + 1 : b - 1);
+}
+
+// The most likely of the entries offered to a wave.
 struct Best {
   Entry list;
-  float bar;
+  float own;        // what a later entry has to reach
   int waiting;      // uniform
+  bool empty;       // uniform: the list is
   float2* aside;    // the wave's 128 places
 
   __device__ inline void start(float2* lds) {
     list = Entry{-INFINITY, INT_MAX};
-    bar = -INFINITY;
+    own = -INFINITY;
     waiting = 0;
+    empty = true;
     aside = lds;
   }
-  __device__ inline void take_in() {
+  // Sorts 64 of `many` entries at `from` into the list.
+  __device__ inline void sort_in(const float2* from, int many) {
+    const int lane = threadIdx.x & 63;
+    const float2 x = from[lane];
+    Entry e{x.x, __float_as_int(x.y)};
+    if (lane >= many) e = Entry{-INFINITY, INT_MAX};
+    sort_wave(e);
+    if (empty) {
+      list = e;
+    } else {
+      merge_wave(list, e);
+    }
+    empty = false;
+  }
+  __device__ inline void take_in(int top) {
     const int lane = threadIdx.x & 63;
     wave_sync();
-    const float2 x = aside[lane], rest = aside[lane + kList];
+    const float2 rest = aside[lane + kList];
+    sort_in(aside, waiting);
     wave_sync();
     aside[lane] = rest;
-    Entry e{x.x, __float_as_int(x.y)};
-    if (lane >= waiting) e = Entry{-INFINITY, INT_MAX};
     waiting = max(waiting - kList, 0);
-    sort_wave(e);
-    merge_wave(list, e);
+    own = next_up(place(list.v, top));
   }
   // Puts this lane's entry aside if `on`.
-  __device__ inline void offer(bool on, float v, int i) {
+  __device__ inline void offer(bool on, float v, int i, int top) {
     const unsigned long long mask = __ballot(on);
     if (mask == 0) return;
     const int before = __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(mask >> 32),
                                                  __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(mask), 0));
     if (on) aside[waiting + before] = make_float2(v, __int_as_float(i));
     waiting += __popcll(mask);
-    if (waiting >= kList) take_in();
+    if (waiting >= kList) take_in(top);
   }
-  __device__ inline void raise(int top) {
-    bar = fmaxf(bar, __shfl(list.v, top - 1));
-  }
-  // The bar that the lanes' largest values set.
-  __device__ inline void first_bar(float lane_max, int top) {
-    Entry e{lane_max, static_cast<int>(threadIdx.x & 63)};
-    sort_wave(e);
-    bar = __shfl(e.v, top - 1);
+  // The n-th largest of a sorted wave.
+  __device__ static inline float place(float v, int n) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), n - 1));
   }
 };
+
+// The lane 63 of a wave's value, in every lane.
+__device__ inline float last_lane(float x) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+__device__ inline float wave_max(float x) {
+  x = fmaxf(x, dpp_mov<kDppQuadXor1>(x));
+  x = fmaxf(x, dpp_mov<kDppQuadXor2>(x));
+  x = fmaxf(x, dpp_mov<kDppHalfMirror>(x));
+  x = fmaxf(x, dpp_mov<kDppMirror>(x));
+  x = fmaxf(x, dpp_mov<kDppBcast15, 0xa>(x));
+  x = fmaxf(x, dpp_mov<kDppBcast31, 0xc>(x));
+  return last_lane(x);
+}
+
+// The n-th largest (n >= 1) of a wave's N values a lane, which have no more than BITS bits, found bit
+// by bit.
+template <int BITS, int N>
+__device__ inline float nth_largest(const float* x, int n) {
+  unsigned key[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int b = __float_as_int(x[j]);
+    key[j] = static_cast<unsigned>(b) ^ (static_cast<unsigned>(b >> 31) | 0x80000000u);
+  }
+  unsigned at = 0;
+#pragma unroll 1
+  for (unsigned bit = 0x80000000u; bit != (BITS == 32 ? 0u : 0x80000000u >> (BITS & 31)); bit >>= 1) {
+    int reach = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) reach += __popcll(__ballot(key[j] >= (at | bit)));
+    if (reach >= n) at |= bit;
+  }
+  const unsigned rest = BITS == 32 ? 0u : 0xffffffffu >> (BITS & 31);
+  return __uint_as_float(at & 0x80000000u ? at ^ 0x80000000u : ~(at | rest));
+}
 
 __device__ inline int64_t row_of(const LogprobsArgs& a, int i) {
   const int r = a.rows ? a.rows[i] : i;
@@ -148,8 +227,9 @@ __device__ inline int64_t row_of(const LogprobsArgs& a, int i) {
 template <int DT>
 __device__ inline void emit(const LogprobsArgs& a, int i, int64_t row, const Sums& x, const Entry& e) {
   const int lane = threadIdx.x & 63;
-  const bool any = row >= 0 && x.s > 0.f && x.s < INFINITY;  // (false for NaN)
-  const float ln = any ? logf(x.s) : NAN;
+  const float total = x.c + x.s;
+  const bool any = row >= 0 && total > 0.f && total < INFINITY && x.m < INFINITY;  // (false for NaN)
+  const float ln = !any ? NAN : x.c > 0.f ? logf(x.c) + log1pf(x.s / x.c) : logf(x.s);
   for (int j = lane; j < a.given; j += 64) {
     const int64_t at = static_cast<int64_t>(i) * a.given + j;
     const int t = a.tokens[at];
@@ -157,7 +237,7 @@ __device__ inline void emit(const LogprobsArgs& a, int i, int64_t row, const Sum
     if (any && t >= 0 && t < a.V) p = (Elem<DT>::scalar(a.logits + row * a.row_bytes, t) - x.m) - ln;
     a.logprob[at] = p;
   }
-  if (a.entropy && lane == 0) a.entropy[i] = any ? ln - x.u / x.s : NAN;
+  if (a.entropy && lane == 0) a.entropy[i] = any ? ln - kLn2 * (x.u / total) : NAN;
   if (lane < a.top) {
     const int64_t at = static_cast<int64_t>(i) * a.top + lane;
     const bool is = any && e.v > -INFINITY;
@@ -166,119 +246,337 @@ __device__ inline void emit(const LogprobsArgs& a, int i, int64_t row, const Sum
   }
 }
 
-// Sums over the lanes of a wave, relative to the largest maximum, in every lane.
-__device__ inline Sums wave_sums(Sums x, float largest) {
+// Joins the sums of a wave's lanes, in every lane.
+__device__ inline Sums wave_sums(Sums x) {
+  float largest = x.m;
   for (int off = 32; off > 0; off >>= 1) largest = fmaxf(largest, __shfl_xor(largest, off));
   x.move(largest);
   for (int off = 32; off > 0; off >>= 1) {
+    x.c += __shfl_xor(x.c, off);
     x.s += __shfl_xor(x.s, off);
     x.u += __shfl_xor(x.u, off);
   }
+  x.m = largest;
   return x;
 }
 
+// What a wave gathers of the vectors it takes.
+template <int DT>
+struct Gather {
+  using E = Elem<DT>;
+  static constexpr int kPer = E::kPerVec;
+  float m, r, over;  // uniform: the reference, m log2 e rounded, what a logit may not pass
+  float s, u;
+  bool careful;      // t comes from x - m
+  bool slow;         // there are -inf among the elements, or careful
+
+  __device__ inline void start() {
+    m = over = -INFINITY;
+    r = s = u = 0.f;
+    careful = slow = false;
+  }
+  // t of an element, no lower than kFar (NaN stays).
+  __device__ inline float scaled(float x) const {
+    const float t = careful ? (x - m) * kLog2E : fmaf(x, kLog2E, -r);
+    return x == -INFINITY ? kFar : __builtin_elementwise_maximum(t, kFar);
+  }
+  // S and U relative to what has t = by.
+  __device__ inline void move(float by) {
+    const float f = __builtin_amdgcn_exp2f(-by);
+    u = f * fmaf(-by, s, u);
+    s *= f;
+  }
+  __device__ inline void move_to(float x) {
+    if (x > -INFINITY) move(careful ? (x - m) * kLog2E : fmaf(x, kLog2E, -r));
+  }
+  // Raises the reference to what a lane has seen, if that has to be.
+  __device__ inline void raise(float most) {
+    if (!__any(most > over)) return;
+    most = wave_max(most);
+    if (m > -INFINITY) {
+      Sums x{m, 0.f, s, u};
+      if (!careful) {
+        move(fmaf(m, kLog2E, -r));
+        x.s = s;
+        x.u = u;
+      }
+      x.move(most);
+      s = x.s;
+      u = x.u;
+    }
+    m = most;
+    r = m * kLog2E;
+    over = m + kSlack;
+    careful = !(fabsf(m) <= kPlain);
+    slow |= careful;
+    if (!careful) move(-fmaf(m, kLog2E, -r));
+  }
+  __device__ inline void one(float x) {
+    const float t = scaled(x), e = __builtin_amdgcn_exp2f(t);
+    s += e;
+    u = fmaf(t, e, u);
+  }
+  // A batch of vectors; most: the largest of the lane's elements so far.
+  __device__ inline void batch(const u32x4* d, float& most) {
+    float y[kAhead * kPer];
+#pragma unroll
+    for (int k = 0; k < kAhead * kPer; ++k) y[k] = E::at(d[k / kPer], k % kPer);
+#pragma unroll
+    for (int k = 0; k < kAhead * kPer; ++k) most = __builtin_elementwise_maximum(most, y[k]);
+    if (!slow) {
+      float s1 = s, u1 = u;
+#pragma unroll
+      for (int k = 0; k < kAhead * kPer; k += 4) {
+        float e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float t = fmaf(y[k + j], kLog2E, -r);
+          e[j] = __builtin_amdgcn_exp2f(t);
+          u1 = fmaf(t, e[j], u1);
+        }
+        s1 += (e[0] + e[1]) + (e[2] + e[3]);
+      }
+      // (-inf among them makes U NaN.)
+      const bool passed = __any(most > over), none = __any(u1 != u1);
+      if (!passed && !none) {
+        s = s1;
+        u = u1;
+        return;
+      }
+      slow = !passed;
+    }
+    raise(most);
+#pragma unroll
+    for (int k = 0; k < kAhead * kPer; ++k) one(y[k]);
+  }
+};
+
 // One workgroup per (row, chunk).
 template <int DT, bool TOP>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobsArgs a) {
   using E = Elem<DT>;
   constexpr int kPer = E::kPerVec;
-  __shared__ float2 aside_s[kWaves][2 * kList];
-  __shared__ float4 stats_s[kWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // A vector of nothing but -inf.
+  constexpr unsigned kNone = DT == WF_BF16 ? 0xff80ff80u : 0xff800000u;
+  constexpr int kBatch = kAhead * kThreads;
+  __shared__ float groups_s[TOP ? kWaves : 1][kSlots * 64];  // then the entries put aside
+  __shared__ int flagged_s[TOP ? kWaves : 1][kFew];
+  __shared__ float most_s[kThreads];
+  __shared__ float4 stats_s[kWaves], sharp_s;
+  __shared__ int2 found_s[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = blockIdx.x / a.chunks, c = blockIdx.x - i * a.chunks;
   const int64_t row = row_of(a, i);
-  Sums x{kFloor, 0.f, 0.f};
-  float largest = kFloor;
-  Best best;
-  best.start(aside_s[wave]);
-  if (row >= 0) {
-    const unsigned char* rowp = a.logits + row * a.row_bytes;
-    const u32x4* vp = reinterpret_cast<const u32x4*>(rowp);
-    const int v0 = c * a.vecs, v1 = min(v0 + a.vecs, a.nvec);
-    auto absorb = [&](const float* y, float top) {
-      largest = fmaxf(largest, top);
-      if (top > x.m + kSlack) x.move(top);
+  Gather<DT> all;
+  all.start();
+  float most = -INFINITY;  // the lane's largest element
+  float over = -INFINITY;  // one that does not fill a vector
+  const unsigned char* rowp = a.logits + (row >= 0 ? row : 0) * a.row_bytes;
+  const u32x4* vp = reinterpret_cast<const u32x4*>(rowp);
+  const int v0 = c * a.vecs, v1 = row >= 0 ? min(v0 + a.vecs, a.nvec) : v0;
+  const int full = v0 + (v1 > v0 ? (v1 - v0) / kBatch * kBatch : 0);
+  float group = -INFINITY;
+  int count = 0;           // batches
+  auto close = [&]() __attribute__((always_inline)) {
+    groups_s[wave][(count >> a.group) * 64 + lane] = group;
+    most = __builtin_elementwise_maximum(most, group);
+    group = -INFINITY;
+  };
+#pragma unroll 1
+  for (int v = v0; v < full; v += kBatch) {
+    u32x4 d[kAhead];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const float d = y[k] - x.m;
-        const float e = __builtin_amdgcn_exp2f(d * kLog2E);
-        x.s += e;
-        x.u += fmaxf(d, kFar) * e;
-      }
-    };
-    auto choose = [&](const float* y, float top, int at, bool first) {
-      if (__ballot(first ? top >= best.bar : top > best.bar) == 0) return;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        best.offer(first ? y[k] >= best.bar : y[k] > best.bar, y[k], at + k);
-      if (!first) best.raise(a.top);
-    };
-    bool first = true;
-    for (int v = v0 + tid - lane; v < v1; v += kAhead * kThreads) {  // (uniform over the wave)
-      u32x4 d[kAhead];
-      float top[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (v + lane + u * kThreads < v1) d[u] = load16(vp + v + lane + u * kThreads);
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) top[u] = v + lane + u * kThreads < v1 ? E::vmax(d[u]) : -INFINITY;
-      if (TOP && first) {
-        float most = top[0];
-#pragma unroll
-        for (int u = 1; u < kAhead; ++u) most = fmaxf(most, top[u]);
-        best.first_bar(most, a.top);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const bool have = v + lane + u * kThreads < v1;
-        float y[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) y[k] = have ? E::at(d[u], k) : -INFINITY;
-        if (have) absorb(y, top[u]);
-        if (TOP) choose(y, top[u], (v + lane + u * kThreads) * kPer, first);
-      }
-      if (TOP && first) best.raise(a.top);
-      first = false;
+    for (int u = 0; u < kAhead; ++u) d[u] = load16(vp + v + u * kThreads + tid);
+    all.batch(d, TOP ? group : most);
+    if (TOP) {
+      if ((count + 1 & (1 << a.group) - 1) == 0) close();
+      ++count;
     }
-    // What does not fill a vector, by the last wave of the last chunk (its indices are the largest).
-    const int rest = a.V - a.nvec * kPer;
-    if (rest > 0 && c == a.chunks - 1 && wave == kWaves - 1) {
-      float y[kPer];
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        y[k] = lane == 0 && k < rest ? E::scalar(rowp, a.nvec * kPer + k) : -INFINITY;
-        top = fmaxf(top, y[k]);
-      }
-      absorb(y, top);
-      if (TOP) choose(y, top, a.nvec * kPer, first);
-    }
-    if (TOP && best.waiting > 0) best.take_in();
   }
-  x = wave_sums(x, largest);
-  if (lane == 0) stats_s[wave] = make_float4(x.m, x.s, x.u, 0.f);
+  if (full < v1) {
+    u32x4 d[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      d[u] = u32x4{kNone, kNone, kNone, kNone};
+      if (full + u * kThreads + tid < v1) d[u] = load16(vp + full + u * kThreads + tid);
+    }
+    all.slow = true;
+    all.batch(d, TOP ? group : most);
+    if (TOP) {
+      if ((count + 1 & (1 << a.group) - 1) == 0) close();
+      ++count;
+    }
+  }
+  if (TOP && (count & (1 << a.group) - 1) != 0) close();
+  // What does not fill a vector, by the last wave of the last chunk (its indices are the largest).
+  if (row >= 0 && c == a.chunks - 1 && wave == kWaves - 1 && a.nvec * kPer < a.V) {
+    if (lane < a.V - a.nvec * kPer) over = E::scalar(rowp, a.nvec * kPer + lane);
+    most = __builtin_elementwise_maximum(most, over);
+    all.raise(over);
+    all.one(over);
+  }
+
+  // The workgroup's largest element and sums.
+  const float largest = wave_max(most);
+  all.move_to(largest);
+  float s = wave_sum_to_lane63(all.s), u = wave_sum_to_lane63(all.u);
+  if (lane == 63) stats_s[wave] = make_float4(largest, 0.f, s, u);
+  if (TOP) most_s[tid] = most;
+  __syncthreads();
+  Sums x{-INFINITY, 0.f, 0.f, 0.f};
+  for (int w = 0; w < kWaves; ++w) {
+    const float4 y = stats_s[w];
+    x.join(Sums{y.x, y.y, y.z, y.w});
+  }
+  const bool sharp = x.m > -INFINITY && x.s < kSharp;
+  const unsigned long long holds = __ballot(most == x.m);
+  if (sharp && holds) {
+    // (One lane of the workgroup: two would have summed to 2.)
+    const int from = __ffsll(holds) - 1;
+    all.m = x.m;
+    all.careful = true;
+    float n = 0.f;
+    if (lane == from) all.s = all.u = 0.f;
+    auto add = [&](float y) {
+      if (y == x.m) {
+        n += 1.f;
+      } else {
+        all.one(y);
+      }
+    };
+    if (lane == from) add(over);
+#pragma unroll 1
+    for (int v = v0 + wave * 64 + from + lane * kThreads; v < v1; v += 64 * kThreads) {
+      const u32x4 d = load16(vp + v);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) add(E::at(d, k));
+    }
+    n = wave_sum_to_lane63(n);
+    s = wave_sum_to_lane63(all.s);
+    u = wave_sum_to_lane63(all.u);
+    if (lane == 63) sharp_s = make_float4(x.m, n, s, u);
+  }
+
+  // The most likely.
+  Best best;
+  best.start(reinterpret_cast<float2*>(groups_s[TOP ? wave : 0]));
   if (TOP) {
-    wave_sync();
-    aside_s[wave][lane] = make_float2(best.list.v, __int_as_float(best.list.i));
+    float bar;
+    {
+      float y[kWaves];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) y[w] = most_s[w * 64 + lane];
+      bar = nth_largest<DT == WF_BF16 ? 16 : 32, kWaves>(y, a.top);
+      bar = fmaxf(bar, next_up(-INFINITY));
+    }
+    const int slots = (count + (1 << a.group) - 1) >> a.group;
+    int flagged = 0;
+    for (int g = 0; g < slots; ++g) {
+      const unsigned long long high = __ballot(groups_s[wave][g * 64 + lane] >= bar);
+      if (high == 0) continue;
+      const int at = flagged + __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(high >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(high), 0));
+      if ((high >> lane & 1) && at < kFew) flagged_s[wave][at] = g << 6 | lane;
+      flagged += __popcll(high);
+    }
+    wave_sync();  // (the groups have been read: their place is that of the entries now)
+    // A vector's elements that reach the bar, the first of them at index `at`.
+    auto offer = [&](u32x4 d, int at) {
+#pragma unroll 1
+      for (int k = 0; k < kPer; ++k) {
+        const float y = E::at(d, 0);
+        best.offer(y >= bar, y, at + k, a.top);
+        // (The next element to the front: a choice among registers by k would cost more.)
+        if constexpr (DT == WF_BF16) {
+          d = u32x4{__builtin_amdgcn_alignbit(d.y, d.x, 16), __builtin_amdgcn_alignbit(d.z, d.y, 16),
+                    __builtin_amdgcn_alignbit(d.w, d.z, 16), d.w >> 16};
+        } else {
+          d = u32x4{d.y, d.z, d.w, d.w};
+        }
+      }
+    };
+    if (flagged <= kFew) {
+      // 2^wide vectors of a group, as many groups at a time as there are lanes for.
+      const int wide = a.group + (kAhead == 2 ? 1 : 0);
+      static_assert(kAhead == 2, "a group's vectors are a power of two");
+      for (int t0 = 0; t0 < flagged << wide; t0 += 64) {
+        const int t = t0 + lane;
+        u32x4 d{kNone, kNone, kNone, kNone};
+        int v = 0;
+        if (t < flagged << wide) {
+          const int f = flagged_s[wave][t >> wide];
+          v = v0 + ((f >> 6 << wide) + (t & (1 << wide) - 1)) * kThreads + wave * 64 + (f & 63);
+          if (v < v1) d = load16(vp + v);
+        }
+        offer(d, v * kPer);
+      }
+    } else {
+#pragma unroll 1
+      for (int v = v0 + wave * 64; v < v1; v += kThreads) {  // (uniform over the wave)
+        u32x4 d{kNone, kNone, kNone, kNone};
+        if (v + lane < v1) d = load16(vp + v + lane);
+        if (!__any(E::vmax(d) >= bar)) continue;
+        offer(d, (v + lane) * kPer);
+        // (A later vector's elements have the larger indices: one that equals the list's last is no better.)
+        bar = fmaxf(bar, best.own);
+      }
+    }
+    best.offer(over >= bar, over, a.nvec * kPer + lane, a.top);
+    if (!best.empty) {
+      if (best.waiting > 0) best.take_in(a.top);
+      wave_sync();
+      best.aside[lane] = make_float2(best.list.v, __int_as_float(best.list.i));
+      best.waiting = kList;
+    }
+    if (lane == 0) found_s[wave] = make_int2(best.waiting, best.empty);
   }
   __syncthreads();
   if (wave > 0) return;
-  const float4 mine = stats_s[lane & (kWaves - 1)];
-  x = wave_sums(lane < kWaves ? Sums{mine.x, mine.y, mine.z} : Sums{kFloor, 0.f, 0.f},
-                lane < kWaves ? mine.x : kFloor);
-  Entry e = best.list;
-  if (TOP)
-    for (int w = 1; w < kWaves; ++w) {
-      const float2 o = aside_s[w][lane];
-      merge_wave(e, Entry{o.x, __float_as_int(o.y)});
+  if (sharp) {
+    x = Sums{-INFINITY, 0.f, 0.f, 0.f};
+    for (int w = 0; w < kWaves; ++w) {
+      const float4 y = stats_s[w].x == sharp_s.x ? sharp_s : stats_s[w];
+      x.join(Sums{y.x, y.y, y.z, y.w});
     }
+  }
+  if (TOP) {
+    best.start(best.aside);
+    int many[kWaves], sum = 0;
+    for (int w = 0; w < kWaves; ++w) sum += many[w] = found_s[w].x;
+    if (sum <= kList) {
+      // All of them at once.
+      Entry e{-INFINITY, INT_MAX};
+      int before = 0;
+      for (int w = 0; w < kWaves; ++w) {
+        if (lane >= before && lane < before + many[w]) {
+          const float2 y = reinterpret_cast<const float2*>(groups_s[w])[lane - before];
+          e = Entry{y.x, __float_as_int(y.y)};
+        }
+        before += many[w];
+      }
+      sort_wave(e);
+      best.list = e;
+    } else {
+      for (int w = 0; w < kWaves; ++w) {
+        const float2* from = reinterpret_cast<const float2*>(groups_s[w]);
+        if (many[w] == 0) continue;
+        if (found_s[w].y) {
+          best.sort_in(from, many[w]);
+        } else {
+          merge_wave(best.list, Entry{from[lane].x, __float_as_int(from[lane].y)});
+          best.empty = false;
+        }
+      }
+    }
+  }
   if (a.chunks == 1) {
-    emit<DT>(a, i, row, x, e);
+    emit<DT>(a, i, row, x, best.list);
     return;
   }
   const int64_t at = static_cast<int64_t>(i) * a.chunks + c;
-  if (lane == 0) a.stats[at] = make_float4(x.m, x.s, x.u, 0.f);
-  if (TOP && lane < a.top) a.lists[at * a.top + lane] = make_float2(e.v, __int_as_float(e.i));
+  if (lane == 0) a.stats[at] = make_float4(x.m, x.c, x.s, x.u);
+  if (TOP && lane < a.top) a.lists[at * a.top + lane] = make_float2(best.list.v, __int_as_float(best.list.i));
 }
 
 // Joins a row's chunks: one wave each.
@@ -287,17 +585,12 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobsArgs a) {
   __shared__ float2 aside_s[2 * kList];
   const int i = blockIdx.x, lane = threadIdx.x;
   const int64_t row = row_of(a, i), base = static_cast<int64_t>(i) * a.chunks;
-  Sums x{kFloor, 0.f, 0.f};
+  Sums x{-INFINITY, 0.f, 0.f, 0.f};
   for (int c = lane; c < a.chunks; c += 64) {
     const float4 y = a.stats[base + c];
-    const float m = fmaxf(x.m, y.x);
-    Sums o{y.x, y.y, y.z};
-    x.move(m);
-    o.move(m);
-    x.s += o.s;
-    x.u += o.u;
+    x.join(Sums{y.x, y.y, y.z, y.w});
   }
-  x = wave_sums(x, x.m);
+  x = wave_sums(x);
   Best best;
   best.start(aside_s);
   if (a.top > 0) {
@@ -305,12 +598,12 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobsArgs a) {
     const int many = a.chunks * a.top;
     float most = -INFINITY;
     for (int t = lane; t < many; t += 64) most = fmaxf(most, all[t].x);
-    best.first_bar(most, a.top);
+    const float bar = nth_largest<32, 1>(&most, a.top);
     for (int t0 = 0; t0 < many; t0 += 64) {
       const float2 y = t0 + lane < many ? all[t0 + lane] : make_float2(-INFINITY, 0.f);
-      best.offer(t0 + lane < many && y.x >= best.bar, y.x, __float_as_int(y.y));
+      best.offer(t0 + lane < many && y.x >= bar, y.x, __float_as_int(y.y), a.top);
     }
-    if (best.waiting > 0) best.take_in();
+    if (best.waiting > 0) best.take_in(a.top);
   }
   emit<DT>(a, i, row, x, best.list);
 }
@@ -370,6 +663,8 @@ hipError_t launch_logprobs(const void* logits, int dtype, int32_t total_rows, in
   a.chunks = plan.chunks;
   a.vecs = plan.vecs;
   a.nvec = V / (dtype == WF_BF16 ? 8 : 4);
+  const int batches = (plan.vecs + kAhead * kThreads - 1) / (kAhead * kThreads);
+  while (batches > kSlots << a.group) ++a.group;
   a.rows = rows;
   a.tokens = tokens;
   a.logprob = logprob;
