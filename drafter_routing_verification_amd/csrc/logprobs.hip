@@ -353,7 +353,7 @@ struct Gather {
 
 // One workgroup per (row, chunk).
 template <int DT, bool TOP>
-__global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobsArgs a) {
+__global__ __launch_bounds__(kThreads, 6) void logprobs_kernel(LogprobsArgs a) {
   using E = Elem<DT>;
   constexpr int kPer = E::kPerVec;
   // A vector of nothing but -inf.
@@ -383,11 +383,21 @@ __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobsArgs a) {
     most = __builtin_elementwise_maximum(most, group);
     group = -INFINITY;
   };
+  // (The next batch is on its way while one is summed.)
+  u32x4 next[kAhead];
+  if (v0 < full) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) next[u] = load16(vp + v0 + u * kThreads + tid);
+  }
 #pragma unroll 1
   for (int v = v0; v < full; v += kBatch) {
     u32x4 d[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) d[u] = load16(vp + v + u * kThreads + tid);
+    for (int u = 0; u < kAhead; ++u) d[u] = next[u];
+    if (v + kBatch < full) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) next[u] = load16(vp + v + kBatch + u * kThreads + tid);
+    }
     all.batch(d, TOP ? group : most);
     if (TOP) {
       if ((count + 1 & (1 << a.group) - 1) == 0) close();
