@@ -11,7 +11,10 @@
 // two teams touch one byte.
 #include <limits.h>
 
+#include <type_traits>
+
 #include "decode.h"
+#include "dpp.h"
 #include "e4m3.h"
 
 namespace wf {
@@ -71,8 +74,10 @@ __device__ inline int64_t scale_at(const Cache8Args& a, int p, int h, int64_t po
 // The largest over a team's lanes.
 template <int TEAM>
 __device__ inline float team_max(float x) {
-#pragma unroll
-  for (int off = 1; off < TEAM; off <<= 1) x = fmaxf(x, __shfl_xor(x, off));
+  x = fmaxf(x, dpp_mov<kDppQuadXor1>(x));
+  x = fmaxf(x, dpp_mov<kDppQuadXor2>(x));
+  x = fmaxf(x, dpp_mov<kDppHalfMirror>(x));
+  if (TEAM > 8) x = fmaxf(x, dpp_mov<kDppMirror>(x));
   return x;
 }
 
@@ -104,11 +109,31 @@ __device__ inline void stand_for(uint2 w, int byte, float* x) {
 
 // ---------------------------------------------------------------- append
 
-template <int DT, int D>
-__global__ __launch_bounds__(kThreads) void cache8_append_kernel(
+// Eight elements of a row that came as one vector (bfloat16) or two.
+template <int DT>
+__device__ inline void eight_of(u32x4 a, u32x4 b, float* x) {
+  if constexpr (DT == WF_BF16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = Elem<DT>::at(a, k);
+  } else {
+    const unsigned y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(y[k]);
+  }
+}
+
+constexpr int kSpan = 8;   // positions of a unit, at least
+constexpr int kHeld = 16;  // the longest block whose rows a team holds in registers
+
+// A unit is a span of positions of a head of the keys or of the values: a block, or as many short
+// ones as kSpan positions hold.  Its rows, ROWS of them, are all on their way at once and stay in
+// registers.  LONG: of a longer block they are read twice, ROWS at a time, first for the largest,
+// then, from the caches, to be written.
+template <int DT, int D, int ROWS, bool LONG>
+__global__ __launch_bounds__(kThreads, ROWS > kSpan ? 2 : 4) void cache8_append_kernel(
     Cache8Args a, int layer, RowsArgs rows, const int32_t* __restrict__ seq,
     const unsigned char* __restrict__ k_rows, int64_t k_bytes,
-    const unsigned char* __restrict__ v_rows, int64_t v_bytes, int wgs) {
+    const unsigned char* __restrict__ v_rows, int64_t v_bytes, int span_log, int wgs) {
   constexpr int kTeam = D / 8, kTeams = kThreads / kTeam;
   const int b = blockIdx.x / wgs;
   const SeqRows q = seq_rows(rows, b);
@@ -116,85 +141,169 @@ __global__ __launch_bounds__(kThreads) void cache8_append_kernel(
   if (q.n == 0 || s < 0) return;
   const int64_t c = a.context[s];
   if (c < 0) return;
-  // Unit: (block of the span, keys or values, head).
-  const int64_t unit = static_cast<int64_t>(blockIdx.x - b * wgs) * kTeams + threadIdx.x / kTeam;
-  const int lane8 = (threadIdx.x % kTeam) * 8;
-  const int64_t nth = unit / (2 * a.heads);
+  const int64_t end = c + q.n;
+  const unsigned unit = static_cast<unsigned>(blockIdx.x - b * wgs) * kTeams + threadIdx.x / kTeam;
+  const int lane = threadIdx.x % kTeam;
+  const unsigned nth = unit / (2 * a.heads);
   const int rest = static_cast<int>(unit - nth * 2 * a.heads);
   const int which = rest >= a.heads ? 1 : 0, h = rest - which * a.heads;
-  const int64_t lo = ((c >> a.block_log) + nth) << a.block_log;
-  const int64_t hi = min(lo + (int64_t{1} << a.block_log), c + q.n);
-  if (lo >= c + q.n) return;
+  const int64_t lo = ((c >> span_log) + nth) << span_log;
+  if (lo >= end) return;
   const int p = page_of(a, s, lo);
   if (p < 0) return;
-  unsigned char* data = a.data[which] + layer * a.layer_bytes + byte_of<D>(a, p, h, lo) + lane8;
+  const int block = 1 << a.block_log;
+  // Positions lo + [kept, fresh) lie in blocks that get rows and have values, lo + [fresh, all) get rows.
+  const int all = static_cast<int>(min(end - lo, int64_t{1} << span_log));
+  const int fresh = static_cast<int>(min(max(c - lo, int64_t{0}), static_cast<int64_t>(all)));
+  const int kept = fresh & ~(block - 1);
+  unsigned char* data = a.data[which] + layer * a.layer_bytes + byte_of<D>(a, p, h, lo) + lane * 8;
   unsigned char* scale = a.scale[which] + layer * a.scale_layer + scale_at(a, p, h, lo);
   const int64_t stride = which ? v_bytes : k_bytes;
   // Row i of the round is position c + i.
   const unsigned char* from = (which ? v_rows : k_rows) + (q.row0 + lo - c) * stride +
-                              (static_cast<int64_t>(h) * D + lane8) * Elem<DT>::kBytes;
-  const int kept = static_cast<int>(min(max(c - lo, int64_t{0}), hi - lo)), all = static_cast<int>(hi - lo);
-  const int old = kept > 0 ? *scale : 0;
-  float top = 0.f;
-  for (int j = 0; j < kept; ++j) {
-    float x[8];
-    stand_for(*reinterpret_cast<const uint2*>(data + j * D), old, x);
-    top = fmaxf(top, largest(x));
-  }
-  for (int j = kept; j < all; ++j) {
-    float x[8];
-    load_eight<DT>(from + j * stride, x);
-    top = fmaxf(top, largest(x));
-  }
-  const int now = scale_for(team_max<kTeam>(top));
-  const float inv = inverse_scale(now);
-  if (now != old) {
-    for (int j = 0; j < kept; ++j) {
-      float x[8];
-      stand_for(*reinterpret_cast<const uint2*>(data + j * D), old, x);
-      *reinterpret_cast<uint2*>(data + j * D) = quantise(x, inv);
+                              (static_cast<int64_t>(h) * D + lane * 8) * Elem<DT>::kBytes;
+  const int old = fresh > kept ? scale[kept >> a.block_log] : 0;
+  u32x4 w[ROWS], w2[ROWS];  // (a bfloat16 row's eight dimensions are the first alone)
+  auto load = [&](int j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int at = j0 + j;
+      if (at >= fresh && at < all) {
+        const unsigned char* x = from + at * stride;
+        w[j] = *reinterpret_cast<const u32x4*>(x);
+        if constexpr (DT != WF_BF16) w2[j] = *reinterpret_cast<const u32x4*>(x + 16);
+      } else if (at >= kept && at < fresh) {
+        const uint2 x = *reinterpret_cast<const uint2*>(data + at * D);
+        w[j] = u32x4{x.x, x.y, 0u, 0u};
+        if constexpr (DT != WF_BF16) w2[j] = u32x4{0u, 0u, 0u, 0u};
+      }
     }
+  };
+  auto value = [&](int j, int at, float* x) __attribute__((always_inline)) {
+    if (at >= fresh) {
+      eight_of<DT>(w[j], w2[j], x);
+    } else {
+      stand_for(make_uint2(w[j].x, w[j].y), old, x);
+    }
+  };
+  float top[ROWS];
+  auto find = [&](int j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      top[j] = 0.f;
+      if (j0 + j < kept || j0 + j >= all) continue;
+      float x[8];
+      value(j, j0 + j, x);
+      top[j] = largest(x);
+    }
+  };
+  int now[ROWS];
+  auto put = [&](int j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int at = j0 + j;
+      if (at < kept || at >= all || (at < fresh && now[j] == old)) continue;
+      float x[8];
+      value(j, at, x);
+      *reinterpret_cast<uint2*>(data + at * D) = quantise(x, inverse_scale(now[j]));
+    }
+  };
+  load(0);
+  find(0);
+  if constexpr (!LONG) {
+    // The largest of each block, in all of its places.
+#pragma unroll
+    for (int step = 1; step < ROWS; step <<= 1) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        if (j & step) continue;
+        const float x = fmaxf(top[j], top[j + step]);
+        top[j] = block > step ? x : top[j];
+        top[j + step] = block > step ? x : top[j + step];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) now[j] = scale_for(team_max<kTeam>(top[j]));
+    put(0);
+    // (Lane j writes the scale of position j's block, if that is the block's first.)
+    int mine = now[0];
+#pragma unroll
+    for (int j = 1; j < ROWS; ++j) mine = lane == j ? now[j] : mine;
+    if (lane >= kept && lane < all && (lane & (block - 1)) == 0)
+      scale[lane >> a.block_log] = static_cast<unsigned char>(mine);
+  } else {
+    float most = 0.f;
+    for (int j0 = 0;;) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) most = fmaxf(most, top[j]);
+      j0 += ROWS;
+      if (j0 >= all) break;
+      load(j0);
+      find(j0);
+    }
+    const int one = scale_for(team_max<kTeam>(most));
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) now[j] = one;
+    for (int j0 = 0; j0 < all; j0 += ROWS) {
+      load(j0);
+      put(j0);
+    }
+    if (lane == 0) *scale = static_cast<unsigned char>(one);
   }
-  for (int j = kept; j < all; ++j) {
-    float x[8];
-    load_eight<DT>(from + j * stride, x);
-    *reinterpret_cast<uint2*>(data + j * D) = quantise(x, inv);
-  }
-  if (lane8 == 0) *scale = static_cast<unsigned char>(now);
 }
 
 // ---------------------------------------------------------------- read
 
-constexpr int kReadRows = 16;  // positions of a workgroup
+constexpr int kReadRows = 16;  // positions of a workgroup, at most
 
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads) void cache8_read_kernel(
     Cache8Args a, int layer, const int32_t* __restrict__ seq, const int32_t* __restrict__ first,
     int count, int pending, unsigned char* __restrict__ k_out, unsigned char* __restrict__ v_out,
-    int wgs) {
-  constexpr int kTeam = D / 8, kTeams = kThreads / kTeam;
-  const int b = blockIdx.x / wgs, i0 = (blockIdx.x - b * wgs) * kReadRows;
+    int per_wg, int wgs) {
+  constexpr int kTeam = D / 8, kTeams = kThreads / kTeam, kOnce = 4;
+  const int b = blockIdx.x / wgs, i0 = (blockIdx.x - b * wgs) * per_wg;
   const int s = slot_of(seq, b, a.seqs);
   const int64_t c = s < 0 ? -1 : a.context[s];
   const int64_t end = c < 0 ? 0 : c + pending;
   const int64_t from = first ? first[b] : 0;
   const int lane8 = (threadIdx.x % kTeam) * 8;
-  const int units = min(count - i0, kReadRows) * a.heads;
-  for (int which = 0; which < 2; ++which) {
-    unsigned char* out = which ? v_out : k_out;
-    if (!out) continue;
-    for (int t = threadIdx.x / kTeam; t < units; t += kTeams) {
-      const int i = t / a.heads, h = t - i * a.heads;
-      const int64_t pos = from + i0 + i;
-      const int p = pos >= 0 && pos < end ? page_of(a, s, pos) : -1;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (p >= 0)
-        stand_for(*reinterpret_cast<const uint2*>(a.data[which] + layer * a.layer_bytes + byte_of<D>(a, p, h, pos) + lane8),
-                  a.scale[which][layer * a.scale_layer + scale_at(a, p, h, pos)], x);
-      const int64_t row = static_cast<int64_t>(b) * count + i0 + i;
-      store_eight<DT>(out + ((row * a.heads + h) * D + lane8) * Elem<DT>::kBytes, x);
+  // Units: (keys or values, position, head).
+  const int each = min(count - i0, per_wg) * a.heads, units = (k_out && v_out ? 2 : 1) * each;
+  for (int t0 = threadIdx.x / kTeam; t0 < units; t0 += kOnce * kTeams) {
+    uint2 w[kOnce];
+    int scale[kOnce];
+    unsigned char* to[kOnce];
+#pragma unroll
+    for (int k = 0; k < kOnce; ++k) {
+      const int t = t0 + k * kTeams, second = t >= each ? 1 : 0;
+      const int which = k_out ? second : 1;
+      const int i = (t - second * each) / a.heads, h = t - second * each - i * a.heads;
+      const int64_t pos = from + i0 + i, row = static_cast<int64_t>(b) * count + i0 + i;
+      const int p = t < units && pos >= 0 && pos < end ? page_of(a, s, pos) : -1;
+      w[k] = make_uint2(0u, 0u);
+      scale[k] = 127;
+      if (p >= 0) {
+        w[k] = *reinterpret_cast<const uint2*>(a.data[which] + layer * a.layer_bytes + byte_of<D>(a, p, h, pos) + lane8);
+        scale[k] = a.scale[which][layer * a.scale_layer + scale_at(a, p, h, pos)];
+      }
+      to[k] = (which ? v_out : k_out) + ((row * a.heads + h) * D + lane8) * Elem<DT>::kBytes;
+    }
+#pragma unroll
+    for (int k = 0; k < kOnce; ++k) {
+      if (t0 + k * kTeams >= units) break;
+      float x[8];
+      stand_for(w[k], scale[k], x);
+      store_eight<DT>(to[k], x);
     }
   }
+}
+
+// Positions a workgroup: fewer of a short read, so that every CU has some.
+int read_rows(int32_t B, int32_t count) {
+  int per = kReadRows;
+  while (per > 1 && static_cast<int64_t>(B) * ((count + per - 1) / per) < 1024) per /= 2;
+  return per;
 }
 
 // ---------------------------------------------------------------- compact
@@ -338,15 +447,18 @@ __global__ __launch_bounds__(kThreads) void cache8_fork_kernel(Cache8Args a,
   }
 }
 
-// Blocks of positions that n rows can reach into.
-int64_t span_blocks(const wf_page_cache8& c, int n) {
-  return (static_cast<int64_t>(n) + 2 * static_cast<int64_t>(c.block) - 2) / c.block;
+// Positions of an append's unit.
+int span_log(const wf_page_cache8& c) {
+  const int span = c.block > kSpan ? c.block : kSpan;
+  return __builtin_ctz(static_cast<unsigned>(span < c.pages.page_size ? span : c.pages.page_size));
 }
 
 // Workgroups a sequence of the append.
 int64_t append_wgs(const wf_page_cache8& c, const RowsArgs& rows) {
   const int teams = kThreads / (c.pages.head_dim / 8);
-  return (span_blocks(c, rows.rmax) * 2 * c.pages.heads + teams - 1) / teams;
+  const int64_t span = int64_t{1} << span_log(c);
+  const int64_t units = (rows.rmax + 2 * span - 2) / span * 2 * c.pages.heads;
+  return units > UINT_MAX - teams ? INT_MAX : (units + teams - 1) / teams;  // (units have 32 bits)
 }
 
 }  // namespace
@@ -363,31 +475,38 @@ hipError_t launch_cache8_append(const wf_page_cache8& cache, int32_t layer, cons
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, cache8_args(cache), layer, rows, seq,
                        static_cast<const unsigned char*>(k_rows), k_stride * bytes,
-                       static_cast<const unsigned char*>(v_rows), v_stride * bytes, wgs);
+                       static_cast<const unsigned char*>(v_rows), v_stride * bytes,
+                       span_log(cache), wgs);
   };
-  const bool wide = cache.pages.head_dim == 128;
-  if (dtype == WF_BF16) {
-    wide ? go(cache8_append_kernel<WF_BF16, 128>) : go(cache8_append_kernel<WF_BF16, 64>);
-  } else {
-    wide ? go(cache8_append_kernel<WF_F32, 128>) : go(cache8_append_kernel<WF_F32, 64>);
-  }
+  const auto sized = [&](auto width) {
+    constexpr int D = decltype(width)::value;
+    const auto rows_of = [&](auto type) {
+      constexpr int DT = decltype(type)::value;
+      if (cache.block <= kSpan) go(cache8_append_kernel<DT, D, kSpan, false>);
+      else if (cache.block <= kHeld) go(cache8_append_kernel<DT, D, kHeld, false>);
+      else go(cache8_append_kernel<DT, D, 4, true>);
+    };
+    dtype == WF_BF16 ? rows_of(std::integral_constant<int, WF_BF16>{}) : rows_of(std::integral_constant<int, WF_F32>{});
+  };
+  cache.pages.head_dim == 128 ? sized(std::integral_constant<int, 128>{}) : sized(std::integral_constant<int, 64>{});
   return hipGetLastError();
 }
 
 int64_t cache8_read_blocks(int32_t B, int32_t count) {
-  return static_cast<int64_t>(B) * ((static_cast<int64_t>(count) + kReadRows - 1) / kReadRows);
+  const int per = read_rows(B, count);
+  return static_cast<int64_t>(B) * ((static_cast<int64_t>(count) + per - 1) / per);
 }
 
 hipError_t launch_cache8_read(const wf_page_cache8& cache, int32_t layer, int32_t B,
                               const int32_t* seq, const int32_t* first, int32_t count,
                               int32_t pending, int dtype, void* k_out, void* v_out,
                               hipStream_t stream) {
-  const int wgs = static_cast<int>(cache8_read_blocks(1, count));
+  const int per = read_rows(B, count), wgs = static_cast<int>(cache8_read_blocks(B, count) / B);
   const dim3 grid(static_cast<unsigned>(B) * wgs), block(kThreads);
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, cache8_args(cache), layer, seq, first, count,
                        pending, static_cast<unsigned char*>(k_out),
-                       static_cast<unsigned char*>(v_out), wgs);
+                       static_cast<unsigned char*>(v_out), per, wgs);
   };
   const bool wide = cache.pages.head_dim == 128;
   if (dtype == WF_BF16) {
