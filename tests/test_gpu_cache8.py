@@ -38,6 +38,22 @@ def test_append(kind, K, N, dtype, heads, dim, page, block):
     same_cache8(o, cache)
 
 
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f32", 64), ("f32", 128), ("bf16", 64)])
+@pytest.mark.parametrize("block", [1, 2, 4, 8, 16, 32, 64, 128])
+def test_append_blocks_of_every_length(dtype, dim, block):
+    # Starts and ends at every place of a block, spans of several blocks, one row and many.
+    heads, page = 3, 128
+    context = [0, 1, 2, 3, 5, 7, 8, 9, 12, 15, 16, 23, 31, 33, 63, 64, 100, 127, 128, 250]
+    for K in (0, 5, 40, 130):
+        r = Round("chain", len(context), K, 0, 100, seed=K)
+        o, cache = make_cache8(1, heads, page, dim, block, context, K + 1, block + K)
+        (k, v), (kx, vx) = vectors(r.total, heads, dim, dtype, 9, parts=2, scale=np.exp(
+            2 * np.random.default_rng(3).normal(0, 1, (r.total, 1, 1))))
+        wf.cache_append(cache, r.rows, k, v)
+        dec.cache_append(o, r.seqs, kx, vx)
+        same_cache8(o, cache)
+
+
 @pytest.mark.parametrize("block", [1, 16])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_every_number_and_odd_values(dtype, block):

@@ -127,6 +127,63 @@ def test_masks_and_odd_rows(dtype):
         _check(x, tokens[i:i + 1], [i], 30, wf.token_logprobs(logits, i32(tokens[i:i + 1]), rows=i32([i]), top=30))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_odd_rows_in_one_piece(dtype):
+    # So many rows that each is one workgroup's: long runs of equal logits, few logits, masks.
+    V, n = 20011, 12
+    rng = np.random.default_rng(4)
+    x = rng.normal(0, 3, (n, V)).astype(np.float32)
+    x[0] = 2.5
+    x[1] = np.round(x[1] / 4)
+    x[2, 40:] = -np.inf
+    x[3, :-5] = -np.inf
+    x[4] = np.sort(x[4])
+    x[5] = -np.inf
+    x[6, ::3] = -np.inf
+    x[7] = 3e6 + np.round(x[7])                 # too far from 0 for the short way to 2^t
+    x[8, 5000:9000] += 40                       # the likely ones side by side
+    x[9, 0] = np.nan
+    x[10, :10000] = -1e30
+    x[11] = -4e6 - np.arange(V) / 4
+    raw = to_bf16(x) if dtype == "bf16" else x
+    x = bits(raw, "bf16") if dtype == "bf16" else x
+    logits = stored(raw, dtype, 20016)
+    rows = np.tile(np.arange(n), 180)
+    tokens = rng.integers(0, V, (len(rows), 1))
+    for top in (0, 3, 64):
+        got = wf.token_logprobs(logits, i32(tokens), rows=i32(rows), top=top)
+        _check(x, tokens[:n], np.arange(n), top, [t[:n] for t in got])
+        for t in got[1:]:
+            first = torch.nan_to_num(t[:n], nan=5.0)
+            for a in range(n, len(rows), n):
+                assert torch.equal(torch.nan_to_num(t[a:a + n], nan=5.0), first)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [20011, 151936])
+@pytest.mark.parametrize("copies", [1, 260])
+def test_the_entropy_of_a_dominant_token_keeps_its_digits(dtype, V, copies):
+    # T = 1 + S: H = ln(1 + S) - ln 2 U / T is a sum of two positive numbers, each as exact as S and U:
+    # every term e^(x - r) is off by a part of (2.3 (d + 8) + 3) u, d at most that of the likeliest of
+    # the others' range that counts (40: what lies further holds less than 2^-24 of the rest), a sum of
+    # V / 256 + 32 of them by as many u, the scaling by 2.3 (d + 8) u, the logarithms and H by 8 u.
+    raw, x = _logits(9, V, "f32", 7, scale=1.0)
+    x = np.array(x)
+    where = [0, 3, V - 1, V - 2, V // 2, 511, 4096, V - 1, 77]
+    gap = [8, 12, 16, 16, 20, 24, 28, 30, 22]
+    for i, (at, d) in enumerate(zip(where, gap)):
+        x[i] = np.random.default_rng(i).normal(0, 1, V)
+        x[i, at] = x[i].max() + d
+    raw = to_bf16(x) if dtype == "bf16" else x
+    x = bits(raw, "bf16") if dtype == "bf16" else x
+    logits = stored(raw, dtype, (V + 7) // 8 * 8)
+    rows = np.tile(np.arange(9), copies)
+    got = host(wf.token_logprobs(logits, rows=i32(rows), top=2)[1]).reshape(copies, 9).astype(np.float64)
+    want = dec.token_logprobs(x, np.zeros((9, 0), int), np.arange(9), 0)[1]
+    tol = (2 * 2.3 * (40 + 8) + 3 + V / 256 + 32 + 8) * 2.0 ** -24 * want
+    assert np.all(np.abs(got - want) <= tol), np.abs(got / want - 1).max()
+
+
 def test_three_dimensions_repeat_and_do_not_depend_on_the_other_rows():
     raw, x = _logits(6, 999, "f32", 5)
     logits = stored(raw, "f32", 1000).unflatten(0, (2, 3))
