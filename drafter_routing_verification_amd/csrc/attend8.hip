@@ -475,8 +475,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
   const int k0 = x.split * a.span;
   if (x.split > 0 && k0 >= sight.end) return;
   const int k1 = min(k0 + a.span, sight.end);
-  // The wave's positions [w0, w1), in whole tiles of the piece.
-  const int share = (a.span / kTile + kWaves - 1) / kWaves * kTile;
+  // The wave's positions [w0, w1), in whole tiles: a quarter of what the piece holds of this sequence.
+  const int share = (max(k1 - k0, 0) + kWaves * kTile - 1) / (kWaves * kTile) * kTile;
   const int w0 = min(k0 + wave * share, k1), w1 = min(w0 + share, k1);
   PageWalk walk(a, call, w0, w1);
   if (call.q.tree && k1 > call.c && call.c >= 0) {
