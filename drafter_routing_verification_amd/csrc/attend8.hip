@@ -458,10 +458,12 @@ __device__ inline void join_shares(Queries<X, MT>& Q, Joins<X, SLOTS>& join_s) {
 }
 
 // Up to 16 MT queries a key-value head: each of the four waves takes a share of the piece, with all
-// queries.  Keys and values come straight from memory, the next tile's while this one is used.
+// queries.  Keys and values come straight from memory, those of the next tiles while one is used: two
+// of them, or one where the registers hold no more.
 template <int DT, int D, int MT>
 __global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
   using X = Ops8<DT, D>;
+  constexpr int kAhead = MT == 1 || D == 64 ? 2 : 1;
   __shared__ int16_t par_s[kMaxSeqRows];
   __shared__ Joins<X, kWaves / 2> join_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -490,45 +492,43 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
   const Walk8 w(a, x.kvh, D);
   const unsigned k_lane = n * D + 16 * g, v_lane = 4 * g * D + n * (D / 16);
   const unsigned char* scales = lane < 32 ? a.k_scale : a.v_scale;
-  typename X::Raw raw;
-  unsigned byte = 0;  // lanes 0 - 31: the scale of a key, lanes 32 - 63: that of a value
-  int id[2] = {-1, -1};
-  // Places the tile from j on; its bits that have a page.
-  auto place = [&](int j) {
-    walk.reach(j, kTile);
-    id[0] = walk.at(j);
-    id[1] = walk.at(j + 16);
-    return (id[0] >= 0 ? 0xffffu : 0u) | (id[1] >= 0 ? 0xffff0000u : 0u);
+  // A tile on its way.
+  struct Tile {
+    typename X::Raw raw;
+    unsigned byte;   // lanes 0 - 31: the scale of a key, lanes 32 - 63: that of a value
+    unsigned pages;  // bits of the positions that have a page
+    int id[2];
   };
-  auto load_keys = [&](int j) {
+  // Places the tile from j on.
+  auto place = [&](Tile& t, int j) __attribute__((always_inline)) {
+    walk.reach(j, kTile);
+    t.id[0] = walk.at(j);
+    t.id[1] = walk.at(j + 16);
+    t.pages = (t.id[0] >= 0 ? 0xffffu : 0u) | (t.id[1] >= 0 ? 0xffff0000u : 0u);
+  };
+  auto load_keys = [&](Tile& to, int j) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const unsigned char* p = a.k + w.at(a, id[t], j + 16 * t, D) + k_lane;
+      const unsigned char* p = a.k + w.at(a, to.id[t], j + 16 * t, D) + k_lane;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) raw.k[t][i] = load16(reinterpret_cast<const u32x4*>(p + 64 * i));
+      for (int i = 0; i < D / 64; ++i) to.raw.k[t][i] = load16(reinterpret_cast<const u32x4*>(p + 64 * i));
     }
     // (A choice between the elements of an array would put it into memory.)
-    const int mine = id[0] ^ ((id[0] ^ id[1]) & static_cast<int>(all_of(lane, 4)));
-    byte = scales[w.scale_at(a, mine, j + (lane & 31))];
+    const int mine = to.id[0] ^ ((to.id[0] ^ to.id[1]) & static_cast<int>(all_of(lane, 4)));
+    to.byte = scales[w.scale_at(a, mine, j + (lane & 31))];
   };
-  unsigned pages = 0;
-  if (w0 < w1) {
-    pages = place(w0);
-    load_keys(w0);
-    load_values<X, true>(raw, a, w, id, w0, v_lane);
-  }
   int odd_from = -1;  // the first tile with NaN that were taken out
-#pragma unroll 1
-  for (int j0 = w0; j0 < w1; j0 += kTile) {
+  // Uses the tile from j0 on and sends for the one kAhead tiles behind it.
+  auto step = [&](Tile& now, int j0) __attribute__((always_inline)) {
     typename Queries<X, MT>::Weights p;
     // Scales to the lanes that use them: those of key n, and of values 4 g + i (a byte each).
-    unsigned four = byte << (8 * (lane & 3));
+    unsigned four = now.byte << (8 * (lane & 3));
     four |= static_cast<unsigned>(dpp_mov<kDppQuadXor1>(static_cast<int>(four)));
     four |= static_cast<unsigned>(dpp_mov<kDppQuadXor2>(static_cast<int>(four)));
     float ks[2], vs[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      ks[t] = __uint_as_float(static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (16 * t + n), static_cast<int>(byte << 23))));
+      ks[t] = __uint_as_float(static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (16 * t + n), static_cast<int>(now.byte << 23))));
       const unsigned b = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(4 * (32 + 16 * t + 4 * g), static_cast<int>(four)));
 #pragma unroll
       for (int i = 0; i < 4; ++i) vs[4 * t + i] = scale_of(b >> (8 * i) & 0xffu);
@@ -536,19 +536,33 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_kernel(Attend8Args a) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       u32x4 k[X::kFrags];
-      X::keys(k, raw, t, ks[t]);
+      X::keys(k, now.raw, t, ks[t]);
       Q.score(p, t, k);
     }
-    const unsigned here = pages;
-    const int next = j0 + kTile;
+    const unsigned here = now.pages;
+    const int next = j0 + kAhead * kTile;
     if (next < w1) {
-      pages = place(next);
-      load_keys(next);
+      place(now, next);
+      load_keys(now, next);
     }
-    if (use_tile<X, MT>(Q, p, raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
-    if (next < w1) load_values<X, true>(raw, a, w, id, next, v_lane);
+    if (use_tile<X, MT>(Q, p, now.raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
+    if (next < w1) load_values<X, true>(now.raw, a, w, now.id, next, v_lane);
+  };
+  Tile tile[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (w0 + i * kTile < w1) {
+      place(tile[i], w0 + i * kTile);
+      load_keys(tile[i], w0 + i * kTile);
+      load_values<X, true>(tile[i].raw, a, w, tile[i].id, w0 + i * kTile, v_lane);
+    }
+#pragma unroll 1
+  for (int j0 = w0; j0 < w1; j0 += kAhead * kTile) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i == 0 || j0 + i * kTile < w1) step(tile[i], j0 + i * kTile);
   }
-  if (odd_from >= 0) poison_from<X, MT>(Q, raw, walk, odd_from, w1, sight, a, w, call, par_s, v_lane);
+  if (odd_from >= 0) poison_from<X, MT>(Q, tile[0].raw, walk, odd_from, w1, sight, a, w, call, par_s, v_lane);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if constexpr (!X::kSums) Q.sum[m][0] = rows_sum(Q.sum[m][0]);
