@@ -12,7 +12,6 @@ import math
 
 import torch
 
-from . import _rounds
 from ._binding import (_check, _device_tensor, _dtype_code, _i32, _out, _rows_view, lib)
 from ._rounds import (_CacheStruct, _I32, _R, _enter, _f, _i, _ints, _l, _leave, _p, _pages_call, _scratch,
                       _sz, _verified, _word, RoundRows)

@@ -1,9 +1,11 @@
 // Attention of a round's rows over the paged cache of 8 bits (whiflash_attend8).
 //
 // Per sequence and key-value head, the rows x (q_heads / heads) queries that share its keys form
-// tiles of 16; a workgroup takes up to five of them over a piece of the positions, its four waves
-// a share of the piece each, with a one-pass softmax in registers (attend_body.h), and joins them
-// in LDS.  Pieces are joined by a second launch.
+// tiles of 16, and a workgroup takes a piece of the positions with a one-pass softmax in registers
+// (attend_body.h).  Up to two tiles: its four waves hold the same queries and take a share of the piece
+// each, straight from memory.  More: its waves share tiles of 64 positions in LDS, up to eight
+// tiles of queries a workgroup.  Waves of the same queries are joined in LDS, pieces by a second
+// launch.
 //
 // An e4m3 number under a power-of-two scale is a bfloat16 number, so keys and values go to the
 // matrix units as bfloat16 without loss, each widened with its own position's scale by one
@@ -14,6 +16,17 @@
 // Keys need no LDS: the order of the dimensions in the first product is free if the queries take
 // the same, and lane (n, g) takes bytes [64 i + 16 g, + 16) of row n, which are 64 bytes of a row
 // for the four lanes of a load.
+//
+// What bounds it (MI355X, 32 query and 8 key-value heads of 128, bfloat16):
+//   64 single tokens over 8-bit contexts of up to 8,192: 141 us, 5.8 TB/s, where reading once takes
+//     111 at the rate of one long read (vector units busy 27%, matrix units 7%; all of 8,192: 6.45
+//     TB/s).  Three waves a SIMD are no faster, and twice the pieces take 166 us;
+//   8 trees of 61 rows over up to 4,096: 69 us, of them 12 the join; 2 chains of 17 over 131,000: 138
+//     us.  There the vector units (33%, 45%) widen and take exponentials, the matrix units are busy
+//     17% and 29%, and the two waves of a SIMD do not hide all of each other's waits.
+//   One wave a row and head, without the matrix units, took 4,378, 4,859 and 68,600 us.
+// Where two positions share a scale their values can be widened together (16 of some 260 vector
+// instructions a tile fewer): 136 for 137 us in the long chains and nothing elsewhere, so left out.
 #include "attend_body.h"
 #include "decode.h"
 #include "dpp.h"
@@ -781,12 +794,18 @@ struct Shape {
   int mt, gs;
 };
 
+// A wave's registers hold two tiles of bfloat16 queries (three with the queries in LDS), one of float32.
+// Two query groups a workgroup are faster than four as long as their rereading of the keys and values
+// stays in the L2 (bfloat16: 8 trees of 61 rows, 16 tiles, 69 and 71 us; float32: the same 88 and 97, two
+// chains of 17 rows over 100,000 301 and 329); four where there are many (8 chains of 1,024 rows, 256
+// tiles, 346 and 301; float32, 8 of 301 rows, 76 tiles, 188 and 177).  Five or six tiles fit one
+// workgroup of three a wave (two chains of 17 rows over 131,000 137 us; two workgroups of four 195,
+// one of eight 176).
 Shape shape_of(int tiles, int dtype) {
-  if (dtype == WF_F32) return tiles <= 1 ? Shape{1, 1} : tiles <= 2 ? Shape{1, 2} : Shape{1, 4};
+  if (dtype == WF_F32) return tiles <= 1 ? Shape{1, 1} : tiles <= 16 ? Shape{1, 2} : Shape{1, 4};
   if (tiles <= 2) return Shape{tiles <= 1 ? 1 : 2, 1};
-  if (tiles <= 4) return Shape{2, 2};
-  if (tiles <= 6) return Shape{3, 2};
-  return Shape{2, 4};
+  if (tiles == 5 || tiles == 6) return Shape{3, 2};
+  return tiles <= 16 ? Shape{2, 2} : Shape{2, 4};
 }
 
 template <int DT, int D>

@@ -9,6 +9,12 @@
 // Everywhere a team of D / 8 lanes owns a block of one head of the keys or of the values, eight
 // dimensions a lane: a row is eight bytes a lane, its maximum a reduction over the team, and no
 // two teams touch one byte.
+//
+// Memory bounds the large calls (MI355X, 8 heads of 128, bfloat16 rows): 32 x 1,024 rows appended under
+// a scale each 55 us, 201 MB, 3.7 TB/s of the 4.9 of a large copy (74 us when a team took a row at a
+// time, and its index a 64-bit division); 2 x 131,000 positions read back 306 us, 1.6 GB, 5.2
+// TB/s.  Small ones are chains of reads (context, page, rows): 64 x 17 rows into blocks of 16 11 us, read
+// back 6 (16 when a workgroup took 16 positions whatever their number).
 #include <limits.h>
 
 #include <type_traits>
@@ -299,7 +305,8 @@ __global__ __launch_bounds__(kThreads) void cache8_read_kernel(
   }
 }
 
-// Positions a workgroup: fewer of a short read, so that every CU has some.
+// Positions a workgroup: fewer of a short read, so that every CU has some (64 x 32 positions 6 us, 16
+// with 16 a workgroup; 2 x 131,000 306 us).
 int read_rows(int32_t B, int32_t count) {
   int per = kReadRows;
   while (per > 1 && static_cast<int64_t>(B) * ((count + per - 1) / per) < 1024) per /= 2;
