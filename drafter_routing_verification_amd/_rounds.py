@@ -477,7 +477,7 @@ def cache_append(cache: PageCache, rows: RoundRows, k_rows, v_rows, *, layer: in
                  stream=None) -> None:
     """Puts the rows' keys and values [rows, heads, head_dim] at positions context + i of their
     sequences in one layer.  seqs [B] int32: the cache sequences (None: 0 .. B-1)."""
-    if type(cache) is not PageCache:
+    if not isinstance(cache, PageCache):
         return cache._append(rows, k_rows, v_rows, layer, seqs, stream)
     seq = _cache_call(cache, rows, seqs)
     ks = _vectors(k_rows, "k_rows", rows.total, cache.heads, cache)
@@ -504,7 +504,7 @@ def attend(q, rows: RoundRows, cache: PageCache, *, layer: int = 0, seqs=None, s
     """Attention of the rows' queries q [rows, q_heads, head_dim] over the cache.  scale: None for
     head_dim ** -0.5; max_context: an upper bound of the sequences' committed lengths that the host
     knows (None: what a table row can hold).  Returns out [rows, q_heads, head_dim]."""
-    if type(cache) is not PageCache:
+    if not isinstance(cache, PageCache):
         return cache._attend(q, rows, layer, seqs, scale, max_context, out, workspace, stream)
     seq = _cache_call(cache, rows, seqs)
     qs = _vectors(q, "q", rows.total, None, cache)
@@ -533,7 +533,7 @@ def cache_compact(cache: PageCache, rows: RoundRows, accept_len, best_node=None,
     """Moves each accepted tree path's rows to the front of the round's positions, in every layer,
     and commits accept_len positions: next_context (None: the cache's context, in place) gets
     context + accept_len.  best_node may be None for rounds of chains."""
-    if type(cache) is not PageCache:
+    if not isinstance(cache, PageCache):
         return cache._compact(rows, accept_len, best_node, seqs, next_context, stream)
     seq = _cache_call(cache, rows, seqs)
     al, best = _verified(rows, accept_len, best_node)
@@ -567,7 +567,7 @@ def _pages_call(fn, cache, ref, first, second, names, status, workspace, stream)
 def cache_fork(cache: PageCache, src, dst, *, status=None, workspace=None, stream=None):
     """Makes sequence dst[i] a fork of src[i]: full pages shared, the last partly filled one copied.
     Returns status [n] int32, 1 where done, 0 where refused."""
-    if type(cache) is not PageCache:
+    if not isinstance(cache, PageCache):
         return cache._fork(src, dst, status, workspace, stream)
     return _pages_call(functions().cache_fork, cache, cache.ref, src, dst, ("src", "dst"), status, workspace, stream)
 

@@ -188,6 +188,24 @@ def test_a_given_stream_is_used():
     assert (got[2] == 7).all()
 
 
+def test_a_page_cache_of_another_class_is_still_one():
+    class Mine(wf.PageCache):
+        pass
+
+    r = Round("tree", 2, 0, 5, 50, seed=1)
+    (q,), _ = vectors(r.total, GROUP * HEADS, DIM, "bf16", 1)
+    (k, v), _ = vectors(r.total, HEADS, DIM, "bf16", 2, parts=2)
+    outs = []
+    for kind in (wf.PageCache, Mine):
+        cache = kind.empty(1, 8, HEADS, PAGE, DIM, 3, 4, dtype=torch.bfloat16, device=DEV)
+        wf.cache_reserve(cache, i32([5, 5]), seqs=i32([0, 1]))
+        wf.cache_append(cache, r.rows, k, v)
+        out = wf.attend(q, r.rows, cache)
+        wf.cache_compact(cache, r.rows, i32([2, 1]), i32([1, 0]))
+        outs.append([out, wf.cache_fork(cache, i32([0]), i32([2])), cache.context, cache.k])
+    _same(*outs, "subclass")
+
+
 def test_refusals():
     r = Round("chain", 2, 3, 0, 50, seed=1)
     _, cache = make_cache8(2, HEADS, PAGE, DIM, 16, [5, 6], 4, 1)
