@@ -8,8 +8,9 @@
 //
 // Memory bounds the large calls (MI355X, 32 + 8 heads of 128): 32 x 1,024 bfloat16 rows 135 us, 671 MB,
 // the rate of a large copy (4.9 TB/s; the angles are 29% of the vector units' time).  64 trees of 61
-// float32 rows take 42 us where the copy takes 33: a workgroup each, its depths, then its angles,
-// then its rows.  One token 3.4 us.
+// float32 rows take 38 us where the copy takes 33: a workgroup each, its depths, then its angles,
+// while the first vectors are on their way (44 us without; four instead of two 42, and 139 for the
+// large call: too many registers), then its rows.  One token 3.4 us.
 #include <math.h>
 
 #include "decode.h"
@@ -19,6 +20,7 @@ namespace wf {
 namespace {
 
 constexpr int kRotaryRows = 8;      // most rows of a workgroup
+constexpr int kFirst = 2;           // vectors (pairs of them) of a thread that come before the angles
 constexpr int kMaxPairs = WHIFLASH_MAX_ROTARY_DIM / 2;
 
 struct RotaryArgs {
@@ -85,7 +87,6 @@ __device__ inline u32x4 pack_vector(const float* x) {
 template <int DT, bool INTERLEAVED, bool VEC>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a) {
   using E = Elem<DT>;
-  constexpr int kPer = VEC ? E::kPerVec : 1;
   __shared__ float2 turn_s[kRotaryRows * kMaxPairs];
   __shared__ int16_t up_s[kMaxSeqRows], deep_s[kMaxSeqRows];
   const int tid = threadIdx.x;
@@ -97,6 +98,55 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a) {
   const int c = a.context[s];
   if (c < 0) return;
   const int rows = min(a.per_wg, q.n - i0);
+  // Threads in groups of `width`, each group a head of a row at a time.
+  const int each = a.items + a.copies;
+  const int width = min(each, kThreads), step = kThreads / width;
+  const int mine = tid / width, j0 = tid - mine * width;
+  const bool idle = mine >= step;
+  // Where a head of a row is, and goes.
+  struct Place {
+    const unsigned char* x;
+    unsigned char* y;
+    const float2* turn;
+    bool stays;  // copied elements are where they belong
+  };
+  auto place = [&](int r, int h) __attribute__((always_inline)) {
+    const bool key = h >= a.q_heads;
+    const int64_t row = static_cast<int64_t>(q.row0) + i0 + r;
+    const int64_t in_head = static_cast<int64_t>(key ? h - a.q_heads : h) * a.head_bytes;
+    return Place{(key ? a.k + row * a.k_bytes : a.q + row * a.q_bytes) + in_head,
+                 (key ? a.k_out + row * a.k_out_bytes : a.q_out + row * a.q_out_bytes) + in_head,
+                 turn_s + r * a.pairs, key ? a.k_in_place : a.q_in_place};
+  };
+  auto advance = [&](int& r, int& h) __attribute__((always_inline)) {
+    h += step;
+    while (h >= a.heads && r < rows) {
+      h -= a.heads;
+      ++r;
+    }
+  };
+  const int far = a.pairs * E::kBytes;  // from one half of the turned part to the other
+  // A thread's vectors of unit j: those it turns, or copies.
+  auto fetch = [&](const Place& p, int j, u32x4& d, u32x4& f) __attribute__((always_inline)) {
+    if (j >= a.items) {
+      if (!p.stays) d = *reinterpret_cast<const u32x4*>(p.x + 2 * far + (j - a.items) * 16);
+      return;
+    }
+    d = *reinterpret_cast<const u32x4*>(p.x + j * 16);
+    if constexpr (!INTERLEAVED) f = *reinterpret_cast<const u32x4*>(p.x + far + j * 16);
+  };
+  int r0 = 0, h0 = mine - step;
+  advance(r0, h0);
+  // The first vectors come while the angles are computed.
+  u32x4 d_first[kFirst], f_first[kFirst];
+  if constexpr (VEC) {
+    int r = r0, h = h0;
+#pragma unroll
+    for (int n = 0; n < kFirst; ++n) {
+      if (!idle && r < rows) fetch(place(r, h), j0, d_first[n], f_first[n]);
+      advance(r, h);
+    }
+  }
   if (q.tree) {
     // Depths by doubling: up is the node as many edges above as deep counts, until no path goes on.
     for (int u = tid; u < q.n; u += kThreads) {
@@ -138,72 +188,67 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotaryArgs a) {
     turn_s[t] = cos_sin(static_cast<double>(static_cast<int64_t>(c) + depth) * a.frequency[i], a.magnitude);
   }
   __syncthreads();
-  // Threads in groups of `width`, each group a head of a row at a time.
-  const int each = a.items + a.copies;
-  const int width = min(each, kThreads), step = kThreads / width;
-  const int mine = tid / width;
-  if (mine >= step) return;
-  int r = 0, h = mine;
-  while (h >= a.heads && r < rows) {
-    h -= a.heads;
-    ++r;
-  }
-  while (r < rows) {
-    const bool key = h >= a.q_heads;
-    const int64_t row = static_cast<int64_t>(q.row0) + i0 + r;
-    const int64_t in_head = static_cast<int64_t>(key ? h - a.q_heads : h) * a.head_bytes;
-    const unsigned char* x = (key ? a.k + row * a.k_bytes : a.q + row * a.q_bytes) + in_head;
-    unsigned char* y = (key ? a.k_out + row * a.k_out_bytes : a.q_out + row * a.q_out_bytes) + in_head;
-    const float2* turn = turn_s + r * a.pairs;
-    for (int j = tid - mine * width; j < each; j += width) {
-      if (j >= a.items) {  // past the turned part
-        if (key ? a.k_in_place : a.q_in_place) break;
-        const int at = 2 * a.pairs * E::kBytes + (j - a.items) * kPer * E::kBytes;
-        if constexpr (VEC) {
-          *reinterpret_cast<u32x4*>(y + at) = *reinterpret_cast<const u32x4*>(x + at);
-        } else {
-          store_element<DT>(y + at, E::scalar(x + at, 0));
-        }
-        continue;
-      }
-      if constexpr (!VEC) {
-        const int one = (INTERLEAVED ? 2 * j : j) * E::kBytes;
-        const int two = one + (INTERLEAVED ? 1 : a.pairs) * E::kBytes;
-        const float u = E::scalar(x + one, 0), v = E::scalar(x + two, 0);
-        const float2 w = turn[j];
-        store_element<DT>(y + one, u * w.x - v * w.y);
-        store_element<DT>(y + two, v * w.x + u * w.y);
-      } else if constexpr (INTERLEAVED) {
-        const u32x4 d = *reinterpret_cast<const u32x4*>(x + j * 16);
-        float o[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const float2 w = turn[j * (kPer / 2) + e / 2];
-          const float u = E::at(d, e), v = E::at(d, e + 1);
-          o[e] = u * w.x - v * w.y;
-          o[e + 1] = v * w.x + u * w.y;
-        }
-        *reinterpret_cast<u32x4*>(y + j * 16) = pack_vector<DT>(o);
-      } else {
-        const int far = a.pairs * E::kBytes;
-        const u32x4 d = *reinterpret_cast<const u32x4*>(x + j * 16);
-        const u32x4 f = *reinterpret_cast<const u32x4*>(x + far + j * 16);
-        float o[kPer], p[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const float2 w = turn[j * kPer + e];
-          const float u = E::at(d, e), v = E::at(f, e);
-          o[e] = u * w.x - v * w.y;
-          p[e] = v * w.x + u * w.y;
-        }
-        *reinterpret_cast<u32x4*>(y + j * 16) = pack_vector<DT>(o);
-        *reinterpret_cast<u32x4*>(y + far + j * 16) = pack_vector<DT>(p);
-      }
+  if (idle) return;
+  auto turn = [&](const Place& p, int j, u32x4 d, u32x4 f) __attribute__((always_inline)) {
+    if (j >= a.items) {  // past the turned part
+      if (!p.stays) *reinterpret_cast<u32x4*>(p.y + 2 * far + (j - a.items) * 16) = d;
+      return;
     }
-    h += step;
-    while (h >= a.heads && r < rows) {
-      h -= a.heads;
-      ++r;
+    float o[E::kPerVec];
+    if constexpr (INTERLEAVED) {
+#pragma unroll
+      for (int e = 0; e < E::kPerVec; e += 2) {
+        const float2 w = p.turn[j * (E::kPerVec / 2) + e / 2];
+        const float u = E::at(d, e), v = E::at(d, e + 1);
+        o[e] = u * w.x - v * w.y;
+        o[e + 1] = v * w.x + u * w.y;
+      }
+    } else {
+      float t[E::kPerVec];
+#pragma unroll
+      for (int e = 0; e < E::kPerVec; ++e) {
+        const float2 w = p.turn[j * E::kPerVec + e];
+        const float u = E::at(d, e), v = E::at(f, e);
+        o[e] = u * w.x - v * w.y;
+        t[e] = v * w.x + u * w.y;
+      }
+      *reinterpret_cast<u32x4*>(p.y + far + j * 16) = pack_vector<DT>(t);
+    }
+    *reinterpret_cast<u32x4*>(p.y + j * 16) = pack_vector<DT>(o);
+  };
+  int r = r0, h = h0;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int n = 0; n < kFirst; ++n) {
+      if (r >= rows) return;
+      const Place p = place(r, h);
+      turn(p, j0, d_first[n], f_first[n]);
+      for (int j = j0 + width; j < each; j += width) {
+        u32x4 d, f;
+        fetch(p, j, d, f);
+        turn(p, j, d, f);
+      }
+      advance(r, h);
+    }
+  }
+  for (; r < rows; advance(r, h)) {
+    const Place p = place(r, h);
+    for (int j = j0; j < each; j += width) {
+      if constexpr (VEC) {
+        u32x4 d, f;
+        fetch(p, j, d, f);
+        turn(p, j, d, f);
+      } else if (j >= a.items) {
+        const int at = 2 * far + (j - a.items) * E::kBytes;
+        if (!p.stays) store_element<DT>(p.y + at, E::scalar(p.x + at, 0));
+      } else {
+        const int one = (INTERLEAVED ? 2 * j : j) * E::kBytes;
+        const int two = one + (INTERLEAVED ? E::kBytes : far);
+        const float u = E::scalar(p.x + one, 0), v = E::scalar(p.x + two, 0);
+        const float2 w = p.turn[j];
+        store_element<DT>(p.y + one, u * w.x - v * w.y);
+        store_element<DT>(p.y + two, v * w.x + u * w.y);
+      }
     }
   }
 }
