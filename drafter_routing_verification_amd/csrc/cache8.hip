@@ -11,7 +11,7 @@
 // two teams touch one byte.
 //
 // Memory bounds the large calls (MI355X, 8 heads of 128, bfloat16 rows): 32 x 1,024 rows appended under
-// a scale each 55 us, 201 MB, 3.7 TB/s of the 4.9 of a large copy (74 us when a team took a row at a
+// a scale each 53 us, 201 MB, 3.8 TB/s of the 4.9 of a large copy (74 us when a team took a row at a
 // time, and its index a 64-bit division); 2 x 131,000 positions read back 306 us, 1.6 GB, 5.2
 // TB/s.  Small ones are chains of reads (context, page, rows): 64 x 17 rows into blocks of 16 11 us, read
 // back 6 (16 when a workgroup took 16 positions whatever their number).
@@ -155,22 +155,17 @@ __global__ __launch_bounds__(kThreads, ROWS > kSpan ? 2 : 4) void cache8_append_
   const int which = rest >= a.heads ? 1 : 0, h = rest - which * a.heads;
   const int64_t lo = ((c >> span_log) + nth) << span_log;
   if (lo >= end) return;
-  const int p = page_of(a, s, lo);
-  if (p < 0) return;
   const int block = 1 << a.block_log;
   // Positions lo + [kept, fresh) lie in blocks that get rows and have values, lo + [fresh, all) get rows.
   const int all = static_cast<int>(min(end - lo, int64_t{1} << span_log));
   const int fresh = static_cast<int>(min(max(c - lo, int64_t{0}), static_cast<int64_t>(all)));
   const int kept = fresh & ~(block - 1);
-  unsigned char* data = a.data[which] + layer * a.layer_bytes + byte_of<D>(a, p, h, lo) + lane * 8;
-  unsigned char* scale = a.scale[which] + layer * a.scale_layer + scale_at(a, p, h, lo);
   const int64_t stride = which ? v_bytes : k_bytes;
   // Row i of the round is position c + i.
   const unsigned char* from = (which ? v_rows : k_rows) + (q.row0 + lo - c) * stride +
                               (static_cast<int64_t>(h) * D + lane * 8) * Elem<DT>::kBytes;
-  const int old = fresh > kept ? scale[kept >> a.block_log] : 0;
   u32x4 w[ROWS], w2[ROWS];  // (a bfloat16 row's eight dimensions are the first alone)
-  auto load = [&](int j0) __attribute__((always_inline)) {
+  auto load_rows = [&](int j0) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       const int at = j0 + j;
@@ -178,7 +173,21 @@ __global__ __launch_bounds__(kThreads, ROWS > kSpan ? 2 : 4) void cache8_append_
         const unsigned char* x = from + at * stride;
         w[j] = *reinterpret_cast<const u32x4*>(x);
         if constexpr (DT != WF_BF16) w2[j] = *reinterpret_cast<const u32x4*>(x + 16);
-      } else if (at >= kept && at < fresh) {
+      }
+    }
+  };
+  load_rows(0);  // (on their way while the page is looked up)
+  const int p = page_of(a, s, lo);
+  if (p < 0) return;
+  unsigned char* data = a.data[which] + layer * a.layer_bytes + byte_of<D>(a, p, h, lo) + lane * 8;
+  unsigned char* scale = a.scale[which] + layer * a.scale_layer + scale_at(a, p, h, lo);
+  const int old = fresh > kept ? scale[kept >> a.block_log] : 0;
+  auto load_kept = [&](int j0) __attribute__((always_inline)) {
+    if (j0 >= fresh) return;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int at = j0 + j;
+      if (at >= kept && at < fresh) {
         const uint2 x = *reinterpret_cast<const uint2*>(data + at * D);
         w[j] = u32x4{x.x, x.y, 0u, 0u};
         if constexpr (DT != WF_BF16) w2[j] = u32x4{0u, 0u, 0u, 0u};
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(kThreads, ROWS > kSpan ? 2 : 4) void cache8_append_
       *reinterpret_cast<uint2*>(data + at * D) = quantise(x, inverse_scale(now[j]));
     }
   };
-  load(0);
+  load_kept(0);
   find(0);
   if constexpr (!LONG) {
     // The largest of each block, in all of its places.
@@ -244,14 +253,16 @@ __global__ __launch_bounds__(kThreads, ROWS > kSpan ? 2 : 4) void cache8_append_
       for (int j = 0; j < ROWS; ++j) most = fmaxf(most, top[j]);
       j0 += ROWS;
       if (j0 >= all) break;
-      load(j0);
+      load_rows(j0);
+      load_kept(j0);
       find(j0);
     }
     const int one = scale_for(team_max<kTeam>(most));
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) now[j] = one;
     for (int j0 = 0; j0 < all; j0 += ROWS) {
-      load(j0);
+      load_rows(j0);
+      load_kept(j0);
       put(j0);
     }
     if (lane == 0) *scale = static_cast<unsigned char>(one);
