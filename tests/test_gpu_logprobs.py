@@ -160,6 +160,21 @@ def test_odd_rows_in_one_piece(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_rows_in_one_piece(dtype):
+    # Rows of 4 million, one workgroup each: groups of many vectors.
+    V = (1 << 22) + 5
+    raw, x = _logits(2, V, dtype, 11)
+    logits = stored(raw, dtype, (1 << 22) + 8)
+    rows = np.arange(2100) % 2
+    for top in (1, 20, 64):
+        got = wf.token_logprobs(logits, i32(np.arange(2100) + V - 2100), rows=i32(rows), top=top)
+        tokens = (np.arange(2100) + V - 2100)[:, None]
+        _check(x, tokens[:2], [0, 1], top, [t[:2] for t in got])
+        for t in got[1:]:
+            assert torch.equal(t[2:], t[:2].repeat(1049, *[1] * (t.dim() - 1)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [20011, 151936])
 @pytest.mark.parametrize("copies", [1, 260])
 def test_the_entropy_of_a_dominant_token_keeps_its_digits(dtype, V, copies):
