@@ -27,6 +27,8 @@
 //   One wave a row and head, without the matrix units, took 4,378, 4,859 and 68,600 us.
 // Where two positions share a scale their values can be widened together (16 of some 260 vector
 // instructions a tile fewer): 136 for 137 us in the long chains and nothing elsewhere, so left out.
+#include <type_traits>
+
 #include "attend_body.h"
 #include "decode.h"
 #include "dpp.h"
@@ -255,12 +257,12 @@ struct Ops8 {
 // lanes and no rescaling.
 constexpr float kSlack8 = 16.f;
 
-template <class X, int MT>
+template <class X, int N, int MT>
 __device__ inline void soften8(Queries<X, MT>& Q, typename Queries<X, MT>::Weights& p, float scale) {
   bool grown = false;
-  float top[MT];
+  float top[N];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int m = 0; m < N; ++m) {
     float x = p[m][0][0];
 #pragma unroll
     for (int t = 0; t < X::kSub; ++t)
@@ -271,7 +273,7 @@ __device__ inline void soften8(Queries<X, MT>& Q, typename Queries<X, MT>::Weigh
   }
   if (__any(grown)) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < N; ++m) {
       const float now = fmaxf(Q.mx[m], rows_max(top[m]));
       const float f = __builtin_amdgcn_exp2f(Q.mx[m] - now);
       Q.mx[m] = now;
@@ -281,7 +283,7 @@ __device__ inline void soften8(Queries<X, MT>& Q, typename Queries<X, MT>::Weigh
     }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < N; ++m)
 #pragma unroll
     for (int t = 0; t < X::kSub; ++t)
 #pragma unroll
@@ -350,9 +352,9 @@ struct Walk8 {
   }
 };
 
-// The weights and outputs of 32 positions from their products with the queries.  here: those with a
-// page.  Returns whether NaN among the values were taken out.
-template <class X, int MT>
+// The weights and outputs of 32 positions from their products with the first N tiles of queries.  here:
+// those with a page.  Returns whether NaN among the values were taken out.
+template <class X, int N, int MT>
 __device__ inline bool use_tile(Queries<X, MT>& Q, typename Queries<X, MT>::Weights& p,
                                 typename X::Raw& raw, float* scale, int j0, unsigned here,
                                 const Sight& sight, const Attend8Args& a, const SeqCall& call,
@@ -364,7 +366,7 @@ __device__ inline bool use_tile(Queries<X, MT>& Q, typename Queries<X, MT>::Weig
     const unsigned any = Q.visible(j0, sight.end, here);
     X::hide(raw, scale, any >> (4 * g));
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < N; ++m) {
       const unsigned see = seen_of(Q, m, j0, any, a, call, par) >> (4 * g);
       __builtin_amdgcn_sched_barrier(0);
       // (By masks of bits: comparisons would take two scalar registers for each product.)
@@ -379,11 +381,11 @@ __device__ inline bool use_tile(Queries<X, MT>& Q, typename Queries<X, MT>::Weig
     odd = __any(X::odd(raw));
     if (odd) X::clean(raw);
   }
-  soften8<X, MT>(Q, p, a.scale_log2);
+  soften8<X, N>(Q, p, a.scale_log2);
   // The wave that feeds the matrix units goes first, so that the SIMD's other one is left with the
   // vector work: 8 trees of 61 76 -> 70 us, long chains 144 -> 140.
   __builtin_amdgcn_s_setprio(1);
-  X::template outputs<MT>(Q.o, Q.sum, raw, scale, p);
+  X::template outputs<N>(Q.o, Q.sum, raw, scale, p);
   __builtin_amdgcn_s_setprio(0);
   return odd;
 }
@@ -636,7 +638,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
   const int k0 = x.split * a.span;
   if (x.split > 0 && k0 >= all.end) return;
   const int k1 = min(k0 + a.span, all.end);
-  const int first = all_first + wave % GS * MT * 16;
+  // The wave's query group: not the same SIMDs get the first in both workgroups of a CU, since the
+  // last may hold fewer queries (long chains 133 -> 132 us).
+  const int mine = (wave + (blockIdx.x >> 8 & 1)) % GS;
+  const int first = all_first + mine * MT * 16;
+  // (A group whose last tile is empty leaves it out: long chains of five tiles 138 -> 133 us.)
+  const bool all_tiles = MT == 1 || first + (MT - 1) * 16 < rows * a.group;
   const bool work = first < rows * a.group;
   const Sight sight = sight_of(a, call, work ? first : all_first, MT * 16);
   PageWalk walk(a, call, k0, k1);
@@ -650,7 +657,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int f = 0; f < X::kQ; ++f) q_s[wave][m * X::kQ + f][lane] = Q.q[m][f];
+        for (int f = 0; f < X::kQ; ++f) q_s[mine][m * X::kQ + f][lane] = Q.q[m][f];
   }
   __syncthreads();
 
@@ -673,20 +680,21 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
     unsigned pages = 0;
 #pragma unroll
     for (int t = 0; t < kWide / 16; ++t) pages |= walk.at(j + 16 * t) >= 0 ? 1u << t : 0u;
-    const int mine = j + 16 * wave, id = walk.at(mine);
-    const int64_t at = w.at(a, id, mine, D);
+    const int own = j + 16 * wave, id = walk.at(own);
+    const int64_t at = w.at(a, id, own, D);
     Stage<D>& st = ring_s[to];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       to_lds16(st.k + wave * 16 * kRow + i * 64, a.k + at, k_from[i]);
       to_lds16(st.v + wave * 16 * kRow + i * 64, a.v + at, v_from[i]);
     }
-    to_lds1(st.scale[wave], scales + w.scale_at(a, id, mine + n));
+    to_lds1(st.scale[wave], scales + w.scale_at(a, id, own + n));
     return pages;
   };
   constexpr int kInFlight = 2 * kLoads + 1;
   int odd_from = -1;
-  auto take = [&](const Stage<D>& st, int j, unsigned pages) __attribute__((always_inline)) {
+  auto take = [&](auto tiles, const Stage<D>& st, int j, unsigned pages) __attribute__((always_inline)) {
+    constexpr int N = decltype(tiles)::value;
 #pragma unroll 1
     for (int step = 0; step < kSteps; ++step) {
       const int sub = (wave / GS * kSteps + step) * 2, j0 = j + 16 * sub;
@@ -707,13 +715,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
       u32x4 q[2][kInLds ? X::kQ : 1];
       if constexpr (kInLds)
 #pragma unroll
-        for (int f = 0; f < X::kQ; ++f) q[0][f] = q_s[wave % GS][f][lane];
+        for (int f = 0; f < X::kQ; ++f) q[0][f] = q_s[mine][f][lane];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < N; ++m) {
         if constexpr (kInLds)
-          if (m + 1 < MT)
+          if (m + 1 < N)
 #pragma unroll
-            for (int f = 0; f < X::kQ; ++f) q[(m + 1) % 2][f] = q_s[wave % GS][(m + 1) * X::kQ + f][lane];
+            for (int f = 0; f < X::kQ; ++f) q[(m + 1) % 2][f] = q_s[mine][(m + 1) * X::kQ + f][lane];
         f32x4 sum[2] = {};
 #pragma unroll
         for (int f = X::kQ - 1; f >= 0; --f) {
@@ -752,12 +760,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
         }
       }
       const unsigned here = (pages >> sub & 1u ? 0xffffu : 0u) | (pages >> sub & 2u ? 0xffff0000u : 0u);
-      if (use_tile<X, MT>(Q, p, raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
+      if (use_tile<X, N>(Q, p, raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
     }
   };
   // The tile at hand has arrived when no more than the next one's loads are in flight, for every
   // wave; and every wave is done with the one before it, whose place the tile after the next takes.
-  if (k0 < k1) {
+  auto walk_all = [&](auto tiles) __attribute__((always_inline)) {
     unsigned here = issue(0, k0), next = issue(1, k0 + kWide);
     int now = 0;
 #pragma unroll 1
@@ -767,10 +775,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       const unsigned after = issue(now == 0 ? kRing - 1 : now - 1, j + 2 * kWide);
-      take(ring_s[now], j, here);
+      take(tiles, ring_s[now], j, here);
       here = next;
       next = after;
       now = now == kRing - 1 ? 0 : now + 1;
+    }
+  };
+  if (k0 < k1) {
+    if (all_tiles) {
+      walk_all(std::integral_constant<int, MT>{});
+    } else {
+      walk_all(std::integral_constant<int, (MT > 1 ? MT - 1 : 1)>{});
     }
   }
   __builtin_amdgcn_s_waitcnt(0x0070);
