@@ -21,8 +21,8 @@
 //   64 single tokens over 8-bit contexts of up to 8,192: 141 us, 5.8 TB/s, where reading once takes
 //     111 at the rate of one long read (vector units busy 27%, matrix units 7%; all of 8,192: 6.45
 //     TB/s).  Three waves a SIMD are no faster, and twice the pieces take 166 us;
-//   8 trees of 61 rows over up to 4,096: 69 us, of them 12 the join; 2 chains of 17 over 131,000: 138
-//     us.  There the vector units (33%, 45%) widen and take exponentials, the matrix units are busy
+//   8 trees of 61 rows over up to 4,096: 66 us, of them 12 the join; 2 chains of 17 over 131,000:
+//     132 to 137 us.  There the vector units (33%, 45%) widen and take exponentials, the matrix units are busy
 //     17% and 29%, and the two waves of a SIMD do not hide all of each other's waits.
 //   One wave a row and head, without the matrix units, took 4,378, 4,859 and 68,600 us.
 // Where two positions share a scale their values can be widened together (16 of some 260 vector
@@ -710,6 +710,27 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
         for (int i = 0; i < D / 64; ++i) raw.k[t][i] = st.k[(row + n) * kRow + ((4 * i + g) ^ k_turn)];
         X::keys(k[t], raw, t, scale_of(st.scale[sub + t][n]));
       }
+      auto fetch_values = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const u32x4 b = *reinterpret_cast<const u32x4*>(&st.scale[sub + t][16 + 4 * g]);
+          const unsigned char* v = reinterpret_cast<const unsigned char*>(st.v + 16 * (sub + t) * kRow) + g * D + n * (D / 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            vs[4 * t + i] = scale_of(b[i]);
+            if constexpr (D == 128) {
+              const uint2 y = *reinterpret_cast<const uint2*>(v + 4 * i * D);
+              raw.v[4 * t + i][0] = y.x;
+              raw.v[4 * t + i][1] = y.y;
+            } else {
+              raw.v[4 * t + i][0] = *reinterpret_cast<const unsigned*>(v + 4 * i * D);
+            }
+          }
+        }
+      };
+      // (Values while the scores multiply: trees 67.8 -> 66.3 us; not where the queries come from LDS too,
+      // long chains 136 -> 138.)
+      if constexpr (!kInLds) fetch_values();
       __builtin_amdgcn_s_setprio(1);
       // (A tile's queries are fetched while the one before multiplies.)
       u32x4 q[2][kInLds ? X::kQ : 1];
@@ -743,22 +764,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend8_wide_kernel(Attend8Args a
         if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_s_setprio(0);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const u32x4 b = *reinterpret_cast<const u32x4*>(&st.scale[sub + t][16 + 4 * g]);
-        const unsigned char* v = reinterpret_cast<const unsigned char*>(st.v + 16 * (sub + t) * kRow) + g * D + n * (D / 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vs[4 * t + i] = scale_of(b[i]);
-          if constexpr (D == 128) {
-            const uint2 y = *reinterpret_cast<const uint2*>(v + 4 * i * D);
-            raw.v[4 * t + i][0] = y.x;
-            raw.v[4 * t + i][1] = y.y;
-          } else {
-            raw.v[4 * t + i][0] = *reinterpret_cast<const unsigned*>(v + 4 * i * D);
-          }
-        }
-      }
+      if constexpr (kInLds) fetch_values();
       const unsigned here = (pages >> sub & 1u ? 0xffffu : 0u) | (pages >> sub & 2u ? 0xffff0000u : 0u);
       if (use_tile<X, N>(Q, p, raw, vs, j0, here, sight, a, call, par_s) && odd_from < 0) odd_from = j0;
     }
